@@ -393,6 +393,129 @@ int splitzip_decode_batch(const splitzip_decode_item_t* h_items, uint32_t count,
 int splitzip_merge(const void* const* h_parts, const uint64_t* part_bytes, uint32_t count, void* h_out,
                    uint64_t out_capacity, uint64_t* out_bytes);
 
+/* ---------------------------------------------------------------------------
+ * Paged KV cache operators: writing the keys and values of new tokens into
+ * the pages of a cache (quantising them where the cache is FP8), reading them
+ * back, and attention of the new tokens over the pages.  The page has no
+ * counterpart; they are what a serving engine runs on either side of the
+ * transfer that the codec speeds up, on the same pools and page lists that
+ * splitzip_encode_paged and splitzip_decode_paged take (an E5M2 cache is
+ * written by splitzip_kv_write and compressed by splitzip_encode_paged).
+ *
+ * All three take one description of a step.  Sequence b of the batch holds
+ * kv_len[b] tokens, position p of it in token slot p mod page_tokens of pool
+ * page page_table[b * table_stride + p / page_tokens].  Its new tokens are
+ * rows cu_tokens[b] .. cu_tokens[b+1] - 1 of the packed row tensors, and are
+ * its LAST positions: with t = cu_tokens[b+1] - cu_tokens[b] of them, row
+ * cu_tokens[b] + i is position kv_len[b] - t + i.  A row of negative position
+ * (t > kv_len[b]) has no place: it is not written, reads back as zeros and
+ * sees nothing.  Rows at and past cu_tokens[batch] belong to no sequence and
+ * are left alone, so a captured graph can be sized for more rows than it gets.
+ *
+ * The integer arrays are read on the GPU, in stream order.  A sequence whose
+ * entries are out of range (cu_tokens not ascending within 0 .. tokens, more
+ * than max_tokens new tokens, kv_len outside 0 .. max_kv_len) is left out, a
+ * page outside [0, pool_pages) is neither read nor written, and both are
+ * reported in *d_status as SPLITZIP_ERR_INVALID_ARG (the outputs of that
+ * sequence are then unspecified).  *d_status is cleared by each call.
+ */
+typedef enum {
+    SPLITZIP_KV_BF16 = 0,
+    SPLITZIP_KV_FP8_E5M2 = 1,
+    SPLITZIP_KV_FP16 = 2,     /* these three as splitzip_dtype_t */
+    SPLITZIP_KV_FP8_E4M3 = 3  /* 1 sign, 4 exponent, 3 mantissa bits, no infinity, largest 448 */
+} splitzip_kv_type_t;
+
+/* One layer's cache: pools of K and of V with the same geometry.  Element
+ * (page, token, head, i) is at page * page_stride + token * token_stride +
+ * head * head_stride + i; strides are in elements, multiples of 16 bytes, so
+ * [page][token][head][dim], [page][head][token][dim] and pools that hold K
+ * and V side by side are all expressed.  FP8 caches have one scale for each
+ * (page, head, token): byte s stands for 2^(s - 127), s in 1 .. 254, at
+ * (page * kv_heads + head) * page_tokens + token of d_k_scale / d_v_scale;
+ * the element's value is its FP8 value times the scale.  Scale pointers are
+ * ignored (may be null) for 16-bit caches. */
+typedef struct {
+    void* d_k;
+    void* d_v;
+    uint8_t* d_k_scale;
+    uint8_t* d_v_scale;
+    uint64_t pool_pages;
+    uint64_t page_stride, token_stride, head_stride;
+    uint32_t page_tokens;  /* a power of two, 1 .. 65536 */
+    uint32_t kv_heads;     /* 1 .. 1024 */
+    uint32_t head_dim;     /* 64 or 128 (SPLITZIP_ERR_UNSUPPORTED otherwise) */
+    int32_t type;          /* splitzip_kv_type_t */
+} splitzip_kv_cache_t;
+
+/* One step of a batch (see above).  Device arrays of int32, 4-byte aligned. */
+typedef struct {
+    const int32_t* d_cu_tokens;   /* batch + 1 */
+    const int32_t* d_kv_len;      /* batch */
+    const int32_t* d_page_table;  /* batch rows of table_stride entries */
+    uint64_t table_stride;        /* >= ceil(max_kv_len / page_tokens) */
+    uint32_t batch;               /* 1 .. 65536 */
+    uint32_t tokens;              /* rows of the packed tensors */
+    uint32_t max_tokens;          /* most new tokens of one sequence, <= tokens */
+    uint32_t max_kv_len;          /* most tokens that a sequence holds, < 2^30 */
+} splitzip_kv_batch_t;
+
+/* Packed rows [row][head][head_dim]: element (row, head, i) is at
+ * row * token_stride + head * head_stride + i (elements; multiples of 8, so a
+ * slice of a fused projection's output needs no copy).  Base 16-byte aligned. */
+typedef struct {
+    void* d;
+    uint64_t token_stride, head_stride;
+} splitzip_kv_rows_t;
+
+/* Write the keys and values of the new tokens (k, v: kv_heads heads of
+ * `dtype`, SPLITZIP_BF16 or SPLITZIP_FP16) into their pages.  A 16-bit cache
+ * has to be of that type and gets the bits.  An FP8 cache gets, for each
+ * (token, head), the scale 2^k with the smallest k for which no finite
+ * element exceeds 2^k times the type's largest value (57344 or 448; k = 0 for
+ * a row of zeros, k >= -126), and round-to-nearest-even of x * 2^-k.  Both
+ * x * 2^-k and the stored value times 2^k are exact, so the stored value is
+ * off by one rounding.  NaN stays NaN; an infinity stays one in E5M2 and
+ * becomes NaN in E4M3.  Two rows of one call must not have the same place. */
+int splitzip_kv_write(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                      const splitzip_kv_rows_t* k, const splitzip_kv_rows_t* v, int dtype, int* d_status,
+                      cudaStream_t stream);
+
+/* Read the last tokens of every sequence back into packed rows of `dtype`
+ * (BF16 or FP16; a 16-bit cache has to be of that type).  FP8 values times
+ * their scale are exact in BF16; in FP16 they are rounded to nearest even, to
+ * infinity beyond its range. */
+int splitzip_kv_read(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                     const splitzip_kv_rows_t* k, const splitzip_kv_rows_t* v, int dtype, int* d_status,
+                     cudaStream_t stream);
+
+/* Scratch that splitzip_kv_attention needs on any step of at most these
+ * sizes (the batch's device pointers are not looked at). */
+int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                                         uint32_t q_heads, uint64_t* out_bytes);
+
+/* Attention of the new tokens over the pages: for row i of position p of a
+ * sequence and query head h, with kv head h / (q_heads / kv_heads),
+ *   s_j = scale * dot(q, k_j),   out = sum_j exp(s_j - lse) v_j,
+ *   lse = log(sum_j exp(s_j))
+ * over the positions j < kv_len that the row sees: j <= p unless `causal` is
+ * 0, and j > p - window unless `window` is 0.  The new tokens' own keys and
+ * values have to be in the cache (splitzip_kv_write).  A row that sees
+ * nothing gets out = 0 and lse = -infinity; what a position holds that a row
+ * does not see (NaN and infinities included) has no part in that row.
+ * q, out: q_heads heads (a multiple of kv_heads, at most 64 times as many) of
+ * `dtype` (BF16 or FP16; a 16-bit cache has to be of that type); out may be
+ * q.  d_lse: float [tokens][q_heads] or null.  scale: finite.
+ * Statistics and sums are held in 32 bits; each exp() is rounded to 16 bits
+ * (FP16 for an FP16 cache, else BF16) for the product with V.
+ * d_ws: ws_bytes >= splitzip_kv_attention_workspace_size, 16-byte aligned,
+ * contents need not be initialised; calls that share it must not overlap on
+ * the GPU.  Results do not depend on the order in which blocks run. */
+int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                          const splitzip_kv_rows_t* q, const splitzip_kv_rows_t* out, float* d_lse, int dtype,
+                          uint32_t q_heads, float scale, int causal, uint32_t window, void* d_ws,
+                          uint64_t ws_bytes, int* d_status, cudaStream_t stream);
+
 /* Self-test of the bounded device wait.  Every wait of the encode and
  * decode kernels on a bulk-copy barrier gives up after a bounded number of SM
  * cycles (about one second), records SPLITZIP_ERR_TIMEOUT in the status word

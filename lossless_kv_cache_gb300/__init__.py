@@ -23,6 +23,7 @@ FP16 = 2
 OK, ERR_INVALID_ARG, ERR_CAPACITY, ERR_CORRUPT, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED = range(7)
 DEFAULT_CHUNK_ELEMS = 65536
 HEADER_BYTES = 64
+KV_BF16, KV_FP8_E5M2, KV_FP16, KV_FP8_E4M3 = BF16, FP8_E5M2, FP16, 3  # splitzip_kv_type_t
 NOALLOC_SCRATCH_BYTES = 32 << 20  # SPLITZIP_NOALLOC_SCRATCH_BYTES
 
 
@@ -78,6 +79,26 @@ class DecodeItem(ctypes.Structure):
                 ("n", ctypes.c_uint64)]
 
 
+class KVCacheDesc(ctypes.Structure):
+    """splitzip_kv_cache_t."""
+    _fields_ = [("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p), ("d_k_scale", ctypes.c_void_p),
+                ("d_v_scale", ctypes.c_void_p), ("pool_pages", ctypes.c_uint64), ("page_stride", ctypes.c_uint64),
+                ("token_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64), ("page_tokens", ctypes.c_uint32),
+                ("kv_heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32), ("type", ctypes.c_int32)]
+
+
+class KVBatchDesc(ctypes.Structure):
+    """splitzip_kv_batch_t."""
+    _fields_ = [("d_cu_tokens", ctypes.c_void_p), ("d_kv_len", ctypes.c_void_p), ("d_page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_uint64), ("batch", ctypes.c_uint32), ("tokens", ctypes.c_uint32),
+                ("max_tokens", ctypes.c_uint32), ("max_kv_len", ctypes.c_uint32)]
+
+
+class KVRowsDesc(ctypes.Structure):
+    """splitzip_kv_rows_t."""
+    _fields_ = [("d", ctypes.c_void_p), ("token_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64)]
+
+
 MAX_BATCH = 256                 # SPLITZIP_MAX_BATCH
 MAX_BATCH_ITEM_ELEMS = 1 << 26  # SPLITZIP_MAX_BATCH_ITEM_ELEMS
 
@@ -106,6 +127,7 @@ class _Address(ctypes.c_void_p):
 
 _u64, _u32, _int, _vp = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int, _Address
 _P_u64 = ctypes.POINTER(ctypes.c_uint64)
+_P_cache, _P_batch, _P_rows = (ctypes.POINTER(t) for t in (KVCacheDesc, KVBatchDesc, KVRowsDesc))
 
 # name -> (restype, argtypes); mirrors include/splitzip.h
 SIGNATURES = {
@@ -140,6 +162,11 @@ SIGNATURES = {
     "splitzip_encode_batch": (_int, [ctypes.POINTER(EncodeItem), _u32, _int, ctypes.POINTER(Codebook), _u32, _vp,
                                      _u64, _vp, _vp]),
     "splitzip_decode_batch": (_int, [ctypes.POINTER(DecodeItem), _u32, _int, _vp, _vp]),
+    "splitzip_kv_write": (_int, [_P_cache, _P_batch, _P_rows, _P_rows, _int, _vp, _vp]),
+    "splitzip_kv_read": (_int, [_P_cache, _P_batch, _P_rows, _P_rows, _int, _vp, _vp]),
+    "splitzip_kv_attention_workspace_size": (_int, [_P_cache, _P_batch, _u32, _P_u64]),
+    "splitzip_kv_attention": (_int, [_P_cache, _P_batch, _P_rows, _P_rows, _vp, _int, _u32, ctypes.c_float, _int, _u32,
+                                     _vp, _u64, _vp, _vp]),
 }
 
 _lib = None
@@ -278,6 +305,28 @@ def splitzip_encode_batch(h_items, count, dtype, cb, chunk_elems, d_ws, ws_bytes
 def splitzip_decode_batch(h_items, count, dtype, d_status, stream):
     """h_items: ctypes array of DecodeItem."""
     return lib().splitzip_decode_batch(h_items, count, dtype, d_status, stream)
+
+
+def splitzip_kv_write(cache, batch, k, v, dtype, d_status, stream):
+    """cache, batch, k, v: KVCacheDesc, KVBatchDesc, KVRowsDesc, KVRowsDesc."""
+    return lib().splitzip_kv_write(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(k), ctypes.byref(v), dtype,
+                                   d_status, stream)
+
+
+def splitzip_kv_read(cache, batch, k, v, dtype, d_status, stream):
+    return lib().splitzip_kv_read(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(k), ctypes.byref(v), dtype,
+                                  d_status, stream)
+
+
+def splitzip_kv_attention_workspace_size(cache, batch, q_heads, out_bytes):
+    return lib().splitzip_kv_attention_workspace_size(ctypes.byref(cache), ctypes.byref(batch), q_heads,
+                                                      ctypes.byref(out_bytes))
+
+
+def splitzip_kv_attention(cache, batch, q, out, d_lse, dtype, q_heads, scale, causal, window, d_ws, ws_bytes, d_status,
+                          stream):
+    return lib().splitzip_kv_attention(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(q), ctypes.byref(out),
+                                       d_lse, dtype, q_heads, scale, causal, window, d_ws, ws_bytes, d_status, stream)
 
 
 # ------------------------------------------------------------ size helpers
@@ -565,3 +614,173 @@ def ablation_decode_status(blob, n, dtype, variant, stream=None):
     _check(splitzip_ablation_decode(blob.data_ptr(), blob.numel(), out.data_ptr() if n else 0, n, dtype, variant,
                                     status.data_ptr(), _stream_handle(stream)), "splitzip_ablation_decode")
     return int(status[0].item()), out[:n]
+
+
+# paged-cache operators (see splitzip_kv_write, splitzip_kv_read, splitzip_kv_attention)
+
+def _kv_type_of(t):
+    torch = _torch()
+    types = {torch.bfloat16: KV_BF16, torch.float16: KV_FP16, torch.float8_e5m2: KV_FP8_E5M2,
+             torch.float8_e4m3fn: KV_FP8_E4M3}
+    if t.dtype not in types:
+        raise TypeError("cache element type: expected bfloat16, float16, float8_e5m2 or float8_e4m3fn, got %s" % t.dtype)
+    return types[t.dtype]
+
+
+def _device_tensor(t, dtype, shape, what):
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: expected a CUDA tensor of %s and shape %s, got %s %s on %s"
+                         % (what, dtype, tuple(shape), t.dtype, tuple(t.shape), t.device))
+    return t
+
+
+class KVCache:
+    """One layer's paged cache: pools k and v of shape (pages, page_tokens,
+    kv_heads, head_dim), any strides with a contiguous last axis (a
+    permuted view of [page][head][token][dim] will do), bfloat16, float16,
+    float8_e5m2 or float8_e4m3fn.  FP8 caches take k_scale and v_scale, uint8
+    (pages, kv_heads, page_tokens).  The codec takes an E5M2 cache's pools as
+    raw bits: k.view(torch.uint8)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        torch = _torch()
+        self.type = _kv_type_of(k)
+        fp8 = self.type in (KV_FP8_E5M2, KV_FP8_E4M3)
+        if k.dim() != 4:
+            raise ValueError("k: expected (pages, page_tokens, kv_heads, head_dim), got %s" % (tuple(k.shape),))
+        pages, page_tokens, heads, dim = k.shape
+        _device_tensor(k, k.dtype, k.shape, "k")
+        _device_tensor(v, k.dtype, k.shape, "v")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v: expected the same strides and a contiguous last axis, got %s and %s"
+                             % (k.stride(), v.stride()))
+        if fp8:
+            for s, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if s is None or not s.is_contiguous():
+                    raise ValueError("%s: an FP8 cache needs a contiguous scale tensor" % what)
+                _device_tensor(s, torch.uint8, (pages, heads, page_tokens), what)
+        self.k, self.v = k, v
+        self.k_scale, self.v_scale = (k_scale, v_scale) if fp8 else (None, None)
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fp8 else None,
+                                v_scale.data_ptr() if fp8 else None, pages, k.stride(0), k.stride(1), k.stride(2),
+                                page_tokens, heads, dim, self.type)
+
+    @classmethod
+    def empty(cls, pages, page_tokens, kv_heads, head_dim, dtype, device="cuda"):
+        """A cache of zeros; dtype: a torch dtype."""
+        torch = _torch()
+        fp8 = dtype in (torch.float8_e5m2, torch.float8_e4m3fn)
+        raw = torch.uint8 if fp8 else torch.int16
+        pools = [torch.zeros(pages, page_tokens, kv_heads, head_dim, dtype=raw, device=device).view(dtype)
+                 for _ in range(2)]
+        scales = [torch.full((pages, kv_heads, page_tokens), 127, dtype=torch.uint8, device=device)
+                  for _ in range(2)] if fp8 else [None, None]
+        return cls(*pools, *scales)
+
+
+class KVBatch:
+    """One step of a batch, the same for every layer (splitzip_kv_batch_t):
+    int32 device tensors cu_tokens (batch + 1), kv_len (batch) and page_table
+    (batch, at least the pages of max_kv_len tokens); the packed tensors' row
+    count; the most new tokens and the most tokens of a sequence.  The device
+    tensors may be updated in place between steps within those maxima."""
+
+    def __init__(self, cu_tokens, kv_len, page_table, tokens, max_tokens, max_kv_len):
+        torch = _torch()
+        batch = kv_len.numel()
+        _device_tensor(cu_tokens, torch.int32, (batch + 1,), "cu_tokens")
+        _device_tensor(kv_len, torch.int32, (batch,), "kv_len")
+        if page_table.dim() != 2 or page_table.stride(1) != 1:
+            raise ValueError("page_table: expected (batch, pages) with a contiguous last axis")
+        _device_tensor(page_table, torch.int32, (batch, page_table.shape[1]), "page_table")
+        if not (cu_tokens.is_contiguous() and kv_len.is_contiguous()):
+            raise ValueError("cu_tokens and kv_len: expected contiguous tensors")
+        # a row's entries end where the table does, whatever the stride between rows
+        self.table_pages = page_table.shape[1]
+        self.cu_tokens, self.kv_len, self.page_table = cu_tokens, kv_len, page_table
+        self.tokens = tokens
+        self.desc = KVBatchDesc(cu_tokens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.stride(0),
+                                batch, tokens, max_tokens, max_kv_len)
+
+    def check(self, cache):
+        """Raises where the page table is narrower than max_kv_len tokens need."""
+        if self.table_pages * cache.desc.page_tokens < self.desc.max_kv_len:
+            raise SplitZipError(ERR_INVALID_ARG, "page_table of %d pages for %d tokens"
+                                % (self.table_pages, self.desc.max_kv_len))
+
+
+def _kv_rows(t, tokens, heads, dim, what):
+    """(KVRowsDesc, dtype constant) of a packed (tokens, heads, head_dim) tensor."""
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        dtype = BF16
+    elif t.dtype == torch.float16:
+        dtype = FP16
+    else:
+        raise TypeError("%s: expected bfloat16 or float16, got %s" % (what, t.dtype))
+    if not t.is_cuda or t.shape != (tokens, heads, dim) or t.stride(2) != 1:
+        raise ValueError("%s: expected a CUDA tensor (%d, %d, %d) with a contiguous last axis, got %s of strides %s on %s"
+                         % (what, tokens, heads, dim, tuple(t.shape), t.stride(), t.device))
+    return KVRowsDesc(t.data_ptr(), t.stride(0), t.stride(1)), dtype
+
+
+def _kv_rw(call, cache, batch, k, v, status, stream):
+    d = cache.desc
+    batch.check(cache)
+    rk, dtype = _kv_rows(k, batch.tokens, d.kv_heads, d.head_dim, "k")
+    rv, dtype_v = _kv_rows(v, batch.tokens, d.kv_heads, d.head_dim, "v")
+    if dtype != dtype_v:
+        raise TypeError("k and v: expected the same type")
+    _check(call(d, batch.desc, rk, rv, dtype, status.data_ptr(), _stream_handle(stream)), call.__name__)
+
+
+def kv_write(cache, batch, k, v, status, stream=None):
+    """Enqueue the write of the new tokens' keys and values, packed (tokens,
+    kv_heads, head_dim) tensors, into `cache`'s pages (asynchronous; status:
+    device int32, as for decode_into)."""
+    _kv_rw(splitzip_kv_write, cache, batch, k, v, status, stream)
+
+
+def kv_read(cache, batch, k, v, status, stream=None):
+    """Enqueue the read of every sequence's last tokens from `cache`'s pages into
+    the packed tensors k and v (asynchronous)."""
+    _kv_rw(splitzip_kv_read, cache, batch, k, v, status, stream)
+
+
+def kv_attention_workspace_size(cache, batch, q_heads):
+    out = ctypes.c_uint64(0)
+    _check(splitzip_kv_attention_workspace_size(cache.desc, batch.desc, q_heads, out),
+           "splitzip_kv_attention_workspace_size")
+    return out.value
+
+
+class KVAttentionBuffers:
+    """Device workspace and status word of kv_attention, for any step of at most
+    `batch`'s sizes on caches of `cache`'s geometry."""
+
+    def __init__(self, cache, batch, q_heads):
+        torch = _torch()
+        device = batch.kv_len.device
+        self.q_heads = q_heads
+        self.ws_bytes = kv_attention_workspace_size(cache, batch, q_heads)
+        self.ws = torch.empty(max(self.ws_bytes, 16), dtype=torch.uint8, device=device)
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)  # [0] = status
+
+
+def kv_attention(cache, batch, q, out, bufs, scale, causal=True, window=0, lse=None, stream=None):
+    """Enqueue the attention of the new tokens' queries over `cache`'s pages
+    (asynchronous).  q, out: packed (tokens, q_heads, head_dim); lse: None or
+    float32 (tokens, q_heads); bufs: KVAttentionBuffers."""
+    d = cache.desc
+    batch.check(cache)
+    rq, dtype = _kv_rows(q, batch.tokens, bufs.q_heads, d.head_dim, "q")
+    ro, dtype_o = _kv_rows(out, batch.tokens, bufs.q_heads, d.head_dim, "out")
+    if dtype != dtype_o:
+        raise TypeError("q and out: expected the same type")
+    if lse is not None:
+        if not lse.is_contiguous():
+            raise ValueError("lse: expected a contiguous tensor")
+        _device_tensor(lse, _torch().float32, (batch.tokens, bufs.q_heads), "lse")
+    _check(splitzip_kv_attention(d, batch.desc, rq, ro, None if lse is None else lse.data_ptr(), dtype, bufs.q_heads,
+                                 scale, int(causal), window, bufs.ws.data_ptr(), bufs.ws_bytes, bufs.status.data_ptr(),
+                                 _stream_handle(stream)), "splitzip_kv_attention")

@@ -195,6 +195,13 @@ int make_input_map(const void* d_in, int dtype, EncodeArgs* a, CUtensorMap* map,
 
 }  // namespace
 
+int splitzip::device_sms(int* sms) {
+    DeviceState d;
+    const int st = device_state(&d);
+    if (st == SPLITZIP_OK) *sms = d.sms;
+    return st;
+}
+
 extern "C" {
 
 const char* splitzip_status_string(int status) {

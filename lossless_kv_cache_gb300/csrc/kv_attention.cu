@@ -1,0 +1,83 @@
+// Host side of splitzip_kv_attention: argument checks, workspace, and which
+// kernel a step takes.
+#include <algorithm>
+#include <cmath>
+
+#include "kv_attention.cuh"
+
+using namespace splitzip;
+
+namespace {
+
+uint64_t align256(uint64_t x) { return (x + 255u) & ~uint64_t(255); }
+
+struct Plan {
+    uint32_t group, ctas;
+    uint64_t parts_off, ws_bytes;
+};
+
+// The same for every step of these largest sizes, so that a workspace sized
+// once serves them all.
+int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, Plan* p) {
+    if (q_heads == 0 || q_heads % c.kv_heads != 0) return SPLITZIP_ERR_INVALID_ARG;
+    p->group = q_heads / c.kv_heads;
+    if (p->group > 64) return SPLITZIP_ERR_UNSUPPORTED;
+    // tiles of rows over all sequences: each has a partial one at most
+    const uint64_t tiles = std::min<uint64_t>((uint64_t(b.tokens) * p->group + kStepRows - 1) / kStepRows + b.batch,
+                                              uint64_t(b.tokens) * p->group);
+    p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);
+    p->parts_off = align256(4ull * p->ctas);
+    p->ws_bytes = align256(p->parts_off + 4ull * 2 * p->ctas * step_part_floats(c.head_dim));
+    return SPLITZIP_OK;
+}
+
+}  // namespace
+
+extern "C" int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* cache,
+                                                    const splitzip_kv_batch_t* batch, uint32_t q_heads,
+                                                    uint64_t* out_bytes) {
+    KvCache c;
+    KvBatch b;
+    Plan p;
+    int st = check_kv(cache, batch, &c, &b, false);
+    if (st != SPLITZIP_OK) return st;
+    if (!out_bytes) return SPLITZIP_ERR_INVALID_ARG;
+    if ((st = plan_for(c, b, q_heads, &p)) != SPLITZIP_OK) return st;
+    *out_bytes = p.ws_bytes;
+    return SPLITZIP_OK;
+}
+
+extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                                     const splitzip_kv_rows_t* q, const splitzip_kv_rows_t* out, float* d_lse,
+                                     int dtype, uint32_t q_heads, float scale, int causal, uint32_t window,
+                                     void* d_ws, uint64_t ws_bytes, int* d_status, cudaStream_t stream) {
+    AttentionArgs a;
+    Plan p;
+    int st = check_kv(cache, batch, &a.c, &a.b, true);
+    if (st != SPLITZIP_OK) return st;
+    if ((st = plan_for(a.c, a.b, q_heads, &p)) != SPLITZIP_OK) return st;
+    if (!kv_dtype_fits(a.c.type, dtype) || !std::isfinite(scale)) return SPLITZIP_ERR_INVALID_ARG;
+    if ((st = check_rows(q, a.b, q_heads, a.c.head_dim, &a.q)) != SPLITZIP_OK) return st;
+    if ((st = check_rows(out, a.b, q_heads, a.c.head_dim, &a.out)) != SPLITZIP_OK) return st;
+    if (!d_status || (reinterpret_cast<uintptr_t>(d_status) & 3u) || (reinterpret_cast<uintptr_t>(d_lse) & 3u))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (ws_bytes < p.ws_bytes) return SPLITZIP_ERR_CAPACITY;
+    if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 15u)) return SPLITZIP_ERR_INVALID_ARG;
+    a.lse = d_lse;
+    a.q_heads = q_heads;
+    a.group = p.group;
+    a.scale_log2 = float(double(scale) * 1.4426950408889634);
+    a.causal = causal != 0;
+    a.window = std::min(window, 1u << 30);  // past every position
+    a.counters = static_cast<uint32_t*>(d_ws);
+    a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + p.parts_off);
+    a.status = d_status;
+    int sms;
+    if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
+    if (launch_kv_begin(d_status, a.counters, p.ctas, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return SPLITZIP_ERR_CUDA;
+    }
+    if (a.b.tokens == 0) return SPLITZIP_OK;
+    return launch_kv_step(a, dtype == SPLITZIP_FP16, p.ctas, stream);
+}

@@ -1,0 +1,350 @@
+// Writing new keys and values into the pages of a KV cache, and reading them
+// back (splitzip_kv_write, splitzip_kv_read).
+//
+// Mathematics.  An FP8 cache keeps, for each (token, head), q_i = RN8(x_i /
+// 2^k) and the exponent k = min{k : max |x_i| <= M 2^k} of the row's scale, M
+// the type's largest value.  M is 1.75 * 2^T (T = 15 for E5M2, 8 for E4M3), so
+// with max |x_i| = m 2^e, 1 <= m < 2, k = e - T, plus 1 where m > 1.75: one
+// comparison of mantissa bits, no division.  The scale being a power of two,
+// x_i / 2^k and q_i 2^k are exact and the only rounding is RN8.
+//
+// What bounds it: HBM.  Nothing is reused, so a row of head_dim elements goes
+// through the registers of head_dim / 8 lanes, 16 bytes of the 16-bit side
+// and 8 or 16 of the cache's side in each lane; the row's maximum is one
+// redux.sync over those lanes.  A warp takes up to 8 rows (K or V of several
+// heads) of one token, so the search for the token's sequence and its page is
+// done once for all of them while their loads are in flight.
+#include "kv_common.cuh"
+
+namespace splitzip {
+namespace {
+
+constexpr int kRwWarps = 4;
+
+__global__ void kv_begin_kernel(int* status, uint32_t* words, uint32_t count) {
+    release_successor();
+    if (threadIdx.x == 0) *status = SPLITZIP_OK;
+    for (uint32_t i = threadIdx.x; i < count; i += blockDim.x) words[i] = 0;
+}
+
+// The last sequence b with cu[b] <= row, 32 candidates a step; every lane gets
+// the same answer (-1: none).
+__device__ __forceinline__ int find_seq(const KvBatch& B, int row, uint32_t lane) {
+    int lo = 0, n = int(B.batch);
+    while (true) {
+        const int step = (n + 31) / 32;
+        const int i = lo + int(lane) * step;
+        const bool le = i < lo + n && B.cu[i] <= row;
+        const int found = __popc(__ballot_sync(~0u, le));
+        if (found == 0) return -1;
+        n = min(step, n - (found - 1) * step);
+        lo += (found - 1) * step;
+        if (step == 1) return lo;
+    }
+}
+
+struct RwArgs {
+    KvCache c;
+    KvBatch b;
+    KvRows k, v;
+    int* status;
+};
+
+// One element's 16 bits as a float, and back.
+template <bool H>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+    return H ? half2_to_float2(w) : bf16x2_to_float2(w);
+}
+
+template <bool H>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    return H ? pack_half2(a, b) : pack_bf16x2(a, b);
+}
+
+// Eight elements of a row, quantised; lanes `mask` (LPR of them) hold the row.
+template <bool E5M2, bool H, int LPR>
+__device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t mask, uint32_t* scale) {
+    constexpr uint32_t kInf = H ? 0x7C00u : 0x7F80u;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t top = 0;  // largest magnitude: 16-bit floats order as integers
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    uint32_t most = __reduce_max_sync(mask, max(top & 0xFFFFu, top >> 16));
+    const bool special = most >= kInf;  // the row has an infinity or a NaN
+    if (special) {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+            top = max(top, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
+        }
+        most = __reduce_max_sync(mask, top);
+    }
+    const uint32_t bits = __float_as_uint(unpack16<H>(most).x);
+    int k = int(bits >> 23) - 127 - (E5M2 ? 15 : 8) + ((bits & 0x7FFFFFu) > 0x600000u);
+    k = most == 0 ? 0 : max(k, -126);
+    *scale = uint32_t(k + 127);
+    const float inv = __uint_as_float(uint32_t(127 - k) << 23);
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack16<H>(w[i]);
+        q[i] = float2_to_fp8x2<E5M2>(f.x * inv, f.y * inv);
+        if (special) {  // the conversion saturates infinities
+            if ((w[i] & 0x7FFFu) == kInf) q[i] = (q[i] & 0xFF00u) | (E5M2 ? 0x7Cu : 0x7Fu) | ((w[i] >> 8) & 0x80u);
+            if (((w[i] >> 16) & 0x7FFFu) == kInf)
+                q[i] = (q[i] & 0x00FFu) | (E5M2 ? 0x7C00u : 0x7F00u) | ((w[i] >> 16) & 0x8000u);
+        }
+    }
+    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+
+template <bool E5M2, bool H>
+__device__ __forceinline__ uint4 dequantise8(const uint2& q, float scale) {
+    const uint32_t w[2] = {q.x, q.y};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = half2_to_float2(fp8x2_to_half2<E5M2>(w[i / 2] >> (16 * (i & 1))));
+        o[i] = pack16<H>(f.x * scale, f.y * scale);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// FMT 0: 16-bit cache, 1: E5M2, 2: E4M3.  LPR lanes hold a row, PASSES times
+// 32 / LPR rows a warp.
+template <bool WRITE, int FMT, bool H, int LPR, int PASSES>
+__global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_constant__ RwArgs a) {
+    constexpr uint32_t kRows = 32 / LPR;  // rows a pass
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t items = 2 * a.c.kv_heads;  // rows of one token: K then V
+    const uint32_t parts = (items + kRows * PASSES - 1) / (kRows * PASSES);
+    const uint64_t warp = uint64_t(blockIdx.x) * kRwWarps + (threadIdx.x >> 5);
+    const uint64_t token = warp / parts;
+    const uint32_t first = uint32_t(warp - token * parts) * (kRows * PASSES) + lane / LPR;
+    const uint32_t col = lane % LPR;
+    bool bad = false;
+    if (token < a.b.tokens) {
+        uint4 x[PASSES];
+        if (WRITE) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const uint32_t item = first + p * kRows;
+                if (item < items) {
+                    const bool is_v = item >= a.c.kv_heads;
+                    const KvRows& r = is_v ? a.v : a.k;
+                    const uint32_t head = item - (is_v ? a.c.kv_heads : 0u);
+                    x[p] = __ldcs(reinterpret_cast<const uint4*>(r.d + token * r.token_stride + head * r.head_stride) + col);
+                }
+            }
+        }
+        const int b = find_seq(a.b, int(token), lane);
+        bool mine = b >= 0, placed = false;
+        uint64_t page = 0;
+        uint32_t slot = 0;
+        if (mine) {
+            const int c1 = a.b.cu[b + 1];
+            mine = int(token) < c1;
+            if (mine) {
+                const KvSeq s = load_seq(a.b, uint32_t(b));
+                bad = !s.ok;
+                const int pos = s.n - (c1 - int(token));
+                if (s.ok && pos >= 0) {
+                    const int32_t pg = a.b.table[uint64_t(b) * a.b.table_stride + (uint32_t(pos) >> a.c.page_shift)];
+                    placed = pg >= 0 && uint64_t(pg) < a.c.pool_pages;
+                    bad = !placed;
+                    page = uint64_t(uint32_t(pg));
+                    slot = uint32_t(pos) & ((1u << a.c.page_shift) - 1u);
+                }
+            }
+        }
+        if (mine && !bad && (placed || !WRITE)) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const uint32_t item = first + p * kRows;
+                if (item >= items) continue;
+                const bool is_v = item >= a.c.kv_heads;
+                const uint32_t head = item - (is_v ? a.c.kv_heads : 0u);
+                uint8_t* at = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + uint64_t(slot) * a.c.token_stride +
+                              head * a.c.head_stride;
+                uint8_t* scale_at = FMT == 0 ? nullptr
+                                             : (is_v ? a.c.v_scale : a.c.k_scale) +
+                                                   (((page * a.c.kv_heads + head) << a.c.page_shift) + slot);
+                if (WRITE) {
+                    if (FMT == 0) {
+                        reinterpret_cast<uint4*>(at)[col] = x[p];
+                    } else {
+                        const uint32_t mask = (LPR == 32 ? ~0u : ((1u << (LPR % 32)) - 1u)) << (lane / LPR * LPR);
+                        uint32_t scale;
+                        reinterpret_cast<uint2*>(at)[col] = quantise8<FMT == 1, H, LPR>(x[p], mask, &scale);
+                        if (col == 0) *scale_at = uint8_t(scale);
+                    }
+                } else {
+                    x[p] = make_uint4(0, 0, 0, 0);  // a row without a place reads as zeros
+                    if (placed) {
+                        if (FMT == 0)
+                            x[p] = __ldcs(reinterpret_cast<const uint4*>(at) + col);
+                        else
+                            x[p] = dequantise8<FMT == 1, H>(__ldcs(reinterpret_cast<const uint2*>(at) + col),
+                                                            scale_value(*scale_at));
+                    }
+                }
+            }
+            if (!WRITE) {
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p) {
+                    const uint32_t item = first + p * kRows;
+                    if (item >= items) continue;
+                    const bool is_v = item >= a.c.kv_heads;
+                    const KvRows& r = is_v ? a.v : a.k;
+                    const uint32_t head = item - (is_v ? a.c.kv_heads : 0u);
+                    __stcs(reinterpret_cast<uint4*>(r.d + token * r.token_stride + head * r.head_stride) + col, x[p]);
+                }
+            }
+        }
+    }
+    wait_predecessor();  // the status word has been cleared
+    if (bad && lane == 0) report(a.status, SPLITZIP_ERR_INVALID_ARG);
+}
+
+template <bool WRITE, int FMT, bool H>
+cudaError_t launch_rw(const RwArgs& a, cudaStream_t s) {
+    constexpr int kPasses = 4;
+    const uint32_t lpr = a.c.head_dim / 8, rows = 32 / lpr * kPasses;
+    const uint64_t parts = (2 * a.c.kv_heads + rows - 1) / rows;
+    const uint64_t grid = (uint64_t(a.b.tokens) * parts + kRwWarps - 1) / kRwWarps;
+    if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    ChainedLaunch l(dim3(uint32_t(grid)), dim3(kRwWarps * 32), 0, s);
+    return lpr == 16 ? cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 16, kPasses>, a)
+                     : cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 8, kPasses>, a);
+}
+
+template <bool WRITE>
+int kv_rw_call(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch, const splitzip_kv_rows_t* k,
+               const splitzip_kv_rows_t* v, int dtype, int* d_status, cudaStream_t stream) {
+    RwArgs a;
+    int st = check_kv(cache, batch, &a.c, &a.b, true);
+    if (st != SPLITZIP_OK) return st;
+    if (!d_status || (reinterpret_cast<uintptr_t>(d_status) & 3u) || !kv_dtype_fits(a.c.type, dtype))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if ((st = check_rows(k, a.b, a.c.kv_heads, a.c.head_dim, &a.k)) != SPLITZIP_OK) return st;
+    if ((st = check_rows(v, a.b, a.c.kv_heads, a.c.head_dim, &a.v)) != SPLITZIP_OK) return st;
+    a.status = d_status;
+    int sms;
+    if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
+    cudaError_t e = launch_kv_begin(d_status, nullptr, 0, stream);
+    if (e == cudaSuccess && a.b.tokens > 0) {
+        const bool h = dtype == SPLITZIP_FP16;
+        if (a.c.type == SPLITZIP_KV_FP8_E5M2)
+            e = h ? launch_rw<WRITE, 1, true>(a, stream) : launch_rw<WRITE, 1, false>(a, stream);
+        else if (a.c.type == SPLITZIP_KV_FP8_E4M3)
+            e = h ? launch_rw<WRITE, 2, true>(a, stream) : launch_rw<WRITE, 2, false>(a, stream);
+        else
+            e = launch_rw<WRITE, 0, false>(a, stream);
+    }
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? SPLITZIP_OK : SPLITZIP_ERR_CUDA;
+}
+
+bool multiple_of(uint64_t x, uint64_t m) { return x % m == 0; }
+
+}  // namespace
+
+cudaError_t launch_kv_begin(int* status, uint32_t* words, uint32_t count, cudaStream_t s) {
+    kv_begin_kernel<<<1, 256, 0, s>>>(status, words, count);
+    return cudaGetLastError();
+}
+
+bool kv_dtype_fits(int type, int dtype) {
+    if (dtype != SPLITZIP_BF16 && dtype != SPLITZIP_FP16) return false;
+    if (type == SPLITZIP_KV_BF16) return dtype == SPLITZIP_BF16;
+    if (type == SPLITZIP_KV_FP16) return dtype == SPLITZIP_FP16;
+    return true;
+}
+
+int check_kv(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch, KvCache* c, KvBatch* b,
+             bool need_ptrs) {
+    if (!cache || !batch) return SPLITZIP_ERR_INVALID_ARG;
+    const auto addr = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+    if (cache->type < SPLITZIP_KV_BF16 || cache->type > SPLITZIP_KV_FP8_E4M3) return SPLITZIP_ERR_INVALID_ARG;
+    const bool fp8 = cache->type == SPLITZIP_KV_FP8_E5M2 || cache->type == SPLITZIP_KV_FP8_E4M3;
+    const uint64_t size = fp8 ? 1 : 2, quantum = 16 / size;
+    const uint32_t pt = cache->page_tokens;
+    if (pt == 0 || pt > 65536u || (pt & (pt - 1u)) || cache->kv_heads == 0 || cache->kv_heads > 1024u ||
+        cache->pool_pages == 0)
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (cache->head_dim != 64u && cache->head_dim != 128u) return SPLITZIP_ERR_UNSUPPORTED;
+    if (cache->pool_pages > 0x7FFFFFFFull) return SPLITZIP_ERR_UNSUPPORTED;
+    if (!multiple_of(cache->page_stride, quantum) || !multiple_of(cache->token_stride, quantum) ||
+        !multiple_of(cache->head_stride, quantum))
+        return SPLITZIP_ERR_INVALID_ARG;
+    // keeps every byte offset below 2^62
+    const uint64_t limit = uint64_t(1) << 40;
+    if (cache->page_stride > limit || cache->token_stride > limit || cache->head_stride > limit ||
+        cache->page_stride * cache->pool_pages > (uint64_t(1) << 48))
+        return SPLITZIP_ERR_UNSUPPORTED;
+    if (need_ptrs) {
+        if (!cache->d_k || !cache->d_v || (addr(cache->d_k) & 15u) || (addr(cache->d_v) & 15u))
+            return SPLITZIP_ERR_INVALID_ARG;
+        if (fp8 && (!cache->d_k_scale || !cache->d_v_scale)) return SPLITZIP_ERR_INVALID_ARG;
+        if (!batch->d_cu_tokens || !batch->d_kv_len || !batch->d_page_table || (addr(batch->d_cu_tokens) & 3u) ||
+            (addr(batch->d_kv_len) & 3u) || (addr(batch->d_page_table) & 3u))
+            return SPLITZIP_ERR_INVALID_ARG;
+    }
+    if (batch->batch == 0 || batch->max_tokens > batch->tokens) return SPLITZIP_ERR_INVALID_ARG;
+    if (batch->batch > 65536u || batch->tokens >= (1u << 30) || batch->max_kv_len >= (1u << 30))
+        return SPLITZIP_ERR_UNSUPPORTED;
+    uint32_t shift = 0;
+    while ((1u << shift) < pt) ++shift;
+    if (batch->table_stride < (uint64_t(batch->max_kv_len) + pt - 1u) >> shift ||
+        batch->table_stride > (uint64_t(1) << 32))
+        return SPLITZIP_ERR_INVALID_ARG;
+    c->k = static_cast<uint8_t*>(cache->d_k);
+    c->v = static_cast<uint8_t*>(cache->d_v);
+    c->k_scale = cache->d_k_scale;
+    c->v_scale = cache->d_v_scale;
+    c->pool_pages = cache->pool_pages;
+    c->page_stride = cache->page_stride * size;
+    c->token_stride = cache->token_stride * size;
+    c->head_stride = cache->head_stride * size;
+    c->page_shift = shift;
+    c->kv_heads = cache->kv_heads;
+    c->head_dim = cache->head_dim;
+    c->type = cache->type;
+    b->cu = batch->d_cu_tokens;
+    b->kv_len = batch->d_kv_len;
+    b->table = batch->d_page_table;
+    b->table_stride = batch->table_stride;
+    b->batch = batch->batch;
+    b->tokens = batch->tokens;
+    b->max_tokens = batch->max_tokens;
+    b->max_kv_len = batch->max_kv_len;
+    return SPLITZIP_OK;
+}
+
+int check_rows(const splitzip_kv_rows_t* r, const KvBatch& b, uint32_t heads, uint32_t head_dim, KvRows* out) {
+    if (!r || r->token_stride % 8u || r->head_stride % 8u) return SPLITZIP_ERR_INVALID_ARG;
+    if (b.tokens > 0 && (!r->d || (reinterpret_cast<uintptr_t>(r->d) & 15u))) return SPLITZIP_ERR_INVALID_ARG;
+    // rows must not overlap: heads apart by a row, tokens apart too
+    if (heads > 1 && r->head_stride < head_dim) return SPLITZIP_ERR_INVALID_ARG;
+    if (b.tokens > 1 && r->token_stride < head_dim) return SPLITZIP_ERR_INVALID_ARG;
+    if (r->token_stride > (uint64_t(1) << 32) || r->head_stride > (uint64_t(1) << 32)) return SPLITZIP_ERR_UNSUPPORTED;
+    out->d = static_cast<uint16_t*>(r->d);
+    out->token_stride = r->token_stride;
+    out->head_stride = r->head_stride;
+    return SPLITZIP_OK;
+}
+
+}  // namespace splitzip
+
+extern "C" int splitzip_kv_write(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                                 const splitzip_kv_rows_t* k, const splitzip_kv_rows_t* v, int dtype, int* d_status,
+                                 cudaStream_t stream) {
+    return splitzip::kv_rw_call<true>(cache, batch, k, v, dtype, d_status, stream);
+}
+
+extern "C" int splitzip_kv_read(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                                const splitzip_kv_rows_t* k, const splitzip_kv_rows_t* v, int dtype, int* d_status,
+                                cudaStream_t stream) {
+    return splitzip::kv_rw_call<false>(cache, batch, k, v, dtype, d_status, stream);
+}

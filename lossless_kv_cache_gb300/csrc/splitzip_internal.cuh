@@ -194,4 +194,8 @@ cudaError_t occupancy_encode(int* blocks_per_sm, int dtype);
 cudaError_t occupancy_decode(int* blocks_per_sm, int dtype);
 cudaError_t occupancy_histogram(int* blocks_per_sm, int dtype);
 
+// SM count of the current device; an error status if it is no sm_103a device
+// (capi.cu).
+int device_sms(int* sms);
+
 }  // namespace splitzip
