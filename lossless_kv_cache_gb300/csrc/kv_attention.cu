@@ -11,23 +11,38 @@ namespace {
 
 uint64_t align256(uint64_t x) { return (x + 255u) & ~uint64_t(255); }
 
+// Rows of a sequence (new tokens by query heads of a group) up to which a step
+// takes the kernel of 16-row tiles, which is bound by the bytes of the cache,
+// rather than the tensor cores' 128-row tiles.
+constexpr uint64_t kStepRowsMax = 64;
+
 struct Plan {
     uint32_t group, ctas;
-    uint64_t parts_off, ws_bytes;
+    bool chunk;
+    uint64_t plan_off, parts_off, ws_bytes;
 };
 
-// The same for every step of these largest sizes, so that a workspace sized
-// once serves them all.
+void size_of(Plan* p, uint64_t plan_bytes, uint64_t counters, uint64_t part_floats) {
+    p->plan_off = align256(4ull * counters);
+    p->parts_off = align256(p->plan_off + plan_bytes);
+    p->ws_bytes = align256(p->parts_off + 4ull * 2 * p->ctas * part_floats);
+}
+
 int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, Plan* p) {
     if (q_heads == 0 || q_heads % c.kv_heads != 0) return SPLITZIP_ERR_INVALID_ARG;
     p->group = q_heads / c.kv_heads;
     if (p->group > 64) return SPLITZIP_ERR_UNSUPPORTED;
-    // tiles of rows over all sequences: each has a partial one at most
-    const uint64_t tiles = std::min<uint64_t>((uint64_t(b.tokens) * p->group + kStepRows - 1) / kStepRows + b.batch,
-                                              uint64_t(b.tokens) * p->group);
-    p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);
-    p->parts_off = align256(4ull * p->ctas);
-    p->ws_bytes = align256(p->parts_off + 4ull * 2 * p->ctas * step_part_floats(c.head_dim));
+    const uint64_t rows = uint64_t(b.tokens) * p->group;
+    p->chunk = uint64_t(b.max_tokens) * p->group > kStepRowsMax;
+    if (p->chunk) {
+        p->ctas = chunk_ctas(rows, b.batch, c.kv_heads, b.max_kv_len);
+        size_of(p, chunk_plan_bytes(p->ctas), 2ull * p->ctas, chunk_part_floats(c.head_dim));
+    } else {
+        // tiles of rows over all sequences: each has a partial one at most
+        const uint64_t tiles = std::min<uint64_t>((rows + kStepRows - 1) / kStepRows + b.batch, rows);
+        p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);
+        size_of(p, 0, p->ctas, step_part_floats(c.head_dim));
+    }
     return SPLITZIP_OK;
 }
 
@@ -67,6 +82,13 @@ extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const spl
     a.q_heads = q_heads;
     a.group = p.group;
     a.scale_log2 = float(double(scale) * 1.4426950408889634);
+    a.negate = 0;
+    a.lag = 0.f;
+    if (p.chunk) {
+        a.negate = a.scale_log2 < 0.f;
+        a.scale_log2 = std::max(std::fabs(a.scale_log2), 1.17549435e-38f);
+        a.lag = 8.f / a.scale_log2;
+    }
     a.causal = causal != 0;
     a.window = std::min(window, 1u << 30);  // past every position
     a.counters = static_cast<uint32_t*>(d_ws);
@@ -74,10 +96,12 @@ extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const spl
     a.status = d_status;
     int sms;
     if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
+    const bool half = dtype == SPLITZIP_FP16;
+    if (p.chunk && a.b.tokens > 0)
+        return launch_kv_chunk(a, half, static_cast<uint8_t*>(d_ws) + p.plan_off, p.ctas, stream);
     if (launch_kv_begin(d_status, a.counters, p.ctas, stream) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }
-    if (a.b.tokens == 0) return SPLITZIP_OK;
-    return launch_kv_step(a, dtype == SPLITZIP_FP16, p.ctas, stream);
+    return a.b.tokens > 0 ? launch_kv_step(a, half, p.ctas, stream) : int(SPLITZIP_OK);
 }

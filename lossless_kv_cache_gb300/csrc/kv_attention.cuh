@@ -23,10 +23,14 @@ struct AttentionArgs {
     KvRows q, out;
     float* lse;
     uint32_t q_heads, group;
-    float scale_log2;  // scale * log2(e)
+    // scale * log2(e).  The chunk kernel takes its magnitude, at least the
+    // smallest normal, with its sign (`negate`) given to the queries.
+    float scale_log2;
+    int negate;
+    float lag;  // chunk kernel: how far the reference may lag the maximum, before the scale
     int causal;
     uint32_t window;
-    uint32_t* counters;  // workspace, one a CTA
+    uint32_t* counters;  // workspace, one (chunk kernel: two) a CTA
     float* parts;        // workspace, two slots a CTA
     int* status;
 };
@@ -73,8 +77,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // kv_step.cu
 constexpr int kStepRows = 16;  // rows of a tile
-uint32_t step_ctas(uint64_t items_max, uint64_t units_max);
+uint32_t step_ctas(uint64_t items_max, uint64_t keys_max);
 uint64_t step_part_floats(uint32_t head_dim);
 int launch_kv_step(const AttentionArgs& a, bool q_half, uint32_t ctas, cudaStream_t s);
+
+// kv_chunk.cu
+uint32_t chunk_ctas(uint64_t rows, uint64_t batch, uint64_t kv_heads, uint64_t keys_max);
+uint64_t chunk_part_floats(uint32_t head_dim);
+uint64_t chunk_plan_bytes(uint32_t ctas);
+int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s);
 
 }  // namespace splitzip

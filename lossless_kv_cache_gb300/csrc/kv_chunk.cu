@@ -1,0 +1,853 @@
+// Attention of chunks of new tokens over a paged cache, on the fifth-generation
+// tensor cores.
+//
+// Mathematics: as in kv_step.cu, online softmax over units of 128 keys; the
+// running maximum that the exponentials are taken against is allowed to lag
+// the true one by a factor of 2^8, so that the sums o are rescaled only when
+// it grows by more (the exact factor cancels in o / l).
+//
+// What bounds it: the tensor core, 4 * head_dim operations for each (row,
+// key), with the exponentials next.  A CTA holds two tiles of 128 rows (new
+// tokens by the query heads that share a kv head) and passes over the keys
+// once for both.  Sixteen warps:
+//   0-3, 4-7   one tile's softmax each: a thread is a row; scores from TMEM,
+//              exponentials back to TMEM as the first operand of the product
+//              with V; rescaling and the final division are theirs too
+//   8-11       loaders: rows of K and V from their pages into swizzled shared
+//              memory (cp.async for a 16-bit cache; FP8 by way of a staging
+//              buffer, converted by the thread that copied it), rows past the
+//              end as zeros
+//   12         one thread issues the products, in the order
+//              S0(j+1) | P1(j) V(j) | S1(j+1) | P0(j+1) V(j+1) | ...
+//              so that each tile's softmax runs under the other's products
+// TMEM: S0, S1 (128 columns each, the weights overwrite the scores), O0, O1.
+// The tensor core executes a CTA's products in the order of issue, which is
+// what lets S(j+1) overwrite the weights that P(j) V(j) reads.
+//
+// Every wait is bounded.  A thread whose wait ran out stops waiting and
+// working but walks its loops to the end, so that every barrier among threads
+// is still reached, and SPLITZIP_ERR_TIMEOUT is reported.
+#include <algorithm>
+#include <atomic>
+
+#include "kv_attention.cuh"
+#include "tma_pipeline.cuh"
+#include "tcgen05.cuh"
+
+namespace splitzip {
+namespace {
+
+constexpr int kUnit = 128;       // keys
+constexpr int kTileRows = 128;   // rows of a softmax group
+constexpr int kRows = 2 * kTileRows;
+constexpr int kThreads = 512;
+constexpr uint32_t kChunkCtas = 152;  // one on each SM
+constexpr int kPlanThreads = 1024;
+
+struct ChunkStart {
+    uint32_t b, tile;
+    uint64_t group_start;  // first unit of the (sequence, tile)'s kv heads
+};
+
+struct ChunkPlan {
+    uint64_t units;
+    uint32_t ctas, pad;
+    ChunkStart start[1];
+};
+
+__device__ __forceinline__ int tile_count(const AttentionArgs& a, const KvSeq& s) {
+    return (s.t * int(a.group) + kRows - 1) / kRows;
+}
+
+struct Tile {
+    int row_first, rows;
+    KeyRange keys;
+    int units;
+};
+
+__device__ __forceinline__ Tile tile_of(const AttentionArgs& a, const KvSeq& s, int tile) {
+    Tile t;
+    t.row_first = tile * kRows;
+    t.rows = min(kRows, s.t * int(a.group) - t.row_first);
+    t.keys = visible(a, s, t.row_first / int(a.group), (t.row_first + t.rows - 1) / int(a.group));
+    t.units = unit_count(t.keys, kUnit);
+    return t;
+}
+
+// Deals the units of all items to the CTAs (see kv_attention.cuh) and clears
+// the counters and the status word.  Items are in the order sequence, tile, kv
+// head.  One CTA: a thread sums a sequence of one or two tiles, a warp one of
+// more, then a scan over the sequences.
+__global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __grid_constant__ AttentionArgs a,
+                                                                     ChunkPlan* plan, uint32_t grid) {
+    release_successor();
+    __shared__ uint64_t s_warp[kPlanThreads / 32];
+    __shared__ int s_bad;
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+    if (tid == 0) s_bad = 0;
+    for (uint32_t i = tid; i < 2 * grid; i += kPlanThreads) a.counters[i] = 0;
+    __syncthreads();
+    const auto weight = [&](const KvSeq& s, int tile) -> uint64_t {
+        return uint64_t(tile_of(a, s, tile).units) * a.c.kv_heads;
+    };
+    // units of the lane's sequence (every lane of a warp at once)
+    const auto seq_units = [&](const KvSeq& s) -> uint64_t {
+        const int n = tile_count(a, s);
+        uint64_t w = 0;
+        for (int i = 0; i < n && n <= 2; ++i) w += weight(s, i);
+        uint32_t many = __ballot_sync(~0u, n > 2);
+        while (many) {
+            const int src = __ffs(many) - 1;
+            many &= many - 1;
+            KvSeq o;
+            o.row0 = 0;
+            o.ok = true;
+            o.t = __shfl_sync(~0u, s.t, src);
+            o.n = __shfl_sync(~0u, s.n, src);
+            uint64_t part = 0;
+            const int tiles = tile_count(a, o);
+            for (int i = int(lane); i < tiles; i += 32) part += weight(o, i);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(~0u, part, d);
+            if (int(lane) == src) w = part;
+        }
+        return w;
+    };
+    const auto seq_at = [&](uint32_t b) -> KvSeq {
+        KvSeq s{0, 0, 0, true};
+        if (b < a.b.batch) {
+            s = load_seq(a.b, b);
+            if (!s.ok) s_bad = 1;
+        }
+        return s;
+    };
+    // inclusive scan over the CTA; *total for all
+    const auto scan = [&](uint64_t x, uint64_t* total) -> uint64_t {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t y = __shfl_up_sync(~0u, x, d);
+            if (int(lane) >= d) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        uint64_t before = 0, all = 0;
+        for (int i = 0; i < kPlanThreads / 32; ++i) {
+            if (i < int(warp)) before += s_warp[i];
+            all += s_warp[i];
+        }
+        *total = all;
+        return x + before;
+    };
+    uint64_t units = 0;
+    const bool once = a.b.batch <= kPlanThreads;
+    KvSeq s{0, 0, 0, true};
+    uint64_t w = 0, upto = 0;
+    for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) {
+        s = seq_at(b0 + tid);
+        w = seq_units(s);
+        uint64_t total;
+        upto = scan(w, &total);
+        units += total;
+    }
+    const uint32_t ctas = uint32_t(min(uint64_t(grid), max(units, uint64_t(1))));
+    uint64_t base = 0;
+    for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) {
+        uint64_t total = 0;
+        if (!once) {
+            s = seq_at(b0 + tid);
+            w = seq_units(s);
+            upto = scan(w, &total);
+        }
+        uint64_t from = base + upto - w;
+        // the CTAs whose share starts within [lo, hi)
+        const auto starts = [&](uint32_t b, uint32_t tile, uint64_t lo, uint64_t hi) {
+            for (uint64_t c = (lo * ctas + units - 1) / units; c < ctas && share_start(units, ctas, c) < hi; ++c)
+                plan->start[c] = ChunkStart{b, tile, lo};
+        };
+        const int n = tile_count(a, s);
+        if (n <= 2) {
+            for (int i = 0; i < n; ++i) {
+                const uint64_t x = weight(s, i);
+                starts(b0 + tid, uint32_t(i), from, from + x);
+                from += x;
+            }
+        }
+        uint32_t many = __ballot_sync(~0u, n > 2);
+        while (many) {
+            const int src = __ffs(many) - 1;
+            many &= many - 1;
+            KvSeq o;
+            o.row0 = 0;
+            o.ok = true;
+            o.t = __shfl_sync(~0u, s.t, src);
+            o.n = __shfl_sync(~0u, s.n, src);
+            uint64_t at = __shfl_sync(~0u, from, src);
+            const int tiles = tile_count(a, o);
+            for (int i0 = 0; i0 < tiles; i0 += 32) {
+                const int i = i0 + int(lane);
+                const uint64_t x = i < tiles ? weight(o, i) : 0;
+                uint64_t y = x;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint64_t z = __shfl_up_sync(~0u, y, d);
+                    if (int(lane) >= d) y += z;
+                }
+                if (x > 0) starts(b0 + warp * 32 + uint32_t(src), uint32_t(i), at + y - x, at + y);
+                at += __shfl_sync(~0u, y, 31);
+            }
+        }
+        base += total;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        plan->units = units;
+        plan->ctas = ctas;
+        *a.status = s_bad ? SPLITZIP_ERR_INVALID_ARG : SPLITZIP_OK;
+    }
+}
+
+// FMT 0: cache of the queries' 16-bit type, 1: E5M2, 2: E4M3.
+template <int FMT, bool H, int D>
+struct Chunk {
+    static constexpr bool kFp8 = FMT != 0;
+    static constexpr bool kE5M2 = FMT == 1;
+    // Scores are products in the queries' type, the sums over V in FP16 for an
+    // FP16 cache and else in BF16, which holds FP8 values times their scales.
+    static constexpr bool kPvHalf = !kFp8 && H;
+    // K's scales fold into K in BF16; FP16 has not their range, so there the
+    // scores' columns take them.
+    static constexpr bool kScoreScale = kFp8 && H;
+    // FP16 weights are up to 2^kLag above 2^7, within FP16's range, so that
+    // those down to 2^-28 of the largest are not lost.
+    static constexpr float kShift = kPvHalf ? 7.f : 0.f;
+    static constexpr int kHalves = D / 64;                 // blocks of 64 columns, 128 bytes a row
+    static constexpr int kBlockBytes = 128 * 128;
+    static constexpr int kTileBytes = kHalves * kBlockBytes;
+    static constexpr int kStages = 131072 / kTileBytes;    // K and V tiles, alternating
+    static constexpr int kLagTiles = kFp8 ? 1 : 2;         // copies in flight ahead of their hand-over
+    static constexpr int kRaw = kFp8 ? 2 : 0;              // FP8 staging buffers
+    static constexpr int kRawBytes = 128 * D;
+    static constexpr int kChunks = kFp8 ? D / 16 : D / 8;  // 16-byte pieces of a cache row
+    static constexpr int kRowStep = 128 / kChunks;         // rows that the loaders copy at a time
+    static constexpr int kPartFloats = kTileRows * (D + 2);  // of one group
+
+    struct Shared {
+        uint8_t q[2][kTileBytes];
+        uint8_t stage[kStages][kTileBytes];
+        uint8_t raw[kRaw > 0 ? kRaw : 1][kRaw > 0 ? kRawBytes : 16];
+        int32_t page[2][kUnit];          // of a unit's keys, -1: none
+        uint8_t k_scale[4][kUnit], v_scale[4][kUnit];
+        uint64_t kv_full[kStages], kv_empty[kStages];
+        uint64_t q_full[2], s_full[2], p_full[2], o_full[2], noted, drained;
+        uint32_t tmem, joined[2];
+    };
+    static constexpr int kSmem = int(sizeof(Shared));
+};
+
+// The segments of a CTA's share: part or all of an item.
+struct Walk {
+    uint64_t u, end, group_start, units;
+    uint32_t b, tile, ctas;
+    // of the segment
+    KvSeq s;
+    Tile t;
+    uint32_t head;
+    int first_unit, n;             // of the segment, in units of kUnit positions
+    uint64_t item_start, item_end;
+
+    __device__ __forceinline__ Walk(const ChunkPlan* plan) {
+        units = __ldcg(&plan->units);
+        ctas = __ldcg(&plan->ctas);
+        u = end = group_start = 0;
+        b = tile = 0;
+        if (blockIdx.x < ctas) {
+            u = share_start(units, ctas, blockIdx.x);
+            end = share_start(units, ctas, uint64_t(blockIdx.x) + 1);
+            if (u < end) {
+                b = __ldcg(&plan->start[blockIdx.x].b);
+                tile = __ldcg(&plan->start[blockIdx.x].tile);
+                group_start = __ldcg(&plan->start[blockIdx.x].group_start);
+            }
+        }
+    }
+    __device__ __forceinline__ bool next(const AttentionArgs& a) {
+        if (u >= end) return false;
+        while (true) {
+            s = load_seq(a.b, b);
+            if (int(tile) >= tile_count(a, s)) {
+                ++b;
+                tile = 0;
+                continue;
+            }
+            t = tile_of(a, s, int(tile));
+            const uint64_t size = uint64_t(t.units) * a.c.kv_heads;
+            if (u < group_start + size) break;
+            group_start += size;
+            ++tile;
+        }
+        head = uint32_t((u - group_start) / uint32_t(t.units));
+        item_start = group_start + uint64_t(head) * uint32_t(t.units);
+        item_end = item_start + uint32_t(t.units);
+        const uint64_t stop = min(item_end, end);
+        first_unit = t.keys.lo / kUnit + int(u - item_start);
+        n = int(stop - u);
+        u = stop;
+        return true;
+    }
+    __device__ __forceinline__ bool two() const { return t.rows > kTileRows; }
+    // whether the segment is its whole item
+    __device__ __forceinline__ bool whole() const { return u == item_end && u - uint32_t(n) == item_start; }
+};
+
+template <int FMT, bool H, int D>
+__device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk<FMT, H, D>::Shared& sh,
+                                          const ChunkPlan* plan, bool& ok, bool& bad) {
+    using C = Chunk<FMT, H, D>;
+    const uint32_t lt = threadIdx.x - 256u;
+    const uint32_t c = lt % C::kChunks, r0 = lt / C::kChunks;
+    uint32_t made = 0, handed = 0;  // tiles whose copies were started, and handed over
+
+    const auto await_empty = [&](uint32_t x) {
+        if (x >= uint32_t(C::kStages)) {
+            if (ok) ok = mbar_wait(&sh.kv_empty[x % C::kStages], (x / C::kStages - 1) & 1u);
+        }
+    };
+    // Hands over tile `handed`, whose copies by this thread have landed.
+    const auto hand_over = [&]() {
+        const uint32_t x = handed++, st = x % C::kStages;
+        if (C::kFp8) {
+            await_empty(x);
+            const bool is_v = x & 1u;
+            const uint8_t* scales = (is_v ? sh.v_scale : sh.k_scale)[(x >> 1) & 3u];
+            if (ok) {
+#pragma unroll
+                for (int i = 0; i < C::kChunks; ++i) {
+                    const uint32_t r = r0 + uint32_t(i) * C::kRowStep;
+                    const uint4 y =
+                        *reinterpret_cast<const uint4*>(sh.raw[x % 2] + (uint32_t(i) * 128u + lt) * 16u);
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+                    uint32_t o[8];
+                    if (C::kScoreScale && !is_v) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            o[2 * j] = fp8x2_to_half2<C::kE5M2>(w[j]);
+                            o[2 * j + 1] = fp8x2_to_half2<C::kE5M2>(w[j] >> 16);
+                        }
+                    } else {
+                        // exact: BF16 holds the value and its product with a power of two
+                        const uint32_t s16 = uint32_t(scales[r]) << 7;
+                        const __nv_bfloat162 s2 = __nv_bfloat162(__ushort_as_bfloat16(uint16_t(s16)),
+                                                                 __ushort_as_bfloat16(uint16_t(s16)));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t v = fp8x2_to_bf16x2<C::kE5M2>(w[j / 2] >> (16 * (j & 1)));
+                            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), s2);
+                            o[j] = *reinterpret_cast<const uint32_t*>(&z);
+                        }
+                    }
+                    uint8_t* row = sh.stage[st] + (c >> 2) * C::kBlockBytes + r * 128u;
+                    *reinterpret_cast<uint4*>(row + ((((2u * c) & 7u) ^ (r & 7u)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(row + ((((2u * c + 1u) & 7u) ^ (r & 7u)) << 4)) =
+                        make_uint4(o[4], o[5], o[6], o[7]);
+                }
+            }
+        }
+        fence_async_proxy();
+        mbar_arrive(&sh.kv_full[st]);
+    };
+
+    Walk w(plan);
+    while (w.next(a)) {
+        const int32_t* table = a.b.table + uint64_t(w.b) * a.b.table_stride;
+        const auto page_of = [&](int j) -> int32_t {
+            const int pos = (w.first_unit + j) * kUnit + int(lt);
+            if (j >= w.n || pos < w.t.keys.lo || pos >= w.t.keys.hi) return -1;
+            const int32_t pg = table[uint32_t(pos) >> a.c.page_shift];
+            if (pg < 0 || uint64_t(pg) >= a.c.pool_pages) {
+                bad = true;
+                return -1;
+            }
+            return pg;
+        };
+        const uint32_t slots = (1u << a.c.page_shift) - 1u;
+        int32_t page = page_of(0);
+        for (int j = 0; j < w.n; ++j) {
+            const uint32_t unit = made >> 1;  // of the share
+            const int pos0 = (w.first_unit + j) * kUnit;
+            {
+                sh.page[unit & 1u][lt] = page;
+                if (C::kFp8) {
+                    const uint32_t slot = (uint32_t(pos0) + lt) & slots;
+                    const uint64_t at =
+                        ((uint64_t(uint32_t(page)) * a.c.kv_heads + w.head) << a.c.page_shift) + slot;
+                    sh.k_scale[unit & 3u][lt] = page < 0 ? 127 : a.c.k_scale[at];
+                    sh.v_scale[unit & 3u][lt] = page < 0 ? 127 : a.c.v_scale[at];
+                }
+            }
+            page = page_of(j + 1);
+            named_barrier(1, 128);
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                const uint32_t x = made++;
+                const uint8_t* pool = (side ? a.c.v : a.c.k) + uint64_t(w.head) * a.c.head_stride + c * 16u;
+                if (!C::kFp8) await_empty(x);
+                if (ok) {
+                    const uint32_t dst = C::kFp8 ? smem_u32(sh.raw[x % 2])
+                                                 : smem_u32(sh.stage[x % C::kStages]) + (c >> 3) * C::kBlockBytes;
+#pragma unroll
+                    for (int i = 0; i < C::kChunks; ++i) {
+                        const uint32_t r = r0 + uint32_t(i) * C::kRowStep;
+                        const int32_t pg = sh.page[unit & 1u][r];
+                        const uint8_t* from = pool;
+                        if (pg >= 0)
+                            from += uint64_t(uint32_t(pg)) * a.c.page_stride +
+                                    uint64_t((uint32_t(pos0) + r) & slots) * a.c.token_stride;
+                        const uint32_t to = C::kFp8 ? dst + (uint32_t(i) * 128u + lt) * 16u
+                                                    : dst + r * 128u + (((c & 7u) ^ (r & 7u)) << 4);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                                     "l"(from), "r"(pg < 0 ? 0 : 16)
+                                     : "memory");
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (made > uint32_t(C::kLagTiles)) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(C::kLagTiles) : "memory");
+                    hand_over();
+                }
+            }
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    while (handed < made) hand_over();
+}
+
+template <int FMT, bool H, int D>
+__device__ __forceinline__ void product_role(const AttentionArgs& a, typename Chunk<FMT, H, D>::Shared& sh,
+                                             const ChunkPlan* plan, uint32_t tmem, bool& ok) {
+    using C = Chunk<FMT, H, D>;
+    constexpr uint32_t kShapeS = tc_shape(!H, 128, 128, false);
+    constexpr uint32_t kShapeO = tc_shape(!C::kPvHalf, 128, D, true);
+    uint32_t tile = 0, segments[2] = {0, 0}, weights[2] = {0, 0};
+    const auto await = [&](uint64_t* bar, uint32_t count) {
+        if (ok) ok = mbar_wait(bar, count & 1u);
+        tc_fence_after();
+    };
+    const auto scores = [&](int g, uint32_t st) {
+        if (!ok) return;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = uint32_t(k / 4) * C::kBlockBytes + uint32_t(k % 4) * 32u;
+            tc_mma(tmem + uint32_t(g) * 128u, smem_operand(smem_u32(sh.q[g]) + at, 16, 1024),
+                   smem_operand(smem_u32(sh.stage[st]) + at, 16, 1024), kShapeS, k > 0);
+        }
+        tc_commit(&sh.s_full[g]);
+    };
+    const auto sums = [&](int g, uint32_t st, bool first) {
+        if (!ok) return;
+#pragma unroll
+        for (int k = 0; k < kUnit / 16; ++k)
+            tc_mma_ta(tmem + 256u + uint32_t(g) * 128u, tmem + uint32_t(g) * 128u + uint32_t(k) * 8u,
+                      smem_operand(smem_u32(sh.stage[st]) + uint32_t(k) * 2048u, C::kBlockBytes, 1024), kShapeO,
+                      k > 0 || !first);
+    };
+    Walk w(plan);
+    while (w.next(a)) {
+        const int groups = w.two() ? 2 : 1;
+        for (int j = -1; j < w.n; ++j) {
+            const bool last = j == w.n - 1;
+            // tiles of the ring: K(0) V(0) K(1) V(1) ...
+            const uint32_t v_tile = tile + 2u * uint32_t(j) + 1u, k_tile = tile + 2u * uint32_t(j + 1);
+            for (int g = 0; g < groups; ++g) {
+                if (j >= 0) {
+                    if (g == 0) await(&sh.kv_full[v_tile % C::kStages], v_tile / C::kStages);
+                    await(&sh.p_full[g], weights[g]++);
+                    sums(g, v_tile % C::kStages, j == 0);
+                    if (ok && last) tc_commit(&sh.o_full[g]);
+                    if (ok && g == groups - 1) tc_commit(&sh.kv_empty[v_tile % C::kStages]);
+                }
+                if (!last) {
+                    if (j < 0) await(&sh.q_full[g], segments[g]++);
+                    if (g == 0) await(&sh.kv_full[k_tile % C::kStages], k_tile / C::kStages);
+                    scores(g, k_tile % C::kStages);
+                    if (ok && g == groups - 1) tc_commit(&sh.kv_empty[k_tile % C::kStages]);
+                }
+            }
+        }
+        tile += 2u * uint32_t(w.n);
+    }
+    // no product is in flight when the CTA gives its memory back
+    tc_commit(&sh.drained);
+    if (!mbar_wait(&sh.drained, 0)) ok = false;
+}
+
+template <int FMT, bool H, int D>
+__device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Chunk<FMT, H, D>::Shared& sh,
+                                             const ChunkPlan* plan, uint32_t tmem, bool& ok) {
+    using C = Chunk<FMT, H, D>;
+    const int g = int(threadIdx.x >> 7);
+    const uint32_t row = threadIdx.x & 127u, warp = row >> 5;
+    const uint32_t lanes = (warp * 32u) << 16;
+    const uint32_t s_at = tmem + lanes + uint32_t(g) * 128u, o_at = tmem + lanes + 256u + uint32_t(g) * 128u;
+    const float scale = a.scale_log2;
+    uint32_t segments = 0, units_done = 0, tile = 0, noted = 0;
+    const auto await = [&](uint64_t* bar, uint32_t count) {
+        if (ok) ok = mbar_wait(bar, count & 1u);
+        ok = __all_sync(~0u, ok);
+        tc_fence_after();
+    };
+    Walk w(plan);
+    while (w.next(a)) {
+        const uint32_t first_tile = tile;
+        tile += 2u * uint32_t(w.n);
+        if (g == 1 && !w.two()) continue;
+        const int r = int(row) + g * kTileRows;
+        const bool there = r < w.t.rows;
+        const int i = (w.t.row_first + (there ? r : 0)) / int(a.group);
+        const uint32_t qh = w.head * a.group + uint32_t((w.t.row_first + (there ? r : 0)) % int(a.group));
+        KeyRange see = visible(a, w.s, i);
+        if (!there) see.lo = see.hi = 0;
+        {
+            // the row of Q, zeros where there is none; a negative scale's sign goes to Q
+            const uint4* src = reinterpret_cast<const uint4*>(a.q.d + uint64_t(w.s.row0 + i) * a.q.token_stride +
+                                                              uint64_t(qh) * a.q.head_stride);
+            const uint32_t flip = a.negate ? 0x80008000u : 0u;
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+                uint4 x = there ? src[k] : make_uint4(0, 0, 0, 0);
+                x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+                *reinterpret_cast<uint4*>(sh.q[g] + (k >> 3) * C::kBlockBytes + row * 128u +
+                                          ((uint32_t(k & 7) ^ (row & 7u)) << 4)) = x;
+            }
+            fence_async_proxy();
+            mbar_arrive(&sh.q_full[g]);
+        }
+        float low = -INFINITY;             // what exponentials are taken against, before the scale
+        float sum = 0.f;
+        uint32_t plus[D / 32], minus[D / 32];  // columns of the row that an infinity or a NaN (both) reaches
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) plus[k] = minus[k] = 0;
+        for (int j = 0; j < w.n; ++j) {
+            const int pos0 = (w.first_unit + j) * kUnit;
+            await(&sh.s_full[g], units_done++);
+            uint32_t x[128];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_load32(x + 32 * k, s_at + 32u * uint32_t(k));
+            tmem_wait_load();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_loaded32(x + 32 * k);
+            if (C::kScoreScale) {
+                const uint8_t* ks = sh.k_scale[((first_tile >> 1) + uint32_t(j)) & 3u];
+#pragma unroll
+                for (int k = 0; k < 128; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * scale_value(ks[k]));
+            }
+            const int from = see.lo - pos0, to = see.hi - pos0;
+            const bool all = from <= 0 && to >= kUnit;
+            if (!__all_sync(~0u, all)) {
+#pragma unroll
+                for (int k = 0; k < 128; ++k)
+                    if (k < from || k >= to) x[k] = 0xFF800000u;
+            }
+            float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 128; k += 8) {
+                m0 = fmaxf(fmaxf(m0, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+                m1 = fmaxf(fmaxf(m1, __uint_as_float(x[k + 2])), __uint_as_float(x[k + 3]));
+                m2 = fmaxf(fmaxf(m2, __uint_as_float(x[k + 4])), __uint_as_float(x[k + 5]));
+                m3 = fmaxf(fmaxf(m3, __uint_as_float(x[k + 6])), __uint_as_float(x[k + 7]));
+            }
+            const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+            const bool grew = top > low + a.lag;
+            if (__any_sync(~0u, grew)) {
+                // S(j) done means that the product before it is: o can be rescaled
+                const float f = grew ? exp2_fast((low - top) * scale) : 1.f;
+                if (grew) low = top;
+                sum *= f;
+                if (j > 0) {
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t o[32];
+                        tmem_load32(o, o_at + 32u * uint32_t(k));
+                        tmem_wait_load();
+                        tmem_loaded32(o);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tmem_store32(o_at + 32u * uint32_t(k), o);
+                    }
+                }
+            }
+            const float ref = C::kShift - (low == -INFINITY ? 0.f : low * scale);
+            const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
+            float2 part[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+            uint32_t p[64];
+#pragma unroll
+            for (int k = 0; k < 64; ++k) {
+                const float2 y =
+                    fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2, ref2);
+                const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                part[k & 3] = add2(part[k & 3], e);
+                p[k] = C::kPvHalf ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                if ((k & 31) == 31) tmem_store32(s_at + uint32_t(k - 31), p + k - 31);
+            }
+            part[0] = add2(add2(part[0], part[1]), add2(part[2], part[3]));
+            sum += part[0].x + part[0].y;
+
+            // A weight of 0 hides a finite value of V, not an infinity or a NaN: where
+            // some row of the item does not see all of this unit's keys, such values
+            // are noted for the rows that see them and taken out of V.
+            const int k0 = max(pos0, w.t.keys.lo), k1 = min(pos0 + kUnit, w.t.keys.hi);
+            const int i_last = (w.t.row_first + w.t.rows - 1) / int(a.group);
+            const KeyRange first_row = visible(a, w.s, w.t.row_first / int(a.group));
+            const KeyRange last_row = visible(a, w.s, i_last);
+            const bool partial = k0 < k1 && (first_row.hi < k1 || last_row.lo > k0);
+            if (partial) {  // the same in all rows' threads
+                const uint32_t v_tile = first_tile + 2u * uint32_t(j) + 1u, st = v_tile % C::kStages;
+                if (ok) ok = mbar_wait(&sh.kv_full[st], (v_tile / C::kStages) & 1u);
+                uint8_t* v = sh.stage[st];
+                bool special = false;
+#pragma unroll 4
+                for (int k = 0; k < C::kTileBytes / 2048; ++k) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(v + (uint32_t(k) * 128u + row) * 16u);
+                    constexpr uint32_t kInf = C::kPvHalf ? 0x7C00u : 0x7F80u;
+                    const uint32_t z = __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
+                                                __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
+                    special |= (z & 0xFFFFu) >= kInf || (z >> 16) >= kInf;
+                }
+                if (named_barrier_popc(2 + uint32_t(g), 128, special) > 0) {
+                    // both groups found the same
+                    constexpr uint32_t kInf = C::kPvHalf ? 0x7C00u : 0x7F80u;
+                    for (int key = 0; key < kUnit; ++key) {
+                        const bool sees = pos0 + key >= see.lo && pos0 + key < see.hi;
+#pragma unroll
+                        for (int k = 0; k < D / 2; ++k) {
+                            const uint32_t y = *reinterpret_cast<const uint32_t*>(
+                                v + (k >> 5) * C::kBlockBytes + key * 128 + ((((k >> 2) & 7) ^ (key & 7)) << 4) +
+                                (k & 3) * 4);
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t bits = (y >> (16 * z)) & 0xFFFFu, mag = bits & 0x7FFFu;
+                                const uint32_t at = uint32_t(2 * k + z);
+                                if (mag >= kInf && sees) {
+                                    if (mag > kInf || !(bits & 0x8000u)) plus[at >> 5] |= 1u << (at & 31u);
+                                    if (mag > kInf || (bits & 0x8000u)) minus[at >> 5] |= 1u << (at & 31u);
+                                }
+                            }
+                        }
+                    }
+                    // group 0 takes them out once both have noted them; group 1's product
+                    // is issued after group 0's
+                    if (g == 1) mbar_arrive(&sh.noted);
+                    if (g == 0 && w.two() && ok) ok = mbar_wait(&sh.noted, noted++ & 1u);
+                    if (g == 0 && ok) {
+                        for (int k = 0; k < C::kTileBytes / 512; ++k) {
+                            uint32_t* at = reinterpret_cast<uint32_t*>(v) + uint32_t(k) * 128u + row;
+                            uint32_t y = *at;
+                            if ((y & 0x7FFFu) >= kInf) y &= 0xFFFF0000u;
+                            if (((y >> 16) & 0x7FFFu) >= kInf) y &= 0x0000FFFFu;
+                            *at = y;
+                        }
+                        fence_async_proxy();
+                    }
+                }
+            }
+            tmem_wait_store();
+            tc_fence_before();
+            if (ok) mbar_arrive(&sh.p_full[g]);
+        }
+
+        // the segment's sums
+        await(&sh.o_full[g], segments++);
+        const bool whole = w.whole();
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t* dst = a.out.d + uint64_t(w.s.row0 + i) * a.out.token_stride + uint64_t(qh) * a.out.head_stride;
+        const uint32_t first = whole ? 0u : share_of(w.units, w.ctas, w.item_start);
+        const uint32_t last = whole ? 0u : share_of(w.units, w.ctas, w.item_end - 1);
+        const auto slot = [&](uint32_t cta) {
+            return a.parts + ((uint64_t(cta) * 2 + (cta == first ? 1 : 0)) * 2 + uint32_t(g)) * C::kPartFloats;
+        };
+        float* mine = whole ? nullptr : slot(blockIdx.x);
+        const auto put = [&](int k, const float* o, float f) {  // 32 columns of the result
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                uint32_t z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[e] = H ? pack_half2(o[8 * y + 2 * e] * f, o[8 * y + 2 * e + 1] * f)
+                             : pack_bf16x2(o[8 * y + 2 * e] * f, o[8 * y + 2 * e + 1] * f);
+                if (there)
+                    *reinterpret_cast<uint4*>(dst + 32 * k + 8 * y) = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+        };
+        const auto put_lse = [&](float m, float l) {
+            if (a.lse && there)
+                a.lse[uint64_t(w.s.row0 + i) * a.q_heads + qh] =
+                    l == 0.f ? -INFINITY : (m * scale - C::kShift + log2f(l)) * 0.693147180559945309f;
+        };
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            uint32_t bits[32];
+            float o[32];
+            tmem_load32(bits, o_at + 32u * uint32_t(k));
+            tmem_wait_load();
+            tmem_loaded32(bits);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) {
+                o[y] = __uint_as_float(bits[y]);
+                if (plus[k] >> y & 1u) o[y] += INFINITY;
+                if (minus[k] >> y & 1u) o[y] += -INFINITY;
+            }
+            if (whole) {
+                put(k, o, inv);
+            } else {
+#pragma unroll
+                for (int y = 0; y < 32; ++y) mine[(32 * k + y) * kTileRows + int(row)] = o[y];
+            }
+        }
+        if (whole) {
+            put_lse(low == -INFINITY ? 0.f : low, sum);
+        } else {
+            mine[D * kTileRows + int(row)] = low;
+            mine[(D + 1) * kTileRows + int(row)] = sum;
+            __threadfence();
+            named_barrier(2 + uint32_t(g), 128);
+            if (row == 0) sh.joined[g] = atomicAdd(a.counters + 2 * first + uint32_t(g), 1u) == last - first;
+            named_barrier(2 + uint32_t(g), 128);
+            if (sh.joined[g]) {
+                __threadfence();
+                float m = -INFINITY, l = 0.f;
+                for (uint32_t cta = first; cta <= last; ++cta)
+                    m = fmaxf(m, __ldcg(slot(cta) + D * kTileRows + row));
+                for (uint32_t cta = first; cta <= last; ++cta) {
+                    const float* part = slot(cta);
+                    const float mc = __ldcg(part + D * kTileRows + row);
+                    l += (mc == m ? 1.f : exp2_fast((mc - m) * scale)) * __ldcg(part + (D + 1) * kTileRows + row);
+                }
+                const float joined = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = 0.f;
+                    for (uint32_t cta = first; cta <= last; ++cta) {
+                        const float* part = slot(cta);
+                        const float mc = __ldcg(part + D * kTileRows + row);
+                        const float f = mc == m ? 1.f : exp2_fast((mc - m) * scale);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] += f * __ldcg(part + (32 * k + y) * kTileRows + row);
+                    }
+                    put(k, o, joined);
+                }
+                put_lse(m == -INFINITY ? 0.f : m, l);
+            }
+        }
+        // the loads of O are done before the next segment's product overwrites it
+        tc_fence_before();
+    }
+}
+
+template <int FMT, bool H, int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_constant__ AttentionArgs a,
+                                                               const ChunkPlan* plan) {
+    using C = Chunk<FMT, H, D>;
+    extern __shared__ __align__(1024) uint8_t smem_chunk[];  // the swizzle goes by address bits below 1024
+    auto& sh = *reinterpret_cast<typename C::Shared*>(smem_chunk);
+    const uint32_t warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&sh.kv_full[i], 128);
+            mbar_init(&sh.kv_empty[i], 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&sh.q_full[g], 128);
+            mbar_init(&sh.s_full[g], 1);
+            mbar_init(&sh.p_full[g], 128);
+            mbar_init(&sh.o_full[g], 1);
+        }
+        mbar_init(&sh.noted, 128);
+        mbar_init(&sh.drained, 1);
+        mbar_init_fence();
+    }
+    if (warp == 12) tmem_alloc(smem_u32(&sh.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    wait_predecessor();  // the plan is written, counters and status clear
+    bool ok = true, bad = false;
+    // registers of the launch: 512 threads of 128; 2 * 184 + 80 + 64 = 4 * 128
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        softmax_role<FMT, H, D>(a, sh, plan, tmem, ok);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        load_role<FMT, H, D>(a, sh, plan, ok, bad);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (threadIdx.x == 12 * 32) product_role<FMT, H, D>(a, sh, plan, tmem, ok);
+    }
+    if (bad) report(a.status, SPLITZIP_ERR_INVALID_ARG);
+    if (!ok) report(a.status, SPLITZIP_ERR_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+template <int FMT, bool H, int D>
+int launch(const AttentionArgs& a, ChunkPlan* plan, uint32_t ctas, cudaStream_t s) {
+    using C = Chunk<FMT, H, D>;
+    static_assert(C::kSmem <= 232448, "shared memory of a CTA");
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SPLITZIP_ERR_CUDA;
+    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1u)) {
+        if (cudaFuncSetAttribute(kv_chunk_kernel<FMT, H, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return SPLITZIP_ERR_CUDA;
+        }
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
+    }
+    ChainedLaunch l(dim3(ctas), dim3(kThreads), C::kSmem, s);
+    if (cudaLaunchKernelEx(&l.cfg, kv_chunk_kernel<FMT, H, D>, a, static_cast<const ChunkPlan*>(plan)) != cudaSuccess) {
+        cudaGetLastError();
+        return SPLITZIP_ERR_CUDA;
+    }
+    return SPLITZIP_OK;
+}
+
+template <int FMT, bool H>
+int launch_dim(const AttentionArgs& a, ChunkPlan* plan, uint32_t ctas, cudaStream_t s) {
+    return a.c.head_dim == 128 ? launch<FMT, H, 128>(a, plan, ctas, s) : launch<FMT, H, 64>(a, plan, ctas, s);
+}
+
+}  // namespace
+
+uint32_t chunk_ctas(uint64_t rows, uint64_t batch, uint64_t kv_heads, uint64_t keys_max) {
+    const uint64_t tiles = std::min<uint64_t>((rows + kRows - 1) / kRows + batch, rows);
+    const uint64_t units = tiles * kv_heads * ((keys_max + kUnit - 1) / kUnit + 1);
+    return uint32_t(std::min<uint64_t>(kChunkCtas, std::max<uint64_t>(1, units)));
+}
+
+uint64_t chunk_part_floats(uint32_t head_dim) { return uint64_t(kRows) * (head_dim + 2); }
+
+uint64_t chunk_plan_bytes(uint32_t ctas) { return sizeof(ChunkPlan) + uint64_t(ctas) * sizeof(ChunkStart); }
+
+int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan_at, uint32_t ctas, cudaStream_t s) {
+    ChunkPlan* plan = static_cast<ChunkPlan*>(plan_at);
+    kv_chunk_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, plan, ctas);
+    if (cudaGetLastError() != cudaSuccess) return SPLITZIP_ERR_CUDA;
+    switch (a.c.type) {
+        case SPLITZIP_KV_FP8_E5M2:
+            return q_half ? launch_dim<1, true>(a, plan, ctas, s) : launch_dim<1, false>(a, plan, ctas, s);
+        case SPLITZIP_KV_FP8_E4M3:
+            return q_half ? launch_dim<2, true>(a, plan, ctas, s) : launch_dim<2, false>(a, plan, ctas, s);
+        default: return q_half ? launch_dim<0, true>(a, plan, ctas, s) : launch_dim<0, false>(a, plan, ctas, s);
+    }
+}
+
+}  // namespace splitzip
