@@ -17,7 +17,8 @@
 //              memory (cp.async for a 16-bit cache; FP8 by way of a staging
 //              buffer, converted by the thread that copied it), rows past the
 //              end as zeros
-//   12         one thread issues the products, in the order
+//   13         one thread walks the CTA's share and describes its pieces
+//   12         issues the products, in the order
 //              S0(j+1) | P1(j) V(j) | S1(j+1) | P0(j+1) V(j+1) | ...
 //              so that each tile's softmax runs under the other's products
 // TMEM: S0, S1 (128 columns each, the weights overwrite the scores), O0, O1.
@@ -29,6 +30,7 @@
 // is still reached, and SPLITZIP_ERR_TIMEOUT is reported.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kv_attention.cuh"
 #include "tma_pipeline.cuh"
@@ -207,6 +209,18 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     }
 }
 
+// One piece of a CTA's share: part or all of an item.
+struct Segment {
+    int row0, t, held;         // of the sequence: first packed row, new tokens, tokens held
+    int row_first, rows;       // of the item: rows of the sequence
+    int lo, hi;                // positions that some row of the item sees
+    int first_unit, n;         // the piece's units; n = 0: no more pieces
+    uint32_t b, head;
+    uint32_t first_cta, last_cta;  // whose shares the item is in
+};
+
+constexpr int kSegments = 4;  // ring of pieces
+
 // FMT 0: cache of the queries' 16-bit type, 1: E5M2, 2: E4M3.
 template <int FMT, bool H, int D>
 struct Chunk {
@@ -236,73 +250,79 @@ struct Chunk {
         uint8_t q[2][kTileBytes];
         uint8_t stage[kStages][kTileBytes];
         uint8_t raw[kRaw > 0 ? kRaw : 1][kRaw > 0 ? kRawBytes : 16];
-        int32_t page[2][kUnit];          // of a unit's keys, -1: none
+        // of a unit's keys: byte offset in the pools, or page (FP8, which has no room); -1: none
+        std::conditional_t<kFp8, int32_t, int64_t> place[2][kUnit];
         uint8_t k_scale[4][kUnit], v_scale[4][kUnit];
         uint64_t kv_full[kStages], kv_empty[kStages];
         uint64_t q_full[2], s_full[2], p_full[2], o_full[2], noted, drained;
+        uint64_t seg_full[kSegments], seg_empty[kSegments];
         uint32_t tmem, joined[2];
+        Segment seg[kSegments];
     };
     static constexpr int kSmem = int(sizeof(Shared));
 };
 
-// The segments of a CTA's share: part or all of an item.
-struct Walk {
-    uint64_t u, end, group_start, units;
-    uint32_t b, tile, ctas;
-    // of the segment
-    KvSeq s;
-    Tile t;
-    uint32_t head;
-    int first_unit, n;             // of the segment, in units of kUnit positions
-    uint64_t item_start, item_end;
-
-    __device__ __forceinline__ Walk(const ChunkPlan* plan) {
-        units = __ldcg(&plan->units);
-        ctas = __ldcg(&plan->ctas);
-        u = end = group_start = 0;
-        b = tile = 0;
-        if (blockIdx.x < ctas) {
-            u = share_start(units, ctas, blockIdx.x);
-            end = share_start(units, ctas, uint64_t(blockIdx.x) + 1);
-            if (u < end) {
-                b = __ldcg(&plan->start[blockIdx.x].b);
-                tile = __ldcg(&plan->start[blockIdx.x].tile);
-                group_start = __ldcg(&plan->start[blockIdx.x].group_start);
-            }
+// Walks the CTA's share and describes its pieces to the other roles (one
+// thread, ahead of them by up to kSegments).
+template <class Shared>
+__device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh, const ChunkPlan* plan, bool& ok) {
+    const uint64_t units = __ldcg(&plan->units);
+    const uint32_t ctas = __ldcg(&plan->ctas);
+    uint64_t u = 0, end = 0, group_start = 0;
+    uint32_t b = 0, tile = 0;
+    if (blockIdx.x < ctas) {
+        u = share_start(units, ctas, blockIdx.x);
+        end = share_start(units, ctas, uint64_t(blockIdx.x) + 1);
+        if (u < end) {
+            b = __ldcg(&plan->start[blockIdx.x].b);
+            tile = __ldcg(&plan->start[blockIdx.x].tile);
+            group_start = __ldcg(&plan->start[blockIdx.x].group_start);
         }
     }
-    __device__ __forceinline__ bool next(const AttentionArgs& a) {
-        if (u >= end) return false;
-        while (true) {
-            s = load_seq(a.b, b);
-            if (int(tile) >= tile_count(a, s)) {
-                ++b;
-                tile = 0;
-                continue;
+    for (uint32_t i = 0; ok; ++i) {
+        if (i >= uint32_t(kSegments)) ok = mbar_wait(&sh.seg_empty[i % kSegments], (i / kSegments - 1) & 1u);
+        if (!ok) break;
+        Segment g{};
+        const bool more = u < end;
+        if (more) {
+            KvSeq s;
+            Tile t;
+            while (true) {
+                s = load_seq(a.b, b);
+                if (int(tile) >= tile_count(a, s)) {
+                    ++b;
+                    tile = 0;
+                    continue;
+                }
+                t = tile_of(a, s, int(tile));
+                const uint64_t size = uint64_t(t.units) * a.c.kv_heads;
+                if (u < group_start + size) break;
+                group_start += size;
+                ++tile;
             }
-            t = tile_of(a, s, int(tile));
-            const uint64_t size = uint64_t(t.units) * a.c.kv_heads;
-            if (u < group_start + size) break;
-            group_start += size;
-            ++tile;
+            const uint32_t head = uint32_t((u - group_start) / uint32_t(t.units));
+            const uint64_t item_start = group_start + uint64_t(head) * uint32_t(t.units);
+            const uint64_t item_end = item_start + uint32_t(t.units);
+            const uint64_t stop = min(item_end, end);
+            g.row0 = s.row0, g.t = s.t, g.held = s.n;
+            g.row_first = t.row_first, g.rows = t.rows;
+            g.lo = t.keys.lo, g.hi = t.keys.hi;
+            g.first_unit = t.keys.lo / kUnit + int(u - item_start);
+            g.n = int(stop - u);
+            g.b = b, g.head = head;
+            g.first_cta = share_of(units, ctas, item_start);
+            g.last_cta = share_of(units, ctas, item_end - 1);
+            u = stop;
         }
-        head = uint32_t((u - group_start) / uint32_t(t.units));
-        item_start = group_start + uint64_t(head) * uint32_t(t.units);
-        item_end = item_start + uint32_t(t.units);
-        const uint64_t stop = min(item_end, end);
-        first_unit = t.keys.lo / kUnit + int(u - item_start);
-        n = int(stop - u);
-        u = stop;
-        return true;
+        sh.seg[i % kSegments] = g;
+        mbar_arrive(&sh.seg_full[i % kSegments]);
+        if (!more) break;
     }
-    __device__ __forceinline__ bool two() const { return t.rows > kTileRows; }
-    // whether the segment is its whole item
-    __device__ __forceinline__ bool whole() const { return u == item_end && u - uint32_t(n) == item_start; }
-};
+}
 
 template <int FMT, bool H, int D>
 __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk<FMT, H, D>::Shared& sh,
-                                          const ChunkPlan* plan, bool& ok, bool& bad) {
+                                          bool& ok, bool& bad) {
     using C = Chunk<FMT, H, D>;
     const uint32_t lt = threadIdx.x - 256u;
     const uint32_t c = lt % C::kChunks, r0 = lt / C::kChunks;
@@ -358,12 +378,15 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
         mbar_arrive(&sh.kv_full[st]);
     };
 
-    Walk w(plan);
-    while (w.next(a)) {
+    for (uint32_t piece = 0;; ++piece) {
+        const Segment& w = sh.seg[piece % kSegments];
+        if (ok) ok = mbar_wait(&sh.seg_full[piece % kSegments], (piece / kSegments) & 1u);
+        ok = named_barrier_and(1, 128, ok);
+        if (!ok || w.n == 0) break;
         const int32_t* table = a.b.table + uint64_t(w.b) * a.b.table_stride;
         const auto page_of = [&](int j) -> int32_t {
             const int pos = (w.first_unit + j) * kUnit + int(lt);
-            if (j >= w.n || pos < w.t.keys.lo || pos >= w.t.keys.hi) return -1;
+            if (j >= w.n || pos < w.lo || pos >= w.hi) return -1;
             const int32_t pg = table[uint32_t(pos) >> a.c.page_shift];
             if (pg < 0 || uint64_t(pg) >= a.c.pool_pages) {
                 bad = true;
@@ -377,9 +400,13 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
             const uint32_t unit = made >> 1;  // of the share
             const int pos0 = (w.first_unit + j) * kUnit;
             {
-                sh.page[unit & 1u][lt] = page;
-                if (C::kFp8) {
-                    const uint32_t slot = (uint32_t(pos0) + lt) & slots;
+                const uint32_t slot = (uint32_t(pos0) + lt) & slots;
+                if (!C::kFp8) {
+                    sh.place[unit & 1u][lt] = page < 0 ? -1
+                                                       : int64_t(uint64_t(uint32_t(page)) * a.c.page_stride +
+                                                                 uint64_t(slot) * a.c.token_stride);
+                } else {
+                    sh.place[unit & 1u][lt] = page;
                     const uint64_t at =
                         ((uint64_t(uint32_t(page)) * a.c.kv_heads + w.head) << a.c.page_shift) + slot;
                     sh.k_scale[unit & 3u][lt] = page < 0 ? 127 : a.c.k_scale[at];
@@ -397,18 +424,24 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
                     const uint32_t dst = C::kFp8 ? smem_u32(sh.raw[x % 2])
                                                  : smem_u32(sh.stage[x % C::kStages]) + (c >> 3) * C::kBlockBytes;
 #pragma unroll
-                    for (int i = 0; i < C::kChunks; ++i) {
-                        const uint32_t r = r0 + uint32_t(i) * C::kRowStep;
-                        const int32_t pg = sh.page[unit & 1u][r];
-                        const uint8_t* from = pool;
-                        if (pg >= 0)
-                            from += uint64_t(uint32_t(pg)) * a.c.page_stride +
-                                    uint64_t((uint32_t(pos0) + r) & slots) * a.c.token_stride;
-                        const uint32_t to = C::kFp8 ? dst + (uint32_t(i) * 128u + lt) * 16u
-                                                    : dst + r * 128u + (((c & 7u) ^ (r & 7u)) << 4);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
-                                     "l"(from), "r"(pg < 0 ? 0 : 16)
-                                     : "memory");
+                    for (int i0 = 0; i0 < C::kChunks; i0 += 8) {
+                        // all places first: the copies are barriers to the compiler
+                        int64_t pl[8];
+#pragma unroll
+                        for (int i = 0; i < 8 && i0 + i < C::kChunks; ++i)
+                            pl[i] = sh.place[unit & 1u][r0 + uint32_t(i0 + i) * C::kRowStep];
+#pragma unroll
+                        for (int i = 0; i < 8 && i0 + i < C::kChunks; ++i) {
+                            const uint32_t r = r0 + uint32_t(i0 + i) * C::kRowStep;
+                            uint64_t off = uint64_t(max(pl[i], int64_t(0)));
+                            if (C::kFp8)
+                                off = off * a.c.page_stride + uint64_t((uint32_t(pos0) + r) & slots) * a.c.token_stride;
+                            const uint32_t to = C::kFp8 ? dst + (uint32_t(i0 + i) * 128u + lt) * 16u
+                                                        : dst + r * 128u + (((c & 7u) ^ (r & 7u)) << 4);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(pool + off),
+                                         "r"(pl[i] < 0 ? 0 : 16)
+                                         : "memory");
+                        }
                     }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
@@ -418,117 +451,192 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
                 }
             }
         }
+        __syncwarp();
+        if ((lt & 31u) == 0) mbar_arrive(&sh.seg_empty[piece % kSegments]);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     while (handed < made) hand_over();
 }
 
+// One warp, converged, so that operand descriptors stay in uniform registers;
+// one elected lane issues.
 template <int FMT, bool H, int D>
-__device__ __forceinline__ void product_role(const AttentionArgs& a, typename Chunk<FMT, H, D>::Shared& sh,
-                                             const ChunkPlan* plan, uint32_t tmem, bool& ok) {
+__device__ __forceinline__ void product_role(typename Chunk<FMT, H, D>::Shared& sh, uint32_t tmem, bool& ok) {
     using C = Chunk<FMT, H, D>;
     constexpr uint32_t kShapeS = tc_shape(!H, 128, 128, false);
     constexpr uint32_t kShapeO = tc_shape(!C::kPvHalf, 128, D, true);
+    const uint64_t q_operand = smem_operand(smem_u32(sh.q[0]), 16, 1024);
+    const uint64_t k_operand = smem_operand(smem_u32(sh.stage[0]), 16, 1024);
+    const uint64_t v_operand = smem_operand(smem_u32(sh.stage[0]), C::kBlockBytes, 1024);
+    constexpr uint32_t kTileStep = C::kTileBytes >> 4;  // in the descriptors' units
     uint32_t tile = 0, segments[2] = {0, 0}, weights[2] = {0, 0};
     const auto await = [&](uint64_t* bar, uint32_t count) {
         if (ok) ok = mbar_wait(bar, count & 1u);
+        ok = __all_sync(~0u, ok);
         tc_fence_after();
     };
-    const auto scores = [&](int g, uint32_t st) {
-        if (!ok) return;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = uint32_t(k / 4) * C::kBlockBytes + uint32_t(k % 4) * 32u;
-            tc_mma(tmem + uint32_t(g) * 128u, smem_operand(smem_u32(sh.q[g]) + at, 16, 1024),
-                   smem_operand(smem_u32(sh.stage[st]) + at, 16, 1024), kShapeS, k > 0);
-        }
-        tc_commit(&sh.s_full[g]);
-    };
-    const auto sums = [&](int g, uint32_t st, bool first) {
-        if (!ok) return;
-#pragma unroll
-        for (int k = 0; k < kUnit / 16; ++k)
-            tc_mma_ta(tmem + 256u + uint32_t(g) * 128u, tmem + uint32_t(g) * 128u + uint32_t(k) * 8u,
-                      smem_operand(smem_u32(sh.stage[st]) + uint32_t(k) * 2048u, C::kBlockBytes, 1024), kShapeO,
-                      k > 0 || !first);
-    };
-    Walk w(plan);
-    while (w.next(a)) {
-        const int groups = w.two() ? 2 : 1;
-        for (int j = -1; j < w.n; ++j) {
-            const bool last = j == w.n - 1;
+    for (uint32_t piece = 0;; ++piece) {
+        await(&sh.seg_full[piece % kSegments], piece / kSegments);
+        const int n = ok ? sh.seg[piece % kSegments].n : 0;
+        if (n == 0) break;
+        const int groups = sh.seg[piece % kSegments].rows > kTileRows ? 2 : 1;
+        __syncwarp();
+        if (elect_lane()) mbar_arrive(&sh.seg_empty[piece % kSegments]);
+        for (int j = -1; j < n; ++j) {
+            const bool last = j == n - 1;
             // tiles of the ring: K(0) V(0) K(1) V(1) ...
             const uint32_t v_tile = tile + 2u * uint32_t(j) + 1u, k_tile = tile + 2u * uint32_t(j + 1);
-            for (int g = 0; g < groups; ++g) {
+            const uint32_t v_stage = v_tile % C::kStages, k_stage = k_tile % C::kStages;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (g >= groups) break;
                 if (j >= 0) {
-                    if (g == 0) await(&sh.kv_full[v_tile % C::kStages], v_tile / C::kStages);
+                    if (g == 0) await(&sh.kv_full[v_stage], v_tile / C::kStages);
                     await(&sh.p_full[g], weights[g]++);
-                    sums(g, v_tile % C::kStages, j == 0);
-                    if (ok && last) tc_commit(&sh.o_full[g]);
-                    if (ok && g == groups - 1) tc_commit(&sh.kv_empty[v_tile % C::kStages]);
+                    if (ok && elect_lane()) {
+                        const uint64_t v = v_operand + v_stage * kTileStep;
+#pragma unroll
+                        for (int k = 0; k < kUnit / 16; ++k)
+                            tc_mma_ta(tmem + 256u + uint32_t(g) * 128u, tmem + uint32_t(g) * 128u + uint32_t(k) * 8u,
+                                      v + uint32_t(k) * (2048u >> 4), kShapeO, k > 0 || j > 0);
+                        if (last) tc_commit(&sh.o_full[g]);
+                        if (g == groups - 1) tc_commit(&sh.kv_empty[v_stage]);
+                    }
+                    __syncwarp();
                 }
                 if (!last) {
                     if (j < 0) await(&sh.q_full[g], segments[g]++);
-                    if (g == 0) await(&sh.kv_full[k_tile % C::kStages], k_tile / C::kStages);
-                    scores(g, k_tile % C::kStages);
-                    if (ok && g == groups - 1) tc_commit(&sh.kv_empty[k_tile % C::kStages]);
+                    if (g == 0) await(&sh.kv_full[k_stage], k_tile / C::kStages);
+                    if (ok && elect_lane()) {
+                        const uint64_t q = q_operand + uint32_t(g) * kTileStep, kk = k_operand + k_stage * kTileStep;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            constexpr uint32_t kBlock = C::kBlockBytes >> 4;
+                            const uint32_t at = uint32_t(k / 4) * kBlock + uint32_t(k % 4) * 2u;
+                            tc_mma(tmem + uint32_t(g) * 128u, q + at, kk + at, kShapeS, k > 0);
+                        }
+                        tc_commit(&sh.s_full[g]);
+                        if (g == groups - 1) tc_commit(&sh.kv_empty[k_stage]);
+                    }
+                    __syncwarp();
                 }
             }
         }
-        tile += 2u * uint32_t(w.n);
+        tile += 2u * uint32_t(n);
     }
     // no product is in flight when the CTA gives its memory back
-    tc_commit(&sh.drained);
+    if (elect_lane()) tc_commit(&sh.drained);
+    __syncwarp();
     if (!mbar_wait(&sh.drained, 0)) ok = false;
+}
+
+// Columns of a row that an infinity or a NaN (both) of V reaches.
+template <int D>
+struct Reached {
+    uint32_t plus[D / 32], minus[D / 32];
+};
+
+// Notes the infinities and NaN of a V tile for a row that sees its keys
+// from .. to - 1.  Out of line: it hardly ever runs, and its registers are not
+// to weigh on the loop around it.
+template <bool H, int D>
+__device__ __noinline__ void note_special(const uint8_t* v, int from, int to, Reached<D>* reached) {
+    constexpr uint32_t kInf = H ? 0x7C00u : 0x7F80u;
+    for (int key = 0; key < kUnit; ++key) {
+        const bool sees = key >= from && key < to;
+        for (int k = 0; k < D / 2; ++k) {
+            const uint32_t y = *reinterpret_cast<const uint32_t*>(
+                v + (k >> 5) * (128 * 128) + key * 128 + ((((k >> 2) & 7) ^ (key & 7)) << 4) + (k & 3) * 4);
+            for (int z = 0; z < 2; ++z) {
+                const uint32_t bits = (y >> (16 * z)) & 0xFFFFu, mag = bits & 0x7FFFu, at = uint32_t(2 * k + z);
+                if (mag >= kInf && sees) {
+                    if (mag > kInf || !(bits & 0x8000u)) reached->plus[at >> 5] |= 1u << (at & 31u);
+                    if (mag > kInf || (bits & 0x8000u)) reached->minus[at >> 5] |= 1u << (at & 31u);
+                }
+            }
+        }
+    }
 }
 
 template <int FMT, bool H, int D>
 __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Chunk<FMT, H, D>::Shared& sh,
-                                             const ChunkPlan* plan, uint32_t tmem, bool& ok) {
+                                             uint32_t tmem, bool& ok) {
     using C = Chunk<FMT, H, D>;
     const int g = int(threadIdx.x >> 7);
-    const uint32_t row = threadIdx.x & 127u, warp = row >> 5;
+    const uint32_t row = threadIdx.x & 127u, lane = threadIdx.x & 31u, warp = row >> 5;
     const uint32_t lanes = (warp * 32u) << 16;
     const uint32_t s_at = tmem + lanes + uint32_t(g) * 128u, o_at = tmem + lanes + 256u + uint32_t(g) * 128u;
     const float scale = a.scale_log2;
+    // A row of 16-bit elements is kLanes 16-byte pieces; a warp moves kMoves of
+    // them for each of its rows, so that its accesses to memory are whole rows.
+    constexpr uint32_t kLanes = D / 8;
+    constexpr int kMoves = int(kLanes);
+    const uint32_t piece_col = lane % kLanes, piece_row = lane / kLanes;
+    // a row's piece in the group's part of sh.q, in the swizzle of the operands
+    const auto staged = [&](uint32_t r, uint32_t c) {
+        return reinterpret_cast<uint4*>(sh.q[g] + (c >> 3) * C::kBlockBytes + r * 128u + (((c & 7u) ^ (r & 7u)) << 4));
+    };
     uint32_t segments = 0, units_done = 0, tile = 0, noted = 0;
     const auto await = [&](uint64_t* bar, uint32_t count) {
         if (ok) ok = mbar_wait(bar, count & 1u);
         ok = __all_sync(~0u, ok);
         tc_fence_after();
     };
-    Walk w(plan);
-    while (w.next(a)) {
+    for (uint32_t piece = 0;; ++piece) {
+        const Segment& w = sh.seg[piece % kSegments];
+        if (ok) ok = mbar_wait(&sh.seg_full[piece % kSegments], (piece / kSegments) & 1u);
+        ok = named_barrier_and(2 + uint32_t(g), 128, ok);
+        if (!ok || w.n == 0) break;
+        const auto leave = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.seg_empty[piece % kSegments]);
+        };
+        const int n = w.n;
         const uint32_t first_tile = tile;
-        tile += 2u * uint32_t(w.n);
-        if (g == 1 && !w.two()) continue;
-        const int r = int(row) + g * kTileRows;
-        const bool there = r < w.t.rows;
-        const int i = (w.t.row_first + (there ? r : 0)) / int(a.group);
-        const uint32_t qh = w.head * a.group + uint32_t((w.t.row_first + (there ? r : 0)) % int(a.group));
-        KeyRange see = visible(a, w.s, i);
-        if (!there) see.lo = see.hi = 0;
+        tile += 2u * uint32_t(n);
+        if (g == 1 && w.rows <= kTileRows) {
+            leave();
+            continue;
+        }
+        // the thread's row: its packed row and head, -1 where there is none
+        const auto place = [&](const KvRows& rows) -> int64_t {
+            const int r = w.row_first + int(row) + g * kTileRows;  // of the sequence
+            if (r >= w.row_first + w.rows) return -1;
+            const int i = r / int(a.group);
+            return int64_t(uint64_t(w.row0 + i) * rows.token_stride +
+                           uint64_t(w.head * a.group + uint32_t(r - i * int(a.group))) * rows.head_stride);
+        };
+        KeyRange see, each;  // what the row sees, what every row of the item sees
         {
-            // the row of Q, zeros where there is none; a negative scale's sign goes to Q
-            const uint4* src = reinterpret_cast<const uint4*>(a.q.d + uint64_t(w.s.row0 + i) * a.q.token_stride +
-                                                              uint64_t(qh) * a.q.head_stride);
+            const KvSeq seq{w.row0, w.t, w.held, true};
+            const int r = w.row_first + int(row) + g * kTileRows;
+            see = visible(a, seq, r / int(a.group));
+            if (r >= w.row_first + w.rows) see.lo = see.hi = 0;
+            each.hi = visible(a, seq, w.row_first / int(a.group)).hi;
+            each.lo = visible(a, seq, (w.row_first + w.rows - 1) / int(a.group)).lo;
+        }
+        {
+            // the rows of Q, zeros where there is none; a negative scale's sign goes to Q
+            const int64_t mine = place(a.q);
             const uint32_t flip = a.negate ? 0x80008000u : 0u;
+            uint4 x[kMoves];
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-                uint4 x = there ? src[k] : make_uint4(0, 0, 0, 0);
-                x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-                *reinterpret_cast<uint4*>(sh.q[g] + (k >> 3) * C::kBlockBytes + row * 128u +
-                                          ((uint32_t(k & 7) ^ (row & 7u)) << 4)) = x;
+            for (int k = 0; k < kMoves; ++k) {
+                const int64_t at = __shfl_sync(~0u, mine, k * int(32 / kLanes) + int(piece_row));
+                x[k] = at < 0 ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4*>(a.q.d + at)[piece_col];
             }
+#pragma unroll
+            for (int k = 0; k < kMoves; ++k)
+                *staged(warp * 32u + uint32_t(k) * (32 / kLanes) + piece_row, piece_col) =
+                    make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
             fence_async_proxy();
             mbar_arrive(&sh.q_full[g]);
         }
-        float low = -INFINITY;             // what exponentials are taken against, before the scale
+        float low = -INFINITY;  // what exponentials are taken against, before the scale
         float sum = 0.f;
-        uint32_t plus[D / 32], minus[D / 32];  // columns of the row that an infinity or a NaN (both) reaches
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) plus[k] = minus[k] = 0;
-        for (int j = 0; j < w.n; ++j) {
+        Reached<D> reached;
+        bool reaches = false;
+        for (int j = 0; j < n; ++j) {
             const int pos0 = (w.first_unit + j) * kUnit;
             await(&sh.s_full[g], units_done++);
             uint32_t x[128];
@@ -543,8 +651,7 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
                 for (int k = 0; k < 128; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * scale_value(ks[k]));
             }
             const int from = see.lo - pos0, to = see.hi - pos0;
-            const bool all = from <= 0 && to >= kUnit;
-            if (!__all_sync(~0u, all)) {
+            if (!__all_sync(~0u, from <= 0 && to >= kUnit)) {
 #pragma unroll
                 for (int k = 0; k < 128; ++k)
                     if (k < from || k >= to) x[k] = 0xFF800000u;
@@ -559,86 +666,66 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             }
             const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
             const bool grew = top > low + a.lag;
-            if (__any_sync(~0u, grew)) {
-                // S(j) done means that the product before it is: o can be rescaled
-                const float f = grew ? exp2_fast((low - top) * scale) : 1.f;
-                if (grew) low = top;
-                sum *= f;
-                if (j > 0) {
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t o[32];
-                        tmem_load32(o, o_at + 32u * uint32_t(k));
-                        tmem_wait_load();
-                        tmem_loaded32(o);
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                        tmem_store32(o_at + 32u * uint32_t(k), o);
-                    }
-                }
-            }
+            const float f = grew ? exp2_fast((low - top) * scale) : 1.f;
+            if (grew) low = top;
+            sum *= f;
             const float ref = C::kShift - (low == -INFINITY ? 0.f : low * scale);
             const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
             float2 part[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-            uint32_t p[64];
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
-                const float2 y =
-                    fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), scale2, ref2);
-                const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                part[k & 3] = add2(part[k & 3], e);
-                p[k] = C::kPvHalf ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
-                if ((k & 31) == 31) tmem_store32(s_at + uint32_t(k - 31), p + k - 31);
+            for (int y = 0; y < 8; ++y) {
+                uint32_t p[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 z = fma2(make_float2(__uint_as_float(x[16 * y + 2 * k]),
+                                                      __uint_as_float(x[16 * y + 2 * k + 1])), scale2, ref2);
+                    const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                    part[k & 3] = add2(part[k & 3], e);
+                    p[k] = C::kPvHalf ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                }
+                tmem_store8(s_at + uint32_t(8 * y), p);
             }
             part[0] = add2(add2(part[0], part[1]), add2(part[2], part[3]));
             sum += part[0].x + part[0].y;
+            if (j > 0 && __any_sync(~0u, grew)) {
+                // S(j) done means that the product before it is: o can be rescaled
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t o[32];
+                    tmem_load32(o, o_at + 32u * uint32_t(k));
+                    tmem_wait_load();
+                    tmem_loaded32(o);
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                    tmem_store32(o_at + 32u * uint32_t(k), o);
+                }
+            }
 
             // A weight of 0 hides a finite value of V, not an infinity or a NaN: where
             // some row of the item does not see all of this unit's keys, such values
             // are noted for the rows that see them and taken out of V.
-            const int k0 = max(pos0, w.t.keys.lo), k1 = min(pos0 + kUnit, w.t.keys.hi);
-            const int i_last = (w.t.row_first + w.t.rows - 1) / int(a.group);
-            const KeyRange first_row = visible(a, w.s, w.t.row_first / int(a.group));
-            const KeyRange last_row = visible(a, w.s, i_last);
-            const bool partial = k0 < k1 && (first_row.hi < k1 || last_row.lo > k0);
-            if (partial) {  // the same in all rows' threads
+            const int k0 = max(pos0, w.lo), k1 = min(pos0 + kUnit, w.hi);
+            if (k0 < k1 && (each.hi < k1 || each.lo > k0)) {  // the same in all rows' threads
                 const uint32_t v_tile = first_tile + 2u * uint32_t(j) + 1u, st = v_tile % C::kStages;
                 if (ok) ok = mbar_wait(&sh.kv_full[st], (v_tile / C::kStages) & 1u);
                 uint8_t* v = sh.stage[st];
-                bool special = false;
-#pragma unroll 4
+                constexpr uint32_t kInf = C::kPvHalf ? 0x7C00u : 0x7F80u;
+                uint32_t most = 0;
+#pragma unroll 8
                 for (int k = 0; k < C::kTileBytes / 2048; ++k) {
                     const uint4 y = *reinterpret_cast<const uint4*>(v + (uint32_t(k) * 128u + row) * 16u);
-                    constexpr uint32_t kInf = C::kPvHalf ? 0x7C00u : 0x7F80u;
-                    const uint32_t z = __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
-                                                __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
-                    special |= (z & 0xFFFFu) >= kInf || (z >> 16) >= kInf;
+                    most = __vmaxu2(most, __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
+                                                   __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu)));
                 }
-                if (named_barrier_popc(2 + uint32_t(g), 128, special) > 0) {
-                    // both groups found the same
-                    constexpr uint32_t kInf = C::kPvHalf ? 0x7C00u : 0x7F80u;
-                    for (int key = 0; key < kUnit; ++key) {
-                        const bool sees = pos0 + key >= see.lo && pos0 + key < see.hi;
-#pragma unroll
-                        for (int k = 0; k < D / 2; ++k) {
-                            const uint32_t y = *reinterpret_cast<const uint32_t*>(
-                                v + (k >> 5) * C::kBlockBytes + key * 128 + ((((k >> 2) & 7) ^ (key & 7)) << 4) +
-                                (k & 3) * 4);
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const uint32_t bits = (y >> (16 * z)) & 0xFFFFu, mag = bits & 0x7FFFu;
-                                const uint32_t at = uint32_t(2 * k + z);
-                                if (mag >= kInf && sees) {
-                                    if (mag > kInf || !(bits & 0x8000u)) plus[at >> 5] |= 1u << (at & 31u);
-                                    if (mag > kInf || (bits & 0x8000u)) minus[at >> 5] |= 1u << (at & 31u);
-                                }
-                            }
-                        }
-                    }
+                const bool special = (most & 0xFFFFu) >= kInf || (most >> 16) >= kInf;
+                if (named_barrier_popc(2 + uint32_t(g), 128, special) > 0) {  // the same in both groups
+                    if (!reaches) reached = Reached<D>{};
+                    reaches = true;
+                    note_special<C::kPvHalf, D>(v, from, to, &reached);
                     // group 0 takes them out once both have noted them; group 1's product
                     // is issued after group 0's
                     if (g == 1) mbar_arrive(&sh.noted);
-                    if (g == 0 && w.two() && ok) ok = mbar_wait(&sh.noted, noted++ & 1u);
+                    if (g == 0 && w.rows > kTileRows && ok) ok = mbar_wait(&sh.noted, noted++ & 1u);
                     if (g == 0 && ok) {
                         for (int k = 0; k < C::kTileBytes / 512; ++k) {
                             uint32_t* at = reinterpret_cast<uint32_t*>(v) + uint32_t(k) * 128u + row;
@@ -656,18 +743,15 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             if (ok) mbar_arrive(&sh.p_full[g]);
         }
 
-        // the segment's sums
+        // the piece's sums
         await(&sh.o_full[g], segments++);
-        const bool whole = w.whole();
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint16_t* dst = a.out.d + uint64_t(w.s.row0 + i) * a.out.token_stride + uint64_t(qh) * a.out.head_stride;
-        const uint32_t first = whole ? 0u : share_of(w.units, w.ctas, w.item_start);
-        const uint32_t last = whole ? 0u : share_of(w.units, w.ctas, w.item_end - 1);
+        const uint32_t first = w.first_cta, last = w.last_cta;
+        const bool whole = first == last;
         const auto slot = [&](uint32_t cta) {
-            return a.parts + ((uint64_t(cta) * 2 + (cta == first ? 1 : 0)) * 2 + uint32_t(g)) * C::kPartFloats;
+            return a.parts + ((uint64_t(cta) * 2 + (cta == first ? 1 : 0)) * 2 + uint32_t(g)) * C::kPartFloats + row;
         };
-        float* mine = whole ? nullptr : slot(blockIdx.x);
-        const auto put = [&](int k, const float* o, float f) {  // 32 columns of the result
+        // 32 columns of the row, divided, to the stage
+        const auto stage32 = [&](int k, const float* o, float f) {
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 uint32_t z[4];
@@ -675,15 +759,29 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
                 for (int e = 0; e < 4; ++e)
                     z[e] = H ? pack_half2(o[8 * y + 2 * e] * f, o[8 * y + 2 * e + 1] * f)
                              : pack_bf16x2(o[8 * y + 2 * e] * f, o[8 * y + 2 * e + 1] * f);
-                if (there)
-                    *reinterpret_cast<uint4*>(dst + 32 * k + 8 * y) = make_uint4(z[0], z[1], z[2], z[3]);
+                *staged(row, uint32_t(4 * k + y)) = make_uint4(z[0], z[1], z[2], z[3]);
             }
         };
-        const auto put_lse = [&](float m, float l) {
-            if (a.lse && there)
-                a.lse[uint64_t(w.s.row0 + i) * a.q_heads + qh] =
-                    l == 0.f ? -INFINITY : (m * scale - C::kShift + log2f(l)) * 0.693147180559945309f;
+        // the staged rows of the warp and their logarithms to memory
+        const auto put = [&](float m, float l) {
+            __syncwarp();
+            const int64_t mine = place(a.out);
+#pragma unroll
+            for (int k = 0; k < kMoves; ++k) {
+                const uint32_t r = uint32_t(k) * (32 / kLanes) + piece_row;
+                const int64_t at = __shfl_sync(~0u, mine, int(r));
+                const uint4 y = *staged(warp * 32u + r, piece_col);
+                if (at >= 0) reinterpret_cast<uint4*>(a.out.d + at)[piece_col] = y;
+            }
+            if (a.lse && mine >= 0) {
+                const int r = w.row_first + int(row) + g * kTileRows, i = r / int(a.group);
+                a.lse[uint64_t(w.row0 + i) * a.q_heads + w.head * a.group + uint32_t(r - i * int(a.group))] =
+                    l == 0.f ? -INFINITY
+                             : ((m == -INFINITY ? 0.f : m * scale) - C::kShift + log2f(l)) * 0.693147180559945309f;
+            }
         };
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        float* mine = slot(blockIdx.x);
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
             uint32_t bits[32];
@@ -692,23 +790,26 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             tmem_wait_load();
             tmem_loaded32(bits);
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
-                o[y] = __uint_as_float(bits[y]);
-                if (plus[k] >> y & 1u) o[y] += INFINITY;
-                if (minus[k] >> y & 1u) o[y] += -INFINITY;
+            for (int y = 0; y < 32; ++y) o[y] = __uint_as_float(bits[y]);
+            if (reaches) {
+#pragma unroll
+                for (int y = 0; y < 32; ++y) {
+                    if (reached.plus[k] >> y & 1u) o[y] += INFINITY;
+                    if (reached.minus[k] >> y & 1u) o[y] += -INFINITY;
+                }
             }
             if (whole) {
-                put(k, o, inv);
+                stage32(k, o, inv);
             } else {
 #pragma unroll
-                for (int y = 0; y < 32; ++y) mine[(32 * k + y) * kTileRows + int(row)] = o[y];
+                for (int y = 0; y < 32; ++y) mine[(32 * k + y) * kTileRows] = o[y];
             }
         }
         if (whole) {
-            put_lse(low == -INFINITY ? 0.f : low, sum);
+            put(low, sum);
         } else {
-            mine[D * kTileRows + int(row)] = low;
-            mine[(D + 1) * kTileRows + int(row)] = sum;
+            mine[D * kTileRows] = low;
+            mine[(D + 1) * kTileRows] = sum;
             __threadfence();
             named_barrier(2 + uint32_t(g), 128);
             if (row == 0) sh.joined[g] = atomicAdd(a.counters + 2 * first + uint32_t(g), 1u) == last - first;
@@ -716,33 +817,27 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             if (sh.joined[g]) {
                 __threadfence();
                 float m = -INFINITY, l = 0.f;
-                for (uint32_t cta = first; cta <= last; ++cta)
-                    m = fmaxf(m, __ldcg(slot(cta) + D * kTileRows + row));
+                for (uint32_t cta = first; cta <= last; ++cta) m = fmaxf(m, __ldcg(slot(cta) + D * kTileRows));
+                float o[D];
+#pragma unroll
+                for (int y = 0; y < D; ++y) o[y] = 0.f;
                 for (uint32_t cta = first; cta <= last; ++cta) {
                     const float* part = slot(cta);
-                    const float mc = __ldcg(part + D * kTileRows + row);
-                    l += (mc == m ? 1.f : exp2_fast((mc - m) * scale)) * __ldcg(part + (D + 1) * kTileRows + row);
+                    const float mc = __ldcg(part + D * kTileRows);
+                    const float f = mc == m ? 1.f : exp2_fast((mc - m) * scale);
+                    l += f * __ldcg(part + (D + 1) * kTileRows);
+#pragma unroll
+                    for (int y = 0; y < D; ++y) o[y] += f * __ldcg(part + y * kTileRows);
                 }
                 const float joined = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-                for (int k = 0; k < D / 32; ++k) {
-                    float o[32];
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] = 0.f;
-                    for (uint32_t cta = first; cta <= last; ++cta) {
-                        const float* part = slot(cta);
-                        const float mc = __ldcg(part + D * kTileRows + row);
-                        const float f = mc == m ? 1.f : exp2_fast((mc - m) * scale);
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] += f * __ldcg(part + (32 * k + y) * kTileRows + row);
-                    }
-                    put(k, o, joined);
-                }
-                put_lse(m == -INFINITY ? 0.f : m, l);
+                for (int k = 0; k < D / 32; ++k) stage32(k, o + 32 * k, joined);
+                put(m, l);
             }
         }
-        // the loads of O are done before the next segment's product overwrites it
+        // the loads of O are done before the next piece's product overwrites it
         tc_fence_before();
+        leave();
     }
 }
 
@@ -764,6 +859,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
             mbar_init(&sh.p_full[g], 128);
             mbar_init(&sh.o_full[g], 1);
         }
+        for (int i = 0; i < kSegments; ++i) {
+            mbar_init(&sh.seg_full[i], 1);
+            mbar_init(&sh.seg_empty[i], 8 + 4 + 1);  // warps of the softmax groups and loaders, the product thread
+        }
         mbar_init(&sh.noted, 128);
         mbar_init(&sh.drained, 1);
         mbar_init_fence();
@@ -775,16 +874,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
     const uint32_t tmem = sh.tmem;
     wait_predecessor();  // the plan is written, counters and status clear
     bool ok = true, bad = false;
-    // registers of the launch: 512 threads of 128; 2 * 184 + 80 + 64 = 4 * 128
+    // registers of the launch: 512 threads of 128; 2 * 200 + 72 + 40 = 4 * 128
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        softmax_role<FMT, H, D>(a, sh, plan, tmem, ok);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        softmax_role<FMT, H, D>(a, sh, tmem, ok);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        load_role<FMT, H, D>(a, sh, plan, ok, bad);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        load_role<FMT, H, D>(a, sh, ok, bad);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (threadIdx.x == 12 * 32) product_role<FMT, H, D>(a, sh, plan, tmem, ok);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 12) product_role<FMT, H, D>(sh, tmem, ok);
+        if (threadIdx.x == 13 * 32) segment_role(a, sh, plan, ok);
     }
     if (bad) report(a.status, SPLITZIP_ERR_INVALID_ARG);
     if (!ok) report(a.status, SPLITZIP_ERR_TIMEOUT);

@@ -41,6 +41,15 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t at, uint32_t leading_b
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Instruction descriptor: 16-bit operands (both BF16 or both FP16), 32-bit
 // accumulator, M by N; b_rows_k: B's rows run along the reduction.
 constexpr uint32_t tc_shape(bool bf16, uint32_t m, uint32_t n, bool b_rows_k) {
@@ -88,6 +97,12 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t* r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
 // The registers of loads issued before hold their values after tmem_wait_load
