@@ -195,6 +195,23 @@ int make_input_map(const void* d_in, int dtype, EncodeArgs* a, CUtensorMap* map,
 
 }  // namespace
 
+bool splitzip::make_rows_map(void* base, uint32_t rank, const uint64_t* dims, const uint64_t* strides,
+                             const uint32_t* box, CUtensorMap* map) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], ones[5];
+    for (uint32_t i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        ones[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, base, d, st, b, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int splitzip::device_sms(int* sms) {
     DeviceState d;
     const int st = device_state(&d);

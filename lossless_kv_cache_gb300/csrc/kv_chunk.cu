@@ -30,6 +30,7 @@
 // is still reached, and SPLITZIP_ERR_TIMEOUT is reported.
 #include <algorithm>
 #include <atomic>
+#include <cstring>
 #include <type_traits>
 
 #include "kv_attention.cuh"
@@ -42,9 +43,16 @@ namespace {
 constexpr int kUnit = 128;       // keys
 constexpr int kTileRows = 128;   // rows of a softmax group
 constexpr int kRows = 2 * kTileRows;
-constexpr int kThreads = 512;
 constexpr uint32_t kChunkCtas = 152;  // one on each SM
 constexpr int kPlanThreads = 1024;
+// What an item costs beside its keys (its rows of Q in and results out, the
+// pipeline's start), in units: the plan counts that many before the item's own.
+constexpr int kItemCost = 4;
+
+// Tensor maps of K and V (unused by the kernels that copy rows themselves).
+struct ChunkMaps {
+    CUtensorMap k, v;
+};
 
 struct ChunkStart {
     uint32_t b, tile;
@@ -90,7 +98,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     for (uint32_t i = tid; i < 2 * grid; i += kPlanThreads) a.counters[i] = 0;
     __syncthreads();
     const auto weight = [&](const KvSeq& s, int tile) -> uint64_t {
-        return uint64_t(tile_of(a, s, tile).units) * a.c.kv_heads;
+        return uint64_t(tile_of(a, s, tile).units + kItemCost) * a.c.kv_heads;
     };
     // units of the lane's sequence (every lane of a warp at once)
     const auto seq_units = [&](const KvSeq& s) -> uint64_t {
@@ -221,10 +229,12 @@ struct Segment {
 
 constexpr int kSegments = 4;  // ring of pieces
 
-// FMT 0: cache of the queries' 16-bit type, 1: E5M2, 2: E4M3.
+// FMT 0: cache of the queries' 16-bit type, 1: E5M2, 2: E4M3, 3: as 0, read
+// through tensor maps (pages of 8 tokens and more).
 template <int FMT, bool H, int D>
 struct Chunk {
-    static constexpr bool kFp8 = FMT != 0;
+    static constexpr bool kTma = FMT == 3;
+    static constexpr bool kFp8 = FMT == 1 || FMT == 2;
     static constexpr bool kE5M2 = FMT == 1;
     // Scores are products in the queries' type, the sums over V in FP16 for an
     // FP16 cache and else in BF16, which holds FP8 values times their scales.
@@ -239,6 +249,9 @@ struct Chunk {
     static constexpr int kBlockBytes = 128 * 128;
     static constexpr int kTileBytes = kHalves * kBlockBytes;
     static constexpr int kStages = 131072 / kTileBytes;    // K and V tiles, alternating
+    // warps: two softmax groups, then loaders, then products and pieces
+    static constexpr int kThreads = kTma ? 384 : 512;
+    static constexpr uint32_t kProductWarp = kTma ? 9 : 12, kSegmentWarp = kProductWarp + 1;
     static constexpr int kLagTiles = kFp8 ? 1 : 2;         // copies in flight ahead of their hand-over
     static constexpr int kRaw = kFp8 ? 2 : 0;              // FP8 staging buffers
     static constexpr int kRawBytes = 128 * D;
@@ -251,8 +264,8 @@ struct Chunk {
         uint8_t stage[kStages][kTileBytes];
         uint8_t raw[kRaw > 0 ? kRaw : 1][kRaw > 0 ? kRawBytes : 16];
         // of a unit's keys: byte offset in the pools, or page (FP8, which has no room); -1: none
-        std::conditional_t<kFp8, int32_t, int64_t> place[2][kUnit];
-        uint8_t k_scale[4][kUnit], v_scale[4][kUnit];
+        std::conditional_t<kFp8, int32_t, int64_t> place[2][kTma ? 1 : kUnit];
+        uint8_t k_scale[4][kFp8 ? kUnit : 4], v_scale[4][kFp8 ? kUnit : 4];
         uint64_t kv_full[kStages], kv_empty[kStages];
         uint64_t q_full[2], s_full[2], p_full[2], o_full[2], noted, drained;
         uint64_t seg_full[kSegments], seg_empty[kSegments];
@@ -280,13 +293,11 @@ __device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh,
         }
     }
     for (uint32_t i = 0; ok; ++i) {
-        if (i >= uint32_t(kSegments)) ok = mbar_wait(&sh.seg_empty[i % kSegments], (i / kSegments - 1) & 1u);
-        if (!ok) break;
         Segment g{};
-        const bool more = u < end;
-        if (more) {
+        while (g.n == 0 && u < end) {
             KvSeq s;
             Tile t;
+            uint32_t size = 0;
             while (true) {
                 s = load_seq(a.b, b);
                 if (int(tile) >= tile_count(a, s)) {
@@ -295,28 +306,34 @@ __device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh,
                     continue;
                 }
                 t = tile_of(a, s, int(tile));
-                const uint64_t size = uint64_t(t.units) * a.c.kv_heads;
-                if (u < group_start + size) break;
-                group_start += size;
+                size = uint32_t(t.units + kItemCost);
+                if (u < group_start + uint64_t(size) * a.c.kv_heads) break;
+                group_start += uint64_t(size) * a.c.kv_heads;
                 ++tile;
             }
-            const uint32_t head = uint32_t((u - group_start) / uint32_t(t.units));
-            const uint64_t item_start = group_start + uint64_t(head) * uint32_t(t.units);
-            const uint64_t item_end = item_start + uint32_t(t.units);
-            const uint64_t stop = min(item_end, end);
+            const uint32_t head = uint32_t((u - group_start) / size);
+            const uint64_t keys_start = group_start + uint64_t(head) * size + kItemCost;
+            const uint64_t item_end = keys_start + uint32_t(t.units);
+            const uint64_t from = max(u, keys_start), stop = min(item_end, end);
+            if (from >= stop) {  // the share ends before the item's keys
+                u = end;
+                break;
+            }
+            u = stop;
             g.row0 = s.row0, g.t = s.t, g.held = s.n;
             g.row_first = t.row_first, g.rows = t.rows;
             g.lo = t.keys.lo, g.hi = t.keys.hi;
-            g.first_unit = t.keys.lo / kUnit + int(u - item_start);
-            g.n = int(stop - u);
+            g.first_unit = t.keys.lo / kUnit + int(from - keys_start);
+            g.n = int(stop - from);
             g.b = b, g.head = head;
-            g.first_cta = share_of(units, ctas, item_start);
+            g.first_cta = share_of(units, ctas, keys_start);
             g.last_cta = share_of(units, ctas, item_end - 1);
-            u = stop;
         }
+        if (i >= uint32_t(kSegments)) ok = mbar_wait(&sh.seg_empty[i % kSegments], (i / kSegments - 1) & 1u);
+        if (!ok) break;
         sh.seg[i % kSegments] = g;
         mbar_arrive(&sh.seg_full[i % kSegments]);
-        if (!more) break;
+        if (g.n == 0) break;
     }
 }
 
@@ -456,6 +473,65 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     while (handed < made) hand_over();
+}
+
+// The loader of a 16-bit cache whose pages are whole swizzle groups of eight
+// tokens: one warp, a lane a box of up to 128 tokens by 64 columns.  Boxes that
+// hold nothing an item sees lie past the last page, which reads as zeros.
+template <class C>
+__device__ __forceinline__ void load_tma_role(const AttentionArgs& a, typename C::Shared& sh, const CUtensorMap* k_map,
+                                              const CUtensorMap* v_map, bool& ok, bool& bad) {
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t page_tokens = 1u << a.c.page_shift, box = min(page_tokens, uint32_t(kUnit));
+    const uint32_t half = lane % C::kHalves, nth = lane / C::kHalves;  // of the lane's box: column block, box of the unit
+    const bool mine = nth < kUnit / box;
+    uint32_t made = 0, issued = 0;
+    for (uint32_t piece = 0;; ++piece) {
+        const Segment& w = sh.seg[piece % kSegments];
+        if (ok) ok = mbar_wait(&sh.seg_full[piece % kSegments], (piece / kSegments) & 1u);
+        ok = __all_sync(~0u, ok);
+        if (!ok || w.n == 0) break;
+        const int32_t* table = a.b.table + uint64_t(w.b) * a.b.table_stride;
+        const auto page_of = [&](int j) -> int32_t {
+            const int pos = (w.first_unit + j) * kUnit + int(nth * box);
+            if (!mine || j >= w.n || pos + int(box) <= w.lo || pos >= w.hi) return -1;
+            const int32_t pg = table[uint32_t(pos) >> a.c.page_shift];
+            if (pg < 0 || uint64_t(pg) >= a.c.pool_pages) {
+                bad = true;
+                return -1;
+            }
+            return pg;
+        };
+        const int n = w.n, first_unit = w.first_unit;
+        const int head = int(w.head);
+        int32_t page = page_of(0);
+        for (int j = 0; j < n; ++j) {
+            const int token = ((first_unit + j) * kUnit + int(nth * box)) & int(page_tokens - 1u);
+            const int32_t at = page < 0 ? int32_t(a.c.pool_pages) : page;
+            page = page_of(j + 1);
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                const uint32_t x = made++, st = x % C::kStages;
+                if (ok && x >= uint32_t(C::kStages))
+                    ok = mbar_wait(&sh.kv_empty[st], (x / C::kStages - 1) & 1u);
+                ok = __all_sync(~0u, ok);
+                if (!ok) continue;
+                issued = made;
+                if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], C::kTileBytes);
+                __syncwarp();
+                if (mine)
+                    tensor_load_4d(sh.stage[st] + half * C::kBlockBytes + nth * box * 128u, side ? v_map : k_map,
+                                   int(half * 64u), head, token, at, &sh.kv_full[st]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.seg_empty[piece % kSegments]);
+    }
+    // no copy is in flight when the CTA ends
+    for (uint32_t i = 0; i < uint32_t(C::kStages) && i < issued; ++i) {
+        const uint32_t x = issued - 1 - i;
+        if (!mbar_wait(&sh.kv_full[x % C::kStages], (x / C::kStages) & 1u)) ok = false;
+    }
 }
 
 // One warp, converged, so that operand descriptors stay in uniform registers;
@@ -705,14 +781,28 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             // some row of the item does not see all of this unit's keys, such values
             // are noted for the rows that see them and taken out of V.
             const int k0 = max(pos0, w.lo), k1 = min(pos0 + kUnit, w.hi);
-            if (k0 < k1 && (each.hi < k1 || each.lo > k0)) {  // the same in all rows' threads
+            if (k0 < k1 && (each.hi < k1 || each.lo > k0 || (C::kTma && (k0 > pos0 || k1 < pos0 + kUnit)))) {
+                // the same in all rows' threads
                 const uint32_t v_tile = first_tile + 2u * uint32_t(j) + 1u, st = v_tile % C::kStages;
                 if (ok) ok = mbar_wait(&sh.kv_full[st], (v_tile / C::kStages) & 1u);
                 uint8_t* v = sh.stage[st];
                 constexpr uint32_t kInf = C::kPvHalf ? 0x7C00u : 0x7F80u;
                 uint32_t most = 0;
+                if (C::kTma && (k0 > pos0 || k1 < pos0 + kUnit)) {
+                    // a page's tokens past the sequence's end came too: out of the
+                    // products (group 1's are issued after group 0's), and of the search
+                    const bool out = pos0 + int(row) < k0 || pos0 + int(row) >= k1;
+                    if (g == 0 && out && ok) {
+                        for (int k = 0; k < D / 8; ++k)
+                            *reinterpret_cast<uint4*>(v + (k >> 3) * C::kBlockBytes + row * 128u + (k & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_proxy();
+                }
 #pragma unroll 8
                 for (int k = 0; k < C::kTileBytes / 2048; ++k) {
+                    const int key = pos0 + int((uint32_t(k) * 16u + (row >> 3)) & 127u);  // 8 pieces a row
+                    if (C::kTma && (key < k0 || key >= k1)) continue;
                     const uint4 y = *reinterpret_cast<const uint4*>(v + (uint32_t(k) * 128u + row) * 16u);
                     most = __vmaxu2(most, __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
                                                    __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu)));
@@ -842,15 +932,16 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
 }
 
 template <int FMT, bool H, int D>
-__global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_constant__ AttentionArgs a,
-                                                               const ChunkPlan* plan) {
+__global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
+    kv_chunk_kernel(const __grid_constant__ AttentionArgs a, const ChunkPlan* plan,
+                    const __grid_constant__ ChunkMaps maps) {
     using C = Chunk<FMT, H, D>;
     extern __shared__ __align__(1024) uint8_t smem_chunk[];  // the swizzle goes by address bits below 1024
     auto& sh = *reinterpret_cast<typename C::Shared*>(smem_chunk);
     const uint32_t warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&sh.kv_full[i], 128);
+            mbar_init(&sh.kv_full[i], C::kTma ? 1 : 128);
             mbar_init(&sh.kv_empty[i], 1);
         }
         for (int g = 0; g < 2; ++g) {
@@ -861,44 +952,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const __grid_cons
         }
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 8 + 4 + 1);  // warps of the softmax groups and loaders, the product thread
+            mbar_init(&sh.seg_empty[i], 8 + (C::kTma ? 1 : 4) + 1);  // warps of the softmax groups, loaders, products
         }
         mbar_init(&sh.noted, 128);
         mbar_init(&sh.drained, 1);
         mbar_init_fence();
     }
-    if (warp == 12) tmem_alloc(smem_u32(&sh.tmem), 512);
+    if (warp == C::kProductWarp) tmem_alloc(smem_u32(&sh.tmem), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     wait_predecessor();  // the plan is written, counters and status clear
     bool ok = true, bad = false;
-    // registers of the launch: 512 threads of 128; 2 * 200 + 72 + 40 = 4 * 128
+    // registers of the launch: 384 threads of 168, 2 * 216 + 72 = 3 * 168, or 512 of 128,
+    // 2 * 200 + 72 + 40 = 4 * 128
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if (C::kTma)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         softmax_role<FMT, H, D>(a, sh, tmem, ok);
-    } else if (warp < 12) {
+    } else if (C::kTma || warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        load_role<FMT, H, D>(a, sh, ok, bad);
+        if constexpr (!C::kTma) load_role<FMT, H, D>(a, sh, ok, bad);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 12) product_role<FMT, H, D>(sh, tmem, ok);
-        if (threadIdx.x == 13 * 32) segment_role(a, sh, plan, ok);
     }
+    if constexpr (C::kTma) {
+        if (warp == 8) load_tma_role<C>(a, sh, &maps.k, &maps.v, ok, bad);
+    }
+    if (warp == C::kProductWarp) product_role<FMT, H, D>(sh, tmem, ok);
+    if (threadIdx.x == C::kSegmentWarp * 32u) segment_role(a, sh, plan, ok);
     if (bad) report(a.status, SPLITZIP_ERR_INVALID_ARG);
     if (!ok) report(a.status, SPLITZIP_ERR_TIMEOUT);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == C::kProductWarp) {
         tc_fence_after();
         tmem_free(tmem, 512);
     }
 }
 
 template <int FMT, bool H, int D>
-int launch(const AttentionArgs& a, ChunkPlan* plan, uint32_t ctas, cudaStream_t s) {
+int launch(const AttentionArgs& a, ChunkPlan* plan, const ChunkMaps& maps, uint32_t ctas, cudaStream_t s) {
     using C = Chunk<FMT, H, D>;
     static_assert(C::kSmem <= 232448, "shared memory of a CTA");
     static std::atomic<uint64_t> ready{0};
@@ -912,17 +1010,30 @@ int launch(const AttentionArgs& a, ChunkPlan* plan, uint32_t ctas, cudaStream_t 
         }
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     }
-    ChainedLaunch l(dim3(ctas), dim3(kThreads), C::kSmem, s);
-    if (cudaLaunchKernelEx(&l.cfg, kv_chunk_kernel<FMT, H, D>, a, static_cast<const ChunkPlan*>(plan)) != cudaSuccess) {
+    ChainedLaunch l(dim3(ctas), dim3(C::kThreads), C::kSmem, s);
+    if (cudaLaunchKernelEx(&l.cfg, kv_chunk_kernel<FMT, H, D>, a, static_cast<const ChunkPlan*>(plan), maps) !=
+        cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }
     return SPLITZIP_OK;
 }
 
-template <int FMT, bool H>
-int launch_dim(const AttentionArgs& a, ChunkPlan* plan, uint32_t ctas, cudaStream_t s) {
-    return a.c.head_dim == 128 ? launch<FMT, H, 128>(a, plan, ctas, s) : launch<FMT, H, 64>(a, plan, ctas, s);
+template <int FMT>
+int launch_type(const AttentionArgs& a, bool half, ChunkPlan* plan, const ChunkMaps& maps, uint32_t ctas,
+                cudaStream_t s) {
+    if (a.c.head_dim == 128)
+        return half ? launch<FMT, true, 128>(a, plan, maps, ctas, s) : launch<FMT, false, 128>(a, plan, maps, ctas, s);
+    return half ? launch<FMT, true, 64>(a, plan, maps, ctas, s) : launch<FMT, false, 64>(a, plan, maps, ctas, s);
+}
+
+// Maps of the pools for boxes of 64 columns and up to 128 tokens of one head
+// and page; false where the driver takes no such strides.
+bool make_maps(const AttentionArgs& a, ChunkMaps* m) {
+    const uint64_t dims[4] = {a.c.head_dim, a.c.kv_heads, uint64_t(1) << a.c.page_shift, a.c.pool_pages};
+    const uint64_t strides[3] = {a.c.head_stride, a.c.token_stride, a.c.page_stride};
+    const uint32_t box[4] = {64, 1, std::min<uint32_t>(1u << a.c.page_shift, kUnit), 1};
+    return make_rows_map(a.c.k, 4, dims, strides, box, &m->k) && make_rows_map(a.c.v, 4, dims, strides, box, &m->v);
 }
 
 }  // namespace
@@ -941,13 +1052,13 @@ int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan_at, uint32_t
     ChunkPlan* plan = static_cast<ChunkPlan*>(plan_at);
     kv_chunk_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, plan, ctas);
     if (cudaGetLastError() != cudaSuccess) return SPLITZIP_ERR_CUDA;
-    switch (a.c.type) {
-        case SPLITZIP_KV_FP8_E5M2:
-            return q_half ? launch_dim<1, true>(a, plan, ctas, s) : launch_dim<1, false>(a, plan, ctas, s);
-        case SPLITZIP_KV_FP8_E4M3:
-            return q_half ? launch_dim<2, true>(a, plan, ctas, s) : launch_dim<2, false>(a, plan, ctas, s);
-        default: return q_half ? launch_dim<0, true>(a, plan, ctas, s) : launch_dim<0, false>(a, plan, ctas, s);
-    }
+    ChunkMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (a.c.type == SPLITZIP_KV_FP8_E5M2) return launch_type<1>(a, q_half, plan, maps, ctas, s);
+    if (a.c.type == SPLITZIP_KV_FP8_E4M3) return launch_type<2>(a, q_half, plan, maps, ctas, s);
+    // A box's rows have to be whole groups of eight for the swizzle.
+    if (a.c.page_shift >= 3 && make_maps(a, &maps)) return launch_type<3>(a, q_half, plan, maps, ctas, s);
+    return launch_type<0>(a, q_half, plan, maps, ctas, s);
 }
 
 }  // namespace splitzip

@@ -90,6 +90,16 @@ __device__ __forceinline__ void tensor_load_2d(void* dst, const void* map, int32
         : "memory");
 }
 
+// The same for a box of a 4-D tensor.
+__device__ __forceinline__ void tensor_load_4d(void* dst, const void* map, int32_t x, int32_t y, int32_t z, int32_t w,
+                                               uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Named barrier for a subset of the CTA's warps (id 0 is __syncthreads).
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
