@@ -47,7 +47,7 @@ constexpr uint32_t kChunkCtas = 152;  // one on each SM
 constexpr int kPlanThreads = 1024;
 // What an item costs beside its keys (its rows of Q in and results out, the
 // pipeline's start), in units: the plan counts that many before the item's own.
-constexpr int kItemCost = 4;
+constexpr int kItemCost = 8;
 
 // Tensor maps of K and V (unused by the kernels that copy rows themselves).
 struct ChunkMaps {
@@ -249,6 +249,7 @@ struct Chunk {
     static constexpr int kBlockBytes = 128 * 128;
     static constexpr int kTileBytes = kHalves * kBlockBytes;
     static constexpr int kStages = 131072 / kTileBytes;    // K and V tiles, alternating
+    static constexpr int kDepth = kStages / 2;             // units in flight
     // warps: two softmax groups, then loaders, then products and pieces
     static constexpr int kThreads = kTma ? 384 : 512;
     static constexpr uint32_t kProductWarp = kTma ? 9 : 12, kSegmentWarp = kProductWarp + 1;
@@ -266,7 +267,8 @@ struct Chunk {
         // of a unit's keys: byte offset in the pools, or page (FP8, which has no room); -1: none
         std::conditional_t<kFp8, int32_t, int64_t> place[2][kTma ? 1 : kUnit];
         uint8_t k_scale[4][kFp8 ? kUnit : 4], v_scale[4][kFp8 ? kUnit : 4];
-        uint64_t kv_full[kStages], kv_empty[kStages];
+        uint64_t kv_full[kStages];
+        uint64_t freed[kDepth];          // K of unit u and V of unit u - 1 are no longer read
         uint64_t q_full[2], s_full[2], p_full[2], o_full[2], noted, drained;
         uint64_t seg_full[kSegments], seg_empty[kSegments];
         uint32_t tmem, joined[2];
@@ -337,6 +339,14 @@ __device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh,
     }
 }
 
+// Waits until the stage of tile x (K of unit x / 2 where even, else V) can be
+// overwritten.
+template <class C>
+__device__ __forceinline__ bool await_freed(typename C::Shared& sh, uint32_t x) {
+    const int u = int(x >> 1) - C::kDepth + int(x & 1u);  // which release
+    return u < 0 || mbar_wait(&sh.freed[u % C::kDepth], uint32_t(u / C::kDepth) & 1u);
+}
+
 template <int FMT, bool H, int D>
 __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk<FMT, H, D>::Shared& sh,
                                           bool& ok, bool& bad) {
@@ -346,9 +356,7 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
     uint32_t made = 0, handed = 0;  // tiles whose copies were started, and handed over
 
     const auto await_empty = [&](uint32_t x) {
-        if (x >= uint32_t(C::kStages)) {
-            if (ok) ok = mbar_wait(&sh.kv_empty[x % C::kStages], (x / C::kStages - 1) & 1u);
-        }
+        if (ok) ok = await_freed<C>(sh, x);
     };
     // Hands over tile `handed`, whose copies by this thread have landed.
     const auto hand_over = [&]() {
@@ -392,7 +400,8 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
             }
         }
         fence_async_proxy();
-        mbar_arrive(&sh.kv_full[st]);
+        __syncwarp();
+        if ((lt & 31u) == 0) mbar_arrive(&sh.kv_full[st]);
     };
 
     for (uint32_t piece = 0;; ++piece) {
@@ -512,8 +521,7 @@ __device__ __forceinline__ void load_tma_role(const AttentionArgs& a, typename C
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
                 const uint32_t x = made++, st = x % C::kStages;
-                if (ok && x >= uint32_t(C::kStages))
-                    ok = mbar_wait(&sh.kv_empty[st], (x / C::kStages - 1) & 1u);
+                if (ok) ok = await_freed<C>(sh, x);
                 ok = __all_sync(~0u, ok);
                 if (!ok) continue;
                 issued = made;
@@ -534,74 +542,100 @@ __device__ __forceinline__ void load_tma_role(const AttentionArgs& a, typename C
     }
 }
 
-// One warp, converged, so that operand descriptors stay in uniform registers;
-// one elected lane issues.
+// One warp, converged, whose elected lane issues.  What lies between two
+// steps' products counts, for the tensor core queues few of them: a wait of its
+// own between them cost some 45 cycles of it.  So a step (a tile's weights
+// times V, then its next scores) is asked for while the products before it are
+// issued, and waited for only where it was not ready then.
 template <int FMT, bool H, int D>
 __device__ __forceinline__ void product_role(typename Chunk<FMT, H, D>::Shared& sh, uint32_t tmem, bool& ok) {
     using C = Chunk<FMT, H, D>;
     constexpr uint32_t kShapeS = tc_shape(!H, 128, 128, false);
     constexpr uint32_t kShapeO = tc_shape(!C::kPvHalf, 128, D, true);
+    constexpr uint32_t kTileStep = C::kTileBytes >> 4, kBlockStep = C::kBlockBytes >> 4;  // in the descriptors' units
     const uint64_t q_operand = smem_operand(smem_u32(sh.q[0]), 16, 1024);
     const uint64_t k_operand = smem_operand(smem_u32(sh.stage[0]), 16, 1024);
-    const uint64_t v_operand = smem_operand(smem_u32(sh.stage[0]), C::kBlockBytes, 1024);
-    constexpr uint32_t kTileStep = C::kTileBytes >> 4;  // in the descriptors' units
-    uint32_t tile = 0, segments[2] = {0, 0}, weights[2] = {0, 0};
-    const auto await = [&](uint64_t* bar, uint32_t count) {
-        if (ok) ok = mbar_wait(bar, count & 1u);
-        ok = __all_sync(~0u, ok);
-        tc_fence_after();
+    const uint64_t v_operand = smem_operand(smem_u32(sh.stage[1]), C::kBlockBytes, 1024);
+    const bool leader = elect_lane();
+    const auto scores = [&](int g, uint32_t stage) {
+        const uint64_t q = q_operand + uint32_t(g) * kTileStep, kk = k_operand + stage * (2u * kTileStep);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = uint32_t(k / 4) * kBlockStep + uint32_t(k % 4) * 2u;
+            tc_mma(leader && ok, tmem + uint32_t(g) * 128u, q + at, kk + at, kShapeS, k > 0);
+        }
     };
+    const auto sums = [&](int g, uint32_t stage, bool first) {
+        const uint64_t v = v_operand + stage * (2u * kTileStep);
+#pragma unroll
+        for (int k = 0; k < kUnit / 16; ++k)
+            tc_mma_ta(leader && ok, tmem + 256u + uint32_t(g) * 128u, tmem + uint32_t(g) * 128u + uint32_t(k) * 8u,
+                      v + uint32_t(k) * (2048u >> 4), kShapeO, k > 0 || !first);
+    };
+    uint32_t unit = 0;  // of the share
+    uint32_t segments[2] = {0, 0}, weights[2] = {0, 0};
     for (uint32_t piece = 0;; ++piece) {
-        await(&sh.seg_full[piece % kSegments], piece / kSegments);
+        if (ok) ok = mbar_wait(&sh.seg_full[piece % kSegments], (piece / kSegments) & 1u);
+        ok = __all_sync(~0u, ok);
         const int n = ok ? sh.seg[piece % kSegments].n : 0;
         if (n == 0) break;
-        const int groups = sh.seg[piece % kSegments].rows > kTileRows ? 2 : 1;
+        const bool two = sh.seg[piece % kSegments].rows > kTileRows;
         __syncwarp();
-        if (elect_lane()) mbar_arrive(&sh.seg_empty[piece % kSegments]);
-        for (int j = -1; j < n; ++j) {
+        if (leader) mbar_arrive(&sh.seg_empty[piece % kSegments]);
+        // the first scores
+        if (ok) ok = mbar_wait(&sh.kv_full[2u * (unit % C::kDepth)], (unit / C::kDepth) & 1u);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (g == 1 && !two) break;
+            if (ok) ok = mbar_wait(&sh.q_full[g], segments[g]++ & 1u);
+            tc_fence_after();
+            scores(g, unit % C::kDepth);
+            if (leader && ok) tc_commit(&sh.s_full[g]);
+        }
+        if (leader && ok) tc_commit(&sh.freed[unit % C::kDepth]);
+        bool ready0 = false, ready1 = false;
+        for (int j = 0; j < n; ++j, ++unit) {
             const bool last = j == n - 1;
-            // tiles of the ring: K(0) V(0) K(1) V(1) ...
-            const uint32_t v_tile = tile + 2u * uint32_t(j) + 1u, k_tile = tile + 2u * uint32_t(j + 1);
-            const uint32_t v_stage = v_tile % C::kStages, k_stage = k_tile % C::kStages;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                if (g >= groups) break;
-                if (j >= 0) {
-                    if (g == 0) await(&sh.kv_full[v_stage], v_tile / C::kStages);
-                    await(&sh.p_full[g], weights[g]++);
-                    if (ok && elect_lane()) {
-                        const uint64_t v = v_operand + v_stage * kTileStep;
-#pragma unroll
-                        for (int k = 0; k < kUnit / 16; ++k)
-                            tc_mma_ta(tmem + 256u + uint32_t(g) * 128u, tmem + uint32_t(g) * 128u + uint32_t(k) * 8u,
-                                      v + uint32_t(k) * (2048u >> 4), kShapeO, k > 0 || j > 0);
-                        if (last) tc_commit(&sh.o_full[g]);
-                        if (g == groups - 1) tc_commit(&sh.kv_empty[v_stage]);
-                    }
-                    __syncwarp();
-                }
-                if (!last) {
-                    if (j < 0) await(&sh.q_full[g], segments[g]++);
-                    if (g == 0) await(&sh.kv_full[k_stage], k_tile / C::kStages);
-                    if (ok && elect_lane()) {
-                        const uint64_t q = q_operand + uint32_t(g) * kTileStep, kk = k_operand + k_stage * kTileStep;
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            constexpr uint32_t kBlock = C::kBlockBytes >> 4;
-                            const uint32_t at = uint32_t(k / 4) * kBlock + uint32_t(k % 4) * 2u;
-                            tc_mma(tmem + uint32_t(g) * 128u, q + at, kk + at, kShapeS, k > 0);
-                        }
-                        tc_commit(&sh.s_full[g]);
-                        if (g == groups - 1) tc_commit(&sh.kv_empty[k_stage]);
-                    }
-                    __syncwarp();
+            const uint32_t stage = unit % C::kDepth, phase = (unit / C::kDepth) & 1u;
+            const uint32_t next = (unit + 1) % C::kDepth, next_phase = ((unit + 1) / C::kDepth) & 1u;
+            const uint32_t turn0 = weights[0]++ & 1u, turn1 = weights[1] & 1u;
+            if (!ready0) {
+                if (ok) ok = mbar_wait(&sh.p_full[0], turn0);
+                if (ok) ok = mbar_wait(&sh.kv_full[2u * stage + 1u], phase);
+                if (ok && !last) ok = mbar_wait(&sh.kv_full[2u * next], next_phase);
+            }
+            tc_fence_after();
+            sums(0, stage, j == 0);
+            ready1 = two && mbar_try_wait(&sh.p_full[1], turn1);
+            if (last) {
+                if (leader && ok) tc_commit(&sh.o_full[0]);
+            } else {
+                scores(0, next);
+                if (leader && ok) tc_commit(&sh.s_full[0]);
+            }
+            if (two) {
+                ++weights[1];
+                if (!ready1 && ok) ok = mbar_wait(&sh.p_full[1], turn1);
+                tc_fence_after();
+                sums(1, stage, j == 0);
+                if (last) {
+                    if (leader && ok) tc_commit(&sh.o_full[1]);
+                } else {
+                    scores(1, next);
+                    if (leader && ok) tc_commit(&sh.s_full[1]);
                 }
             }
+            if (!last) {
+                // the next unit's first tile: its weights, V, and the keys after
+                const uint32_t after = (unit + 2) % C::kDepth, after_phase = ((unit + 2) / C::kDepth) & 1u;
+                ready0 = mbar_try_wait(&sh.p_full[0], turn0 ^ 1u) & mbar_try_wait(&sh.kv_full[2u * next + 1u], next_phase);
+                if (j + 2 < n) ready0 &= mbar_try_wait(&sh.kv_full[2u * after], after_phase);
+                if (leader && ok) tc_commit(&sh.freed[next]);
+            }
         }
-        tile += 2u * uint32_t(n);
     }
     // no product is in flight when the CTA gives its memory back
-    if (elect_lane()) tc_commit(&sh.drained);
+    if (leader) tc_commit(&sh.drained);
     __syncwarp();
     if (!mbar_wait(&sh.drained, 0)) ok = false;
 }
@@ -706,7 +740,8 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
                 *staged(warp * 32u + uint32_t(k) * (32 / kLanes) + piece_row, piece_col) =
                     make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
             fence_async_proxy();
-            mbar_arrive(&sh.q_full[g]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full[g]);
         }
         float low = -INFINITY;  // what exponentials are taken against, before the scale
         float sum = 0.f;
@@ -735,45 +770,26 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 128; k += 8) {
-                m0 = fmaxf(fmaxf(m0, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
-                m1 = fmaxf(fmaxf(m1, __uint_as_float(x[k + 2])), __uint_as_float(x[k + 3]));
-                m2 = fmaxf(fmaxf(m2, __uint_as_float(x[k + 4])), __uint_as_float(x[k + 5]));
-                m3 = fmaxf(fmaxf(m3, __uint_as_float(x[k + 6])), __uint_as_float(x[k + 7]));
+                m0 = max3(m0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                m1 = max3(m1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+                m2 = max3(m2, __uint_as_float(x[k + 4]), __uint_as_float(x[k + 5]));
+                m3 = max3(m3, __uint_as_float(x[k + 6]), __uint_as_float(x[k + 7]));
             }
             const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
             const bool grew = top > low + a.lag;
             const float f = grew ? exp2_fast((low - top) * scale) : 1.f;
             if (grew) low = top;
-            sum *= f;
-            const float ref = C::kShift - (low == -INFINITY ? 0.f : low * scale);
-            const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
-            float2 part[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                uint32_t p[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float2 z = fma2(make_float2(__uint_as_float(x[16 * y + 2 * k]),
-                                                      __uint_as_float(x[16 * y + 2 * k + 1])), scale2, ref2);
-                    const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                    part[k & 3] = add2(part[k & 3], e);
-                    p[k] = C::kPvHalf ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
-                }
-                tmem_store8(s_at + uint32_t(8 * y), p);
-            }
-            part[0] = add2(add2(part[0], part[1]), add2(part[2], part[3]));
-            sum += part[0].x + part[0].y;
             if (j > 0 && __any_sync(~0u, grew)) {
                 // S(j) done means that the product before it is: o can be rescaled
 #pragma unroll 1
-                for (int k = 0; k < D / 32; ++k) {
-                    uint32_t o[32];
-                    tmem_load32(o, o_at + 32u * uint32_t(k));
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t o[16];
+                    tmem_load16(o, o_at + 16u * uint32_t(k));
                     tmem_wait_load();
-                    tmem_loaded32(o);
+                    tmem_loaded16(o);
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                    tmem_store32(o_at + 32u * uint32_t(k), o);
+                    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                    tmem_store16(o_at + 16u * uint32_t(k), o);
                 }
             }
 
@@ -828,9 +844,29 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
                     }
                 }
             }
+            const float ref = C::kShift - (low == -INFINITY ? 0.f : low * scale);
+            const float2 scale2 = make_float2(scale, scale), ref2 = make_float2(ref, ref);
+            float2 part[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                uint32_t p[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float2 z = fma2(make_float2(__uint_as_float(x[32 * y + 2 * k]),
+                                                      __uint_as_float(x[32 * y + 2 * k + 1])), scale2, ref2);
+                    const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                    part[k & 3] = add2(part[k & 3], e);
+                    p[k] = C::kPvHalf ? pack_half2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+                }
+                tmem_store16(s_at + uint32_t(16 * y), p);
+            }
             tmem_wait_store();
             tc_fence_before();
-            if (ok) mbar_arrive(&sh.p_full[g]);
+            // one arrival a warp: 32 lanes' would be taken one after the other
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&sh.p_full[g]);
+            part[0] = add2(add2(part[0], part[1]), add2(part[2], part[3]));
+            sum = sum * f + (part[0].x + part[0].y);
         }
 
         // the piece's sums
@@ -941,13 +977,13 @@ __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
     const uint32_t warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&sh.kv_full[i], C::kTma ? 1 : 128);
-            mbar_init(&sh.kv_empty[i], 1);
+            mbar_init(&sh.kv_full[i], C::kTma ? 1 : 4);
         }
+        for (int i = 0; i < C::kDepth; ++i) mbar_init(&sh.freed[i], 1);
         for (int g = 0; g < 2; ++g) {
-            mbar_init(&sh.q_full[g], 128);
+            mbar_init(&sh.q_full[g], 4);
             mbar_init(&sh.s_full[g], 1);
-            mbar_init(&sh.p_full[g], 128);
+            mbar_init(&sh.p_full[g], 4);
             mbar_init(&sh.o_full[g], 1);
         }
         for (int i = 0; i < kSegments; ++i) {
