@@ -39,7 +39,7 @@ int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, Plan* p) {
         size_of(p, chunk_plan_bytes(p->ctas), 2ull * p->ctas, chunk_part_floats(c.head_dim));
     } else {
         // tiles of rows over all sequences: each has a partial one at most
-        const uint64_t tiles = std::min<uint64_t>((rows + kStepRows - 1) / kStepRows + b.batch, rows);
+        const uint64_t tiles = std::min<uint64_t>((rows + 7) / 8 + b.batch, rows);
         p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);
         size_of(p, 0, p->ctas, step_part_floats(c.head_dim));
     }
@@ -80,6 +80,7 @@ extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const spl
     if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 15u)) return SPLITZIP_ERR_INVALID_ARG;
     a.lse = d_lse;
     a.q_heads = q_heads;
+    a.q_half = dtype == SPLITZIP_FP16;
     a.group = p.group;
     a.scale_log2 = float(double(scale) * 1.4426950408889634);
     a.negate = 0;
@@ -96,12 +97,11 @@ extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const spl
     a.status = d_status;
     int sms;
     if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
-    const bool half = dtype == SPLITZIP_FP16;
     if (p.chunk && a.b.tokens > 0)
-        return launch_kv_chunk(a, half, static_cast<uint8_t*>(d_ws) + p.plan_off, p.ctas, stream);
+        return launch_kv_chunk(a, a.q_half != 0, static_cast<uint8_t*>(d_ws) + p.plan_off, p.ctas, stream);
     if (launch_kv_begin(d_status, a.counters, p.ctas, stream) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }
-    return a.b.tokens > 0 ? launch_kv_step(a, half, p.ctas, stream) : int(SPLITZIP_OK);
+    return a.b.tokens > 0 ? launch_kv_step(a, p.ctas, stream) : int(SPLITZIP_OK);
 }

@@ -23,6 +23,7 @@ struct AttentionArgs {
     KvRows q, out;
     float* lse;
     uint32_t q_heads, group;
+    int q_half;  // the queries and results are FP16, else BF16
     // scale * log2(e).  The chunk kernel takes its magnitude, at least the
     // smallest normal, with its sign (`negate`) given to the queries.
     float scale_log2;
@@ -76,10 +77,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // kv_step.cu
-constexpr int kStepRows = 16;  // rows of a tile
+constexpr int kStepRows = 16;  // rows of a tile at most
 uint32_t step_ctas(uint64_t items_max, uint64_t keys_max);
 uint64_t step_part_floats(uint32_t head_dim);
-int launch_kv_step(const AttentionArgs& a, bool q_half, uint32_t ctas, cudaStream_t s);
+int launch_kv_step(const AttentionArgs& a, uint32_t ctas, cudaStream_t s);
 
 // kv_chunk.cu
 uint32_t chunk_ctas(uint64_t rows, uint64_t batch, uint64_t kv_heads, uint64_t keys_max);

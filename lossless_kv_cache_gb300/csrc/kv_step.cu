@@ -5,13 +5,20 @@
 // softmax).  For each row m' = max(m, s), l' = l 2^(m-m') + sum 2^(s-m'),
 // o' = o 2^(m-m') + sum 2^(s-m') v, in base 2 with the factor log2(e) in the
 // score's scale; out = o / l.  Parts over different keys join by the same rule.
+// FP8 values are exact in FP16 and are multiplied there without their scales:
+// K's go to the scores, V's, 2^e, to the weights, and m is the maximum of s + e,
+// so that the weights 2^(s+e-m) are at most 1 whatever the scales' range
+// (l sums 2^(s-m), and the difference cancels in o / l).  BF16 queries get a
+// power of two for each row that brings them into FP16's range.
 //
 // What bounds it: HBM.  A tile of 16 rows does 64 operations a byte of a BF16
-// cache, far below the ridge, so the layout is chosen for bytes in flight: a
-// CTA is four warps, each with its own ring of stages of 16 keys (K and V)
-// in shared memory filled by its own 16-byte cp.async copies, and no barrier
-// between warps until an item ends.  The query heads that share a kv head are
-// rows of one tile, so the cache is read once for all of them.
+// cache, far below the ridge, so the layout is chosen for bytes in flight and
+// few instructions a byte: a CTA is four warps, each with its own ring of
+// stages of 16 keys (K and V) in shared memory filled by its own 16-byte
+// cp.async copies, and no barrier between warps until an item ends.  The query
+// heads that share a kv head are rows of one tile, so the cache is read once
+// for all of them; tiles of up to 8 rows have kernels of their own, which hold
+// half the sums.
 #include <algorithm>
 #include <atomic>
 
@@ -24,20 +31,25 @@ namespace {
 constexpr int kUnit = 64;      // keys of a unit: 16 for each of the four warps
 constexpr int kWarps = 4;
 constexpr int kKeys = 16;      // keys of a stage
-constexpr int kMinUnits = 4;   // least share of a CTA
-constexpr uint32_t kStepCtas = 304;  // two on each of 152 SMs
+constexpr int kMinUnits = 2;   // least share of a CTA
+constexpr uint32_t kStepCtas = 456;  // three on each of 152 SMs, at most
 
-__device__ __forceinline__ void mma_16816(bool half, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if (half)
+// d += a b over 16 rows, or (UP false) over the tile's first 8, whose sums are
+// d[0] and d[1] alone.
+template <bool HALF, bool UP>
+__device__ __forceinline__ void mma_16816(float* d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    float u2 = UP ? d[UP ? 2 : 0] : 0.f, u3 = UP ? d[UP ? 3 : 0] : 0.f;
+    if (HALF)
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "+f"(d[0]), "+f"(d[1]), "+f"(u2), "+f"(u3)
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "+f"(d[0]), "+f"(d[1]), "+f"(u2), "+f"(u3)
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (UP) d[UP ? 2 : 0] = u2, d[UP ? 3 : 0] = u3;
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
@@ -64,30 +76,35 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// FMT 0: cache of the queries' 16-bit type, 1: E5M2, 2: E4M3.
-template <int FMT, bool H, int D>
+// FMT 0: cache of the queries' 16-bit type (FP16 with H, else BF16), 1: E5M2,
+// 2: E4M3 (queries of either type).  ROWS: rows of a tile, 8 or 16.
+template <int FMT, bool H, int D, int ROWS>
 struct Step {
     static constexpr bool kFp8 = FMT != 0;
     static constexpr bool kE5M2 = FMT == 1;
-    // P and V are multiplied in FP16 where the cache is FP16, else in BF16: FP8
-    // values are exact in it, and weights times V's scales keep their range.
-    static constexpr bool kPvHalf = !kFp8 && H;
+    static constexpr bool kUp = ROWS == 16;
+    static constexpr int kRowsLane = ROWS / 8;         // rows of a lane: g, and g + 8
+    static constexpr bool kHalf = kFp8 || H;           // products in FP16, else BF16
     // FP16 weights are 2^14 times the exponentials (at most 1), so that those
     // down to 2^-28 keep all bits; the factor cancels in o / l.
-    static constexpr float kShift = kPvHalf ? 14.f : 0.f;
+    static constexpr float kShift = kHalf ? 14.f : 0.f;
     static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
     static constexpr int kChunks = kRowBytes / 16;     // 16-byte pieces of a row
     static constexpr int kRowsACopy = 32 / kChunks;    // rows a warp copies with one instruction
     static constexpr int kCopies = kKeys / kRowsACopy;
     static constexpr int kSideBytes = kKeys * kRowBytes;
     static constexpr int kStageBytes = 2 * kSideBytes;
-    static constexpr int kStages = 24576 / kStageBytes > 8 ? 8 : 24576 / kStageBytes;
+    // Bytes in flight: three CTAs an SM of 16 KB rings a warp, or (stages of
+    // 8 KB) two of 24 KB.
+    static constexpr int kCtasPerSm = kStageBytes > 4096 ? 2 : 3;
+    static constexpr int kStages = kStageBytes > 4096 ? 3 : 16384 / kStageBytes;
     static constexpr int kRing = kStages * kStageBytes;  // a warp's
-    static constexpr int kScaleSlots = kFp8 ? kStages * kKeys * 8 : 0;
-    static constexpr int kMergeBytes = kWarps * kStepRows * (D + 2) * 4;
+    static constexpr int kScaleBytes = kFp8 ? kStages * 2 * kKeys : 0;  // of K and V for a stage's keys
+    static constexpr int kMergeBytes = kWarps * ROWS * (D + 2) * 4;
     static constexpr int kRingBytes = kWarps * kRing > kMergeBytes ? kWarps * kRing : kMergeBytes;
-    static constexpr int kSmem = kRingBytes + kWarps * kScaleSlots;
-    static constexpr int kPartFloats = kStepRows * (D + 2);
+    static constexpr int kJoinBytes = kWarps * int(kStepCtas) * 4;  // a factor for each part of a warp's row
+    static constexpr int kSmem = kRingBytes + kWarps * kScaleBytes;
+    static_assert(kRingBytes >= kJoinBytes, "join");
 
     // Where piece c of key row r lies in its side of a stage: permuted within
     // 128-byte lines so that each access below meets every bank once.
@@ -126,9 +143,10 @@ __device__ __forceinline__ bool special16(const uint4& x) {
     return any;
 }
 
-template <int FMT, bool H, int D>
-__global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_constant__ AttentionArgs a) {
-    using S = Step<FMT, H, D>;
+template <int FMT, bool H, int D, int ROWS>
+__global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm)
+    kv_step_kernel(const __grid_constant__ AttentionArgs a) {
+    using S = Step<FMT, H, D, ROWS>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_scan[kWarps + 1];
     __shared__ uint32_t s_last;
@@ -136,12 +154,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
     const int g = int(lane >> 2), t4 = int(lane & 3u);
     uint8_t* ring = smem + warp * S::kRing;
     const uint32_t ring_u32 = smem_u32(ring);
-    int64_t* scale_ring = reinterpret_cast<int64_t*>(smem + S::kRingBytes + warp * S::kScaleSlots);
+    uint8_t* scale_ring = smem + S::kRingBytes + warp * S::kScaleBytes;
     const uint32_t kv_heads = a.c.kv_heads;
+    // whether a stage's 16 keys are one page's (their rows a stride apart, their scales 16 bytes in a row)
+    const bool one_page = a.c.page_shift >= 4 && (!S::kFp8 || ((reinterpret_cast<uintptr_t>(a.c.k_scale) |
+                                                               reinterpret_cast<uintptr_t>(a.c.v_scale)) & 15u) == 0);
     bool bad = false;
 
     // A sequence's units: those of all its rows' keys, for each kv head and row tile.
-    const auto tiles_of = [&](const KvSeq& s) { return (s.t * int(a.group) + kStepRows - 1) / kStepRows; };
+    const auto tiles_of = [&](const KvSeq& s) { return (s.t * int(a.group) + ROWS - 1) / ROWS; };
     const auto weight_of = [&](uint32_t b) -> uint64_t {
         const KvSeq s = load_seq(a.b, b);
         bad |= !s.ok;
@@ -218,8 +239,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
         const uint64_t item = (u - b_start) / uint32_t(per_item);
         const uint64_t item_start = b_start + item * uint32_t(per_item), item_end = item_start + uint32_t(per_item);
         const uint32_t head = uint32_t(item % kv_heads);
-        const int row_first = int(item / kv_heads) * kStepRows;
-        const int rows = min(kStepRows, s.t * int(a.group) - row_first);
+        const int row_first = int(item / kv_heads) * ROWS;
+        const int rows = min(ROWS, s.t * int(a.group) - row_first);
         const uint64_t stop = item_end < end ? item_end : end;
         const int n_units = int(stop - u);
         const int i0 = row_first / int(a.group), i1 = (row_first + rows - 1) / int(a.group);
@@ -228,9 +249,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
 
         // queries, as the first operand of the products: rows g and g + 8
         uint32_t q[D / 16][4];
-        KeyRange see[2];
+        KeyRange see[S::kRowsLane];
+        float row_scale[S::kRowsLane];
 #pragma unroll
         for (int r2 = 0; r2 < 2; ++r2) {
+            if (r2 >= S::kRowsLane) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) q[k][1] = q[k][3] = 0u;
+                break;
+            }
             const int r = g + 8 * r2;
             const bool there = r < rows;
             const int i = (row_first + (there ? r : 0)) / int(a.group);
@@ -246,187 +273,258 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
                 q[k][r2] = there ? *reinterpret_cast<const uint32_t*>(src + d0) : 0u;
                 q[k][r2 + 2] = there ? *reinterpret_cast<const uint32_t*>(src + d1) : 0u;
             }
+            row_scale[r2] = a.scale_log2;
+            if (S::kFp8 && !a.q_half) {
+                // BF16 to FP16 by way of the power of two that brings the row's largest
+                // finite element to [2^14, 2^15): what FP16 loses of the small ones is
+                // below 2^-39 of it
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int y = 0; y < 4; y += 2) {
+                        const uint32_t lo = q[k][r2 + y] & 0x7FFFu, hi = (q[k][r2 + y] >> 16) & 0x7FFFu;
+                        top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                    }
+                top = max(top, __shfl_xor_sync(~0u, top, 1));
+                top = max(top, __shfl_xor_sync(~0u, top, 2));
+                // 2^up takes exponent e to 14, within what one normal factor can do
+                const int e = int(top >> 7) - 127, up = min(126, 14 - e);
+                const float f = __uint_as_float(uint32_t(127 + up) << 23);
+                row_scale[r2] *= __uint_as_float(uint32_t(127 - up) << 23);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int y = 0; y < 4; y += 2) {
+                        const float2 v = bf16x2_to_float2(q[k][r2 + y]);
+                        q[k][r2 + y] = pack_half2(v.x * f, v.y * f);
+                    }
+            }
         }
+        // positions that every row of the tile sees
+        const KeyRange each{visible(a, s, i1).lo, visible(a, s, i0).hi};
 
-        float o[D / 8][4];
+        float o[D / 8][2 * S::kRowsLane];
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int e = 0; e < 2 * S::kRowsLane; ++e) o[j][e] = 0.f;
+        float m[S::kRowsLane], l[S::kRowsLane];
+#pragma unroll
+        for (int r = 0; r < S::kRowsLane; ++r) m[r] = -INFINITY, l[r] = 0.f;
 
-        // Lane i (mod 16) looks up key i of a stage: its page one stage ahead of
-        // its copies, which start kStages - 1 stages ahead of their use.
+        // Copies start kStages - 1 stages ahead of their use, and the page of a
+        // stage's keys is looked up a stage before that: by lane i (mod 16) for key
+        // i, or where a stage is one page's, by all lanes alike.
         const int32_t* table = a.b.table + uint64_t(b) * a.b.table_stride;
-        const uint32_t key = lane & 15u;
+        const uint32_t key = lane & 15u, slots = (1u << a.c.page_shift) - 1u;
+        const uint32_t copy_row = lane / S::kChunks, copy_col = lane % S::kChunks;
+        const uint64_t copy_off = uint64_t(copy_row) * a.c.token_stride + copy_col * 16u;
+        const uint64_t head_off = uint64_t(head) * a.c.head_stride;
         const auto page_of = [&](int i) -> int32_t {
-            const int pos = base + i * kUnit + int(key);
-            if (i >= n_units || pos < keys.lo || pos >= keys.hi) return -1;
-            const int32_t pg = table[uint32_t(pos) >> a.c.page_shift];
+            const int pos = base + i * kUnit + (one_page ? 0 : int(key));
+            if (i >= n_units || pos + (one_page ? kKeys : 1) <= keys.lo || pos >= keys.hi) return -1;
+            const int32_t pg = __ldg(table + (uint32_t(pos) >> a.c.page_shift));
             if (pg < 0 || uint64_t(pg) >= a.c.pool_pages) {
                 bad = true;
                 return -1;
             }
             return pg;
         };
+        // small pages: a key's scales, loaded with its copies and put into the ring a stage later
+        uint32_t late_scale = 0, late_stage = 0;
+        bool late = false;
         const auto start_stage = [&](int i, int32_t page) {
-            const int pos = base + i * kUnit + int(key);
-            const uint32_t slot = uint32_t(pos) & ((1u << a.c.page_shift) - 1u);
-            const int64_t off = page < 0 ? -1
-                                         : int64_t(uint64_t(uint32_t(page)) * a.c.page_stride +
-                                                   uint64_t(slot) * a.c.token_stride + uint64_t(head) * a.c.head_stride);
+            const int pos0 = base + i * kUnit;
             const uint32_t stage = uint32_t(i) % S::kStages;
             const uint32_t dst = ring_u32 + stage * S::kStageBytes;
             if (i < n_units) {
+                if (one_page) {
+                    const uint64_t at = page < 0 ? 0
+                                                 : uint64_t(uint32_t(page)) * a.c.page_stride +
+                                                       uint64_t(uint32_t(pos0) & slots) * a.c.token_stride + head_off +
+                                                       copy_off;
+                    const uint8_t *k_from = a.c.k + at, *v_from = a.c.v + at;
+                    const uint64_t step = page < 0 ? 0 : uint64_t(S::kRowsACopy) * a.c.token_stride;
 #pragma unroll
-                for (int j = 0; j < S::kCopies; ++j) {
-                    const uint32_t r = uint32_t(j) * S::kRowsACopy + lane / S::kChunks, c = lane % S::kChunks;
-                    const int64_t at = __shfl_sync(~0u, off, int(r));
-                    const int64_t from = (at < 0 ? 0 : at) + int64_t(c) * 16;
-                    copy16(dst + S::place_k(r, c), a.c.k + from, at >= 0);
-                    copy16(dst + S::kSideBytes + S::place_v(r, c), a.c.v + from, at >= 0);
+                    for (int j = 0; j < S::kCopies; ++j) {
+                        const uint32_t r = uint32_t(j) * S::kRowsACopy + copy_row;
+                        const int pos = pos0 + int(r);
+                        const bool there = page >= 0 && pos >= keys.lo && pos < keys.hi;
+                        copy16(dst + S::place_k(r, copy_col), there ? k_from : a.c.k, there);
+                        copy16(dst + S::kSideBytes + S::place_v(r, copy_col), there ? v_from : a.c.v, there);
+                        k_from += step;
+                        v_from += step;
+                    }
+                    if (S::kFp8 && lane < 2) {
+                        const uint64_t sc = page < 0 ? 0
+                                                     : ((uint64_t(uint32_t(page)) * kv_heads + head) << a.c.page_shift) +
+                                                           (uint32_t(pos0) & slots);
+                        copy16(smem_u32(scale_ring) + (stage * 2 + lane) * kKeys, (lane ? a.c.v_scale : a.c.k_scale) + sc,
+                               page >= 0);
+                    }
+                } else {
+                    const uint32_t slot = uint32_t(pos0 + int(key)) & slots;
+                    const int64_t off = page < 0 ? -1
+                                                 : int64_t(uint64_t(uint32_t(page)) * a.c.page_stride +
+                                                           uint64_t(slot) * a.c.token_stride + head_off);
+#pragma unroll
+                    for (int j = 0; j < S::kCopies; ++j) {
+                        const uint32_t r = uint32_t(j) * S::kRowsACopy + copy_row;
+                        const int64_t at = __shfl_sync(~0u, off, int(r));
+                        const int64_t from = (at < 0 ? 0 : at) + int64_t(copy_col) * 16;
+                        copy16(dst + S::place_k(r, copy_col), a.c.k + from, at >= 0);
+                        copy16(dst + S::kSideBytes + S::place_v(r, copy_col), a.c.v + from, at >= 0);
+                    }
                 }
-                if (S::kFp8 && lane < 16)
-                    scale_ring[stage * kKeys + key] =
-                        page < 0 ? -1
-                                 : int64_t(((uint64_t(uint32_t(page)) * kv_heads + head) << a.c.page_shift) + slot);
+            }
+            if (S::kFp8 && !one_page) {
+                if (late) scale_ring[late_stage * 2 * kKeys + lane] = uint8_t(late_scale);
+                late = i < n_units;
+                late_stage = stage;
+                late_scale = 0;
+                if (page >= 0)
+                    late_scale = (lane < 16 ? a.c.k_scale : a.c.v_scale)[((uint64_t(uint32_t(page)) * kv_heads + head)
+                                                                          << a.c.page_shift) +
+                                                                         (uint32_t(pos0 + int(key)) & slots)];
             }
             copy_commit();
         };
-        // lanes 0 .. 15: K's scale of key `lane`; 16 .. 31: V's
-        const auto scale_of = [&](int i) -> float {
-            if (!S::kFp8 || i >= n_units) return 0.f;
-            const int64_t at = scale_ring[uint32_t(i) % S::kStages * kKeys + key];
-            return at < 0 ? 0.f : scale_value((lane < 16 ? a.c.k_scale : a.c.v_scale)[at]);
-        };
-        int32_t page = page_of(0);
+        int32_t page = page_of(0), page_next = page_of(1);
         for (int i = 0; i < S::kStages - 1; ++i) {
-            const int32_t next = page_of(i + 1);
             start_stage(i, page);
-            page = next;
+            page = page_next;
+            page_next = page_of(i + 2);
         }
-        __syncwarp();
-        float scale_next = scale_of(0);
 
         for (int i = 0; i < n_units; ++i) {
             copy_wait<S::kStages - 2>();
             __syncwarp();
-            {
-                const int32_t next = page_of(i + S::kStages);
-                start_stage(i + S::kStages - 1, page);
-                page = next;
-            }
-            __syncwarp();
-            const float scale_now = scale_next;
-            scale_next = scale_of(i + 1);
+            start_stage(i + S::kStages - 1, page);
+            page = page_next;
+            page_next = page_of(i + S::kStages + 1);
             uint8_t* stage = ring + uint32_t(i) % S::kStages * S::kStageBytes;
             uint8_t* v_stage = stage + S::kSideBytes;
             const uint32_t k_at = smem_u32(stage), v_at = smem_u32(v_stage);
             const int pos0 = base + i * kUnit;
 
-            // scores of 16 rows by 16 keys
-            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            // scores of the rows by 16 keys
+            float sc[2][2 * S::kRowsLane];
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2 * S::kRowsLane; ++e) sc[nb][e] = 0.f;
             if (!S::kFp8) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t kr[4];
                     ldmatrix4(kr, k_at + S::place_k((lane & 7u) + (lane >> 4) * 8u, 2u * k + ((lane >> 3) & 1u)));
-                    mma_16816(H, sc[0], q[k], kr[0], kr[1]);
-                    mma_16816(H, sc[1], q[k], kr[2], kr[3]);
+                    mma_16816<S::kHalf, S::kUp>(sc[0], q[k], kr[0], kr[1]);
+                    mma_16816<S::kHalf, S::kUp>(sc[1], q[k], kr[2], kr[3]);
                 }
             } else {
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
+                for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
+                    for (int nb = 0; nb < 2; ++nb) {
                         const uint4 w4 = *reinterpret_cast<const uint4*>(
                             stage + S::place_k(uint32_t(nb * 8 + g), uint32_t(c * 4 + t4)));
                         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t b0 = H ? fp8x2_to_half2<S::kE5M2>(w[j]) : fp8x2_to_bf16x2<S::kE5M2>(w[j]);
-                            const uint32_t b1 =
-                                H ? fp8x2_to_half2<S::kE5M2>(w[j] >> 16) : fp8x2_to_bf16x2<S::kE5M2>(w[j] >> 16);
-                            mma_16816(H, sc[nb], q[c * 4 + j], b0, b1);
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            mma_16816<S::kHalf, S::kUp>(sc[nb], q[c * 4 + j], fp8x2_to_half2<S::kE5M2>(w[j]),
+                                                        fp8x2_to_half2<S::kE5M2>(w[j] >> 16));
+                    }
+            }
+            // scales of the lane's four keys; V's also as exponents
+            float ks[4], vs[4], ve[4];
+            if (S::kFp8) {
+                const uint8_t* at = scale_ring + uint32_t(i) % S::kStages * 2 * kKeys + 2 * t4;
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                    const uint32_t k2 = *reinterpret_cast<const uint16_t*>(at + 4 * x);
+                    const uint32_t v2 = *reinterpret_cast<const uint16_t*>(at + kKeys + 4 * x);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t kb = (k2 >> (8 * y)) & 0xFFu;
+                        // a slot that nothing was written to may hold 255
+                        const uint32_t vb = min((v2 >> (8 * y)) & 0xFFu, 254u);
+                        ks[x + y] = scale_value(kb);
+                        vs[x + y] = scale_value(vb);
+                        // at least -80, which bounds the sums of 2^(s-m)
+                        ve[x + y] = __uint_as_float(0x4B000000u | max(vb, 47u)) - 8388735.f;
                     }
                 }
             }
-            float ks[4], vs[4];  // scales of the lane's four keys
-            if (S::kFp8) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int src = (x >> 1) * 8 + 2 * t4 + (x & 1);
-                    ks[x] = __shfl_sync(~0u, scale_now, src);
-                    vs[x] = __shfl_sync(~0u, scale_now, src + 16);
-                }
-            }
             // scale, mask, running maximum
-            float top[2] = {-INFINITY, -INFINITY};
+            const bool masked = pos0 < each.lo || pos0 + kKeys > each.hi;
+            float top[S::kRowsLane];
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
+            for (int r = 0; r < S::kRowsLane; ++r) {
+                top[r] = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int pos = pos0 + nb * 8 + 2 * t4 + (e & 1);
-                    const KeyRange& r = see[e >> 1];
-                    float x = sc[nb][e] * a.scale_log2;
-                    if (S::kFp8) x *= ks[nb * 2 + (e & 1)];
-                    x = pos >= r.lo && pos < r.hi ? x : -INFINITY;
-                    sc[nb][e] = x;
-                    top[e >> 1] = fmaxf(top[e >> 1], x);
-                }
+                for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = sc[nb][2 * r + e] * row_scale[r];
+                        if (S::kFp8) x *= ks[nb * 2 + e];
+                        if (masked) {
+                            const int pos = pos0 + nb * 8 + 2 * t4 + e;
+                            x = pos >= see[r].lo && pos < see[r].hi ? x : -INFINITY;
+                        }
+                        sc[nb][2 * r + e] = x;
+                        top[r] = fmaxf(top[r], S::kFp8 ? x + ve[nb * 2 + e] : x);
+                    }
+            }
             bool grew = false;
-            float low[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int r = 0; r < S::kRowsLane; ++r) {
                 top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
                 top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
-                top[r] = fmaxf(top[r], m[r]);
                 grew |= top[r] > m[r];
             }
             if (__any_sync(~0u, grew)) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float f = top[r] == m[r] ? 1.f : exp2_fast(m[r] - top[r]);
+                for (int r = 0; r < S::kRowsLane; ++r) {
+                    const float now = fmaxf(top[r], m[r]);
+                    const float f = now == m[r] ? 1.f : exp2_fast(m[r] - now);
                     l[r] *= f;
 #pragma unroll
                     for (int j = 0; j < D / 8; ++j) {
                         o[j][2 * r] *= f;
                         o[j][2 * r + 1] *= f;
                     }
-                    m[r] = top[r];
+                    m[r] = now;
                 }
             }
+            uint32_t p[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int r = 0; r < 2; ++r) low[r] = m[r] == -INFINITY ? 0.f : m[r] - S::kShift;
-            uint32_t p[4];
+            for (int r = 0; r < S::kRowsLane; ++r) {
+                const float low = m[r] == -INFINITY ? 0.f : m[r] - S::kShift;
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sc[nb][e] = exp2_fast(sc[nb][e] - low[e >> 1]);
-                    l[e >> 1] += sc[nb][e];
-                    if (S::kFp8) sc[nb][e] *= vs[nb * 2 + (e & 1)];
+                for (int nb = 0; nb < 2; ++nb) {
+                    float e0 = exp2_fast(sc[nb][2 * r] - low), e1 = exp2_fast(sc[nb][2 * r + 1] - low);
+                    l[r] += e0 + e1;
+                    if (S::kFp8) {
+                        e0 *= vs[nb * 2];
+                        e1 *= vs[nb * 2 + 1];
+                    }
+                    p[nb * 2 + r] = S::kHalf ? pack_half2(e0, e1) : pack_bf16x2(e0, e1);
                 }
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    p[nb * 2 + r] = S::kPvHalf ? pack_half2(sc[nb][2 * r], sc[nb][2 * r + 1])
-                                               : pack_bf16x2(sc[nb][2 * r], sc[nb][2 * r + 1]);
             }
 
             // A weight of 0 hides a finite value, not an infinity or a NaN.  Where some
             // row does not see all the keys of this stage, such values of V are
             // taken out and given to the rows that do see them.
             const int k0 = max(pos0, keys.lo), k1 = min(pos0 + kKeys, keys.hi);
-            const bool partial = k0 < k1 && ((g < rows && (see[0].lo > k0 || see[0].hi < k1)) ||
-                                             (g + 8 < rows && (see[1].lo > k0 || see[1].hi < k1)));
-            if (__any_sync(~0u, partial)) {
+            if (masked && k0 < k1 && (each.lo > k0 || each.hi < k1)) {
                 bool special = false;
 #pragma unroll
                 for (int j = 0; j < S::kCopies; ++j)
                     special |= special16<FMT, H>(
                         *reinterpret_cast<const uint4*>(v_stage + (uint32_t(j) * 32u + lane) * 16u));
                 if (__any_sync(~0u, special)) {
+#pragma unroll 1
                     for (int x = 0; x < kKeys; ++x) {
                         const int pos = pos0 + x;
 #pragma unroll
@@ -444,7 +542,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
                                     v = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
                                 if (!(fabsf(v) < INFINITY)) {
 #pragma unroll
-                                    for (int r = 0; r < 2; ++r)
+                                    for (int r = 0; r < S::kRowsLane; ++r)
                                         if (pos >= see[r].lo && pos < see[r].hi) o[j][2 * r + e] += v;
                                 }
                             }
@@ -477,8 +575,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
                 for (int j = 0; j < D / 16; ++j) {
                     uint32_t vr[4];
                     ldmatrix4_trans(vr, v_at + S::place_v((lane & 7u) + ((lane >> 3) & 1u) * 8u, 2u * j + (lane >> 4)));
-                    mma_16816(S::kPvHalf, o[2 * j], p, vr[0], vr[1]);
-                    mma_16816(S::kPvHalf, o[2 * j + 1], p, vr[2], vr[3]);
+                    mma_16816<S::kHalf, S::kUp>(o[2 * j], p, vr[0], vr[1]);
+                    mma_16816<S::kHalf, S::kUp>(o[2 * j + 1], p, vr[2], vr[3]);
                 }
             } else {
                 // the lane's D / 8 bytes of each of its four keys
@@ -504,10 +602,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
                         const uint32_t sel = h2 ? 0x7362u : 0x5140u;
                         const uint32_t ab = __byte_perm(w[0][y], w[1][y], sel);
                         const uint32_t cd = __byte_perm(w[2][y], w[3][y], sel);
-                        mma_16816(S::kPvHalf, o[4 * y + 2 * h2], p, fp8x2_to_bf16x2<S::kE5M2>(ab),
-                                  fp8x2_to_bf16x2<S::kE5M2>(cd));
-                        mma_16816(S::kPvHalf, o[4 * y + 2 * h2 + 1], p, fp8x2_to_bf16x2<S::kE5M2>(ab >> 16),
-                                  fp8x2_to_bf16x2<S::kE5M2>(cd >> 16));
+                        mma_16816<S::kHalf, S::kUp>(o[4 * y + 2 * h2], p, fp8x2_to_half2<S::kE5M2>(ab),
+                                                    fp8x2_to_half2<S::kE5M2>(cd));
+                        mma_16816<S::kHalf, S::kUp>(o[4 * y + 2 * h2 + 1], p, fp8x2_to_half2<S::kE5M2>(ab >> 16),
+                                                    fp8x2_to_half2<S::kE5M2>(cd >> 16));
                     }
             }
         }
@@ -515,13 +613,13 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
 
         // Join the four warps.  The sums l are still one quad lane's; m is the row's.
         __syncthreads();
-        float* m_o = reinterpret_cast<float*>(smem);               // [warp][row][D]
-        float* m_ml = m_o + kWarps * kStepRows * D;                // [warp][row][m, l]
+        float* m_o = reinterpret_cast<float*>(smem);      // [warp][row][D]
+        float* m_ml = m_o + kWarps * ROWS * D;            // [warp][row][m, l]
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < S::kRowsLane; ++r) {
             l[r] += __shfl_xor_sync(~0u, l[r], 1);
             l[r] += __shfl_xor_sync(~0u, l[r], 2);
-            const int row = int(warp) * kStepRows + g + 8 * r;
+            const int row = int(warp) * ROWS + g + 8 * r;
             if (t4 == 0) {
                 m_ml[2 * row] = m[r];
                 m_ml[2 * row + 1] = l[r];
@@ -532,87 +630,100 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
                 for (int e = 0; e < 2; ++e) m_o[row * D + S::out_dim(j, t4, e)] = o[j][2 * r + e];
         }
         __syncthreads();
-        // eight threads a row, D / 8 columns each
-        constexpr int W = D / 8;
-        const int row = int(tid >> 3), col = int(tid & 7u) * W;
-        float mm = -INFINITY, ll = 0.f, acc[W];
-#pragma unroll
-        for (int x = 0; x < W; ++x) acc[x] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, m_ml[2 * (w * kStepRows + row)]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float mw = m_ml[2 * (w * kStepRows + row)];
-            const float f = mw == mm ? 1.f : exp2_fast(mw - mm);
-            ll += f * m_ml[2 * (w * kStepRows + row) + 1];
-#pragma unroll
-            for (int x = 0; x < W; ++x) acc[x] += f * m_o[(w * kStepRows + row) * D + col + x];
-        }
-        bool write = true;
-        if (u > item_start || stop < item_end) {
-            // a part of the item
-            const uint32_t first = share_of(units, ctas, item_start), last = share_of(units, ctas, item_end - 1);
-            const auto slot = [&](uint32_t c) {
-                return a.parts + (uint64_t(c) * 2 + (c == first ? 1 : 0)) * S::kPartFloats;
-            };
-            float* mine = slot(blockIdx.x);
-            wait_predecessor();  // the counters are clear
-            if (row < rows) {
-                if (col == 0) {
-                    mine[2 * row] = mm;
-                    mine[2 * row + 1] = ll;
-                }
-#pragma unroll
-                for (int x = 0; x < W; x += 4)
-                    *reinterpret_cast<float4*>(mine + 2 * kStepRows + row * D + col + x) =
-                        make_float4(acc[x], acc[x + 1], acc[x + 2], acc[x + 3]);
-            }
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) s_last = atomicAdd(a.counters + first, 1u) == last - first;
-            __syncthreads();
-            write = s_last != 0;
-            if (write && row < rows) {
-                __threadfence();
-                mm = -INFINITY;
-                for (uint32_t c = first; c <= last; ++c) mm = fmaxf(mm, __ldcg(slot(c) + 2 * row));
-                ll = 0.f;
-#pragma unroll
-                for (int x = 0; x < W; ++x) acc[x] = 0.f;
-#pragma unroll 2
-                for (uint32_t c = first; c <= last; ++c) {
-                    const float* part = slot(c);
-                    const float mw = __ldcg(part + 2 * row);
-                    const float f = mw == mm ? 1.f : exp2_fast(mw - mm);
-                    ll += f * __ldcg(part + 2 * row + 1);
-#pragma unroll
-                    for (int x = 0; x < W; x += 4) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(part + 2 * kStepRows + row * D + col + x));
-                        acc[x] += f * y.x;
-                        acc[x + 1] += f * y.y;
-                        acc[x + 2] += f * y.z;
-                        acc[x + 3] += f * y.w;
-                    }
-                }
-            }
-        }
-        if (write && row < rows) {
+        const bool whole = u == item_start && stop == item_end;
+        const uint32_t first = whole ? 0u : share_of(units, ctas, item_start);
+        const uint32_t last = whole ? 0u : share_of(units, ctas, item_end - 1);
+        const auto slot = [&](uint32_t c) {
+            return a.parts + (uint64_t(c) * 2 + (c == first ? 1 : 0)) * uint32_t(ROWS * (D + 2));
+        };
+        // `n` (2 or 4) columns of a row's result from col
+        const auto finish = [&](int row, int col, const float* acc, int n, float mm, float ll) {
             const int i = (row_first + row) / int(a.group);
             const uint32_t qh = head * a.group + uint32_t((row_first + row) % int(a.group));
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
             uint16_t* dst = a.out.d + uint64_t(s.row0 + i) * a.out.token_stride + uint64_t(qh) * a.out.head_stride + col;
-#pragma unroll
-            for (int x = 0; x < W; x += 8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    w[y] = H ? pack_half2(acc[x + 2 * y] * inv, acc[x + 2 * y + 1] * inv)
-                             : pack_bf16x2(acc[x + 2 * y] * inv, acc[x + 2 * y + 1] * inv);
-                *reinterpret_cast<uint4*>(dst + x) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            const bool half = S::kFp8 ? a.q_half != 0 : H;
+            for (int y = 0; y < n; y += 2)
+                *reinterpret_cast<uint32_t*>(dst + y) =
+                    half ? pack_half2(acc[y] * inv, acc[y + 1] * inv) : pack_bf16x2(acc[y] * inv, acc[y + 1] * inv);
             if (a.lse && col == 0)
                 a.lse[uint64_t(s.row0 + i) * a.q_heads + qh] =
                     ll == 0.f ? -INFINITY : (mm - S::kShift + log2f(ll)) * 0.693147180559945309f;
+        };
+        // four columns a thread and turn, a row's on one after another
+        if (!whole) wait_predecessor();  // the counters are clear
+        for (int x = int(tid) * 4; x < rows * D; x += kWarps * 32 * 4) {
+            const int row = x / D, col = x % D;
+            float mm = -INFINITY, ll = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, m_ml[2 * (w * ROWS + row)]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = m_ml[2 * (w * ROWS + row)];
+                const float f = mw == mm ? 1.f : exp2_fast(mw - mm);
+                const float4 y = *reinterpret_cast<const float4*>(m_o + (w * ROWS + row) * D + col);
+                ll += f * m_ml[2 * (w * ROWS + row) + 1];
+                acc.x += f * y.x, acc.y += f * y.y, acc.z += f * y.z, acc.w += f * y.w;
+            }
+            if (whole) {
+                const float four[4] = {acc.x, acc.y, acc.z, acc.w};
+                finish(row, col, four, 4, mm, ll);
+            } else {
+                float* part = slot(blockIdx.x);
+                if (col == 0) *reinterpret_cast<float2*>(part + 2 * row) = make_float2(mm, ll);
+                *reinterpret_cast<float4*>(part + 2 * ROWS + x) = acc;
+            }
+        }
+        if (!whole) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atomicAdd(a.counters + first, 1u) == last - first;
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                // a warp a row: the parts' factors, then its columns, D / 32 a lane
+                const int parts = int(last - first) + 1;
+                float* factor = reinterpret_cast<float*>(smem) + warp * kStepCtas;
+                for (int row = int(warp); row < rows; row += kWarps) {
+                    float mm = -INFINITY;
+                    for (int c = int(lane); c < parts; c += 32) {
+                        const float mc = __ldcg(slot(first + uint32_t(c)) + 2 * row);
+                        factor[c] = mc;
+                        mm = fmaxf(mm, mc);
+                    }
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
+                    float ll = 0.f;
+                    for (int c = int(lane); c < parts; c += 32) {
+                        const float f = factor[c] == mm ? 1.f : exp2_fast(factor[c] - mm);
+                        factor[c] = f;
+                        ll += f * __ldcg(slot(first + uint32_t(c)) + 2 * row + 1);
+                    }
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(~0u, ll, d);
+                    __syncwarp();
+                    constexpr int W = D / 32;
+                    const int col = int(lane) * W;
+                    float acc[W];
+#pragma unroll
+                    for (int y = 0; y < W; ++y) acc[y] = 0.f;
+#pragma unroll 8
+                    for (int c = 0; c < parts; ++c) {
+                        const float f = factor[c];
+                        const float* from = slot(first + uint32_t(c)) + 2 * ROWS + row * D + col;
+                        if (W == 4) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4*>(from));
+                            acc[0] += f * y.x, acc[1] += f * y.y, acc[W - 2] += f * y.z, acc[W - 1] += f * y.w;
+                        } else {
+                            const float2 y = __ldcg(reinterpret_cast<const float2*>(from));
+                            acc[0] += f * y.x, acc[1] += f * y.y;
+                        }
+                    }
+                    finish(row, col, acc, W, mm, ll);
+                    __syncwarp();
+                }
+            }
         }
         __syncthreads();  // the ring is free again
         u = stop;
@@ -621,23 +732,24 @@ __global__ void __launch_bounds__(kWarps * 32) kv_step_kernel(const __grid_const
     if (bad) report(a.status, SPLITZIP_ERR_INVALID_ARG);
 }
 
-template <int FMT, bool H, int D>
+template <int FMT, bool H, int D, int ROWS>
 int launch(const AttentionArgs& a, uint32_t ctas, cudaStream_t s) {
-    using S = Step<FMT, H, D>;
+    using S = Step<FMT, H, D, ROWS>;
     // every device once: the kernel's shared memory limit
     static std::atomic<uint64_t> ready{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SPLITZIP_ERR_CUDA;
     if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1u)) {
-        if (cudaFuncSetAttribute(kv_step_kernel<FMT, H, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
-            cudaSuccess) {
+        if (cudaFuncSetAttribute(kv_step_kernel<FMT, H, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S::kSmem) != cudaSuccess) {
             cudaGetLastError();
             return SPLITZIP_ERR_CUDA;
         }
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     }
-    ChainedLaunch l(dim3(ctas), dim3(kWarps * 32), S::kSmem, s);
-    if (cudaLaunchKernelEx(&l.cfg, kv_step_kernel<FMT, H, D>, a) != cudaSuccess) {
+    // one wave: more CTAs would start when others end and have no even share
+    ChainedLaunch l(dim3(std::min(ctas, uint32_t(S::kCtasPerSm) * 152u)), dim3(kWarps * 32), S::kSmem, s);
+    if (cudaLaunchKernelEx(&l.cfg, kv_step_kernel<FMT, H, D, ROWS>, a) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }
@@ -645,8 +757,10 @@ int launch(const AttentionArgs& a, uint32_t ctas, cudaStream_t s) {
 }
 
 template <int FMT, bool H>
-int launch_dim(const AttentionArgs& a, uint32_t ctas, cudaStream_t s) {
-    return a.c.head_dim == 128 ? launch<FMT, H, 128>(a, ctas, s) : launch<FMT, H, 64>(a, ctas, s);
+int launch_shape(const AttentionArgs& a, uint32_t ctas, cudaStream_t s) {
+    const bool few = uint64_t(a.b.max_tokens) * a.group <= 8;
+    if (a.c.head_dim == 128) return few ? launch<FMT, H, 128, 8>(a, ctas, s) : launch<FMT, H, 128, 16>(a, ctas, s);
+    return few ? launch<FMT, H, 64, 8>(a, ctas, s) : launch<FMT, H, 64, 16>(a, ctas, s);
 }
 
 }  // namespace
@@ -658,11 +772,12 @@ uint32_t step_ctas(uint64_t items_max, uint64_t keys_max) {
     return uint32_t(std::min<uint64_t>(kStepCtas, std::max<uint64_t>(1, (units + kMinUnits - 1) / kMinUnits)));
 }
 
-int launch_kv_step(const AttentionArgs& a, bool q_half, uint32_t ctas, cudaStream_t s) {
+int launch_kv_step(const AttentionArgs& a, uint32_t ctas, cudaStream_t s) {
     switch (a.c.type) {
-        case SPLITZIP_KV_FP8_E5M2: return q_half ? launch_dim<1, true>(a, ctas, s) : launch_dim<1, false>(a, ctas, s);
-        case SPLITZIP_KV_FP8_E4M3: return q_half ? launch_dim<2, true>(a, ctas, s) : launch_dim<2, false>(a, ctas, s);
-        default: return q_half ? launch_dim<0, true>(a, ctas, s) : launch_dim<0, false>(a, ctas, s);
+        case SPLITZIP_KV_FP8_E5M2: return launch_shape<1, false>(a, ctas, s);
+        case SPLITZIP_KV_FP8_E4M3: return launch_shape<2, false>(a, ctas, s);
+        case SPLITZIP_KV_FP16: return launch_shape<0, true>(a, ctas, s);
+        default: return launch_shape<0, false>(a, ctas, s);
     }
 }
 
