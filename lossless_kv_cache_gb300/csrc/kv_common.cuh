@@ -69,6 +69,14 @@ __device__ __forceinline__ uint32_t fp8x2_to_half2(uint32_t two) {
     return r;
 }
 
+// The low (0) or high (1) two FP8 values of a word as FP16, exactly.  An E5M2
+// byte is the upper byte of the FP16 number it stands for.
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8_pair_to_half2(uint32_t word, int which) {
+    if (E5M2) return __byte_perm(word, 0u, which ? 0x3424u : 0x1404u);
+    return fp8x2_to_half2<false>(which ? word >> 16 : word);
+}
+
 // Two floats as an FP8 pair (a in the low byte), rounded to nearest even.
 // Finite values past the largest would saturate; the callers have none.
 template <bool E5M2>

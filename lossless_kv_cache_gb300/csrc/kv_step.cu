@@ -34,22 +34,20 @@ constexpr int kKeys = 16;      // keys of a stage
 constexpr int kMinUnits = 2;   // least share of a CTA
 constexpr uint32_t kStepCtas = 456;  // three on each of 152 SMs, at most
 
-// d += a b over 16 rows, or (UP false) over the tile's first 8, whose sums are
-// d[0] and d[1] alone.
-template <bool HALF, bool UP>
-__device__ __forceinline__ void mma_16816(float* d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    float u2 = UP ? d[UP ? 2 : 0] : 0.f, u3 = UP ? d[UP ? 3 : 0] : 0.f;
+// d += a b over 16 rows (of a tile of 8, the other 8 are zeros in a and stay
+// zeros in d: registers that are always there cost less than clearing them).
+template <bool HALF>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (HALF)
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(u2), "+f"(u3)
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(u2), "+f"(u3)
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    if (UP) d[UP ? 2 : 0] = u2, d[UP ? 3 : 0] = u3;
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
@@ -70,6 +68,9 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -82,7 +83,6 @@ template <int FMT, bool H, int D, int ROWS>
 struct Step {
     static constexpr bool kFp8 = FMT != 0;
     static constexpr bool kE5M2 = FMT == 1;
-    static constexpr bool kUp = ROWS == 16;
     static constexpr int kRowsLane = ROWS / 8;         // rows of a lane: g, and g + 8
     static constexpr bool kHalf = kFp8 || H;           // products in FP16, else BF16
     // FP16 weights are 2^14 times the exponentials (at most 1), so that those
@@ -95,9 +95,9 @@ struct Step {
     static constexpr int kSideBytes = kKeys * kRowBytes;
     static constexpr int kStageBytes = 2 * kSideBytes;
     // Bytes in flight: three CTAs an SM of 16 KB rings a warp, or (stages of
-    // 8 KB) two of 24 KB.
-    static constexpr int kCtasPerSm = kStageBytes > 4096 ? 2 : 3;
-    static constexpr int kStages = kStageBytes > 4096 ? 3 : 16384 / kStageBytes;
+    // 8 KB, or more registers than three CTAs have) two of 24 KB.
+    static constexpr int kCtasPerSm = kStageBytes > 4096 || (ROWS == 16 && kFp8 && D == 128) ? 2 : 3;
+    static constexpr int kStages = (kCtasPerSm == 2 ? 24576 : 16384) / kStageBytes;
     static constexpr int kRing = kStages * kStageBytes;  // a warp's
     static constexpr int kScaleBytes = kFp8 ? kStages * 2 * kKeys : 0;  // of K and V for a stage's keys
     static constexpr int kMergeBytes = kWarps * ROWS * (D + 2) * 4;
@@ -169,6 +169,13 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
         if (s.t == 0) return 0;
         return uint64_t(unit_count(visible(a, s, 0, s.t - 1), kUnit)) * kv_heads * uint32_t(tiles_of(s));
     };
+    // As many CTAs as have kMinUnits each, but one for each item at least.  The
+    // count of items, as far as it matters, rides above the units'.
+    constexpr int kItemsAt = 38;
+    const auto items_of = [&](uint32_t b) -> uint64_t {
+        const KvSeq s = load_seq(a.b, b);
+        return uint64_t(min(uint32_t(kStepCtas), uint32_t(tiles_of(s)) * kv_heads)) << kItemsAt;
+    };
     // Inclusive scan over the CTA's threads of one weight each; s_scan[kWarps]: the total.
     const auto scan = [&](uint64_t w) -> uint64_t {
         uint64_t x = w;
@@ -192,11 +199,13 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
     };
     uint64_t units = 0;
     for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kWarps * 32) {
-        scan(b0 + tid < a.b.batch ? weight_of(b0 + tid) : 0);
+        scan(b0 + tid < a.b.batch ? weight_of(b0 + tid) + items_of(b0 + tid) : 0);
         __syncthreads();
         units += s_scan[kWarps];
     }
-    const uint64_t most = (units + kMinUnits - 1) / kMinUnits;
+    const uint64_t items = units >> kItemsAt;
+    units &= (uint64_t(1) << kItemsAt) - 1;
+    const uint64_t most = max(items, (units + kMinUnits - 1) / kMinUnits);
     const uint32_t ctas = most < gridDim.x ? uint32_t(most) : gridDim.x;
     uint64_t u = 0, end = 0;
     if (blockIdx.x < ctas) {
@@ -304,11 +313,11 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
         // positions that every row of the tile sees
         const KeyRange each{visible(a, s, i1).lo, visible(a, s, i0).hi};
 
-        float o[D / 8][2 * S::kRowsLane];
+        float o[D / 8][4];
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 2 * S::kRowsLane; ++e) o[j][e] = 0.f;
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
         float m[S::kRowsLane], l[S::kRowsLane];
 #pragma unroll
         for (int r = 0; r < S::kRowsLane; ++r) m[r] = -INFINITY, l[r] = 0.f;
@@ -320,6 +329,7 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
         const uint32_t key = lane & 15u, slots = (1u << a.c.page_shift) - 1u;
         const uint32_t copy_row = lane / S::kChunks, copy_col = lane % S::kChunks;
         const uint64_t copy_off = uint64_t(copy_row) * a.c.token_stride + copy_col * 16u;
+        const uint64_t copy_step = uint64_t(S::kRowsACopy) * a.c.token_stride;
         const uint64_t head_off = uint64_t(head) * a.c.head_stride;
         const auto page_of = [&](int i) -> int32_t {
             const int pos = base + i * kUnit + (one_page ? 0 : int(key));
@@ -345,16 +355,23 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                                                        uint64_t(uint32_t(pos0) & slots) * a.c.token_stride + head_off +
                                                        copy_off;
                     const uint8_t *k_from = a.c.k + at, *v_from = a.c.v + at;
-                    const uint64_t step = page < 0 ? 0 : uint64_t(S::kRowsACopy) * a.c.token_stride;
+                    if (page >= 0 && pos0 >= keys.lo && pos0 + kKeys <= keys.hi) {
 #pragma unroll
-                    for (int j = 0; j < S::kCopies; ++j) {
-                        const uint32_t r = uint32_t(j) * S::kRowsACopy + copy_row;
-                        const int pos = pos0 + int(r);
-                        const bool there = page >= 0 && pos >= keys.lo && pos < keys.hi;
-                        copy16(dst + S::place_k(r, copy_col), there ? k_from : a.c.k, there);
-                        copy16(dst + S::kSideBytes + S::place_v(r, copy_col), there ? v_from : a.c.v, there);
-                        k_from += step;
-                        v_from += step;
+                        for (int j = 0; j < S::kCopies; ++j) {
+                            const uint32_t r = uint32_t(j) * S::kRowsACopy + copy_row;
+                            copy16(dst + S::place_k(r, copy_col), k_from + uint64_t(j) * copy_step);
+                            copy16(dst + S::kSideBytes + S::place_v(r, copy_col), v_from + uint64_t(j) * copy_step);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < S::kCopies; ++j) {
+                            const uint32_t r = uint32_t(j) * S::kRowsACopy + copy_row;
+                            const int pos = pos0 + int(r);
+                            const bool there = page >= 0 && pos >= keys.lo && pos < keys.hi;
+                            const uint64_t step = there ? uint64_t(j) * copy_step : 0;
+                            copy16(dst + S::place_k(r, copy_col), k_from + step, there);
+                            copy16(dst + S::kSideBytes + S::place_v(r, copy_col), v_from + step, there);
+                        }
                     }
                     if (S::kFp8 && lane < 2) {
                         const uint64_t sc = page < 0 ? 0
@@ -409,18 +426,18 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
             const int pos0 = base + i * kUnit;
 
             // scores of the rows by 16 keys
-            float sc[2][2 * S::kRowsLane];
+            float sc[2][4];
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-                for (int e = 0; e < 2 * S::kRowsLane; ++e) sc[nb][e] = 0.f;
+                for (int e = 0; e < 4; ++e) sc[nb][e] = 0.f;
             if (!S::kFp8) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t kr[4];
                     ldmatrix4(kr, k_at + S::place_k((lane & 7u) + (lane >> 4) * 8u, 2u * k + ((lane >> 3) & 1u)));
-                    mma_16816<S::kHalf, S::kUp>(sc[0], q[k], kr[0], kr[1]);
-                    mma_16816<S::kHalf, S::kUp>(sc[1], q[k], kr[2], kr[3]);
+                    mma_16816<S::kHalf>(sc[0], q[k], kr[0], kr[1]);
+                    mma_16816<S::kHalf>(sc[1], q[k], kr[2], kr[3]);
                 }
             } else {
 #pragma unroll
@@ -432,8 +449,8 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma_16816<S::kHalf, S::kUp>(sc[nb], q[c * 4 + j], fp8x2_to_half2<S::kE5M2>(w[j]),
-                                                        fp8x2_to_half2<S::kE5M2>(w[j] >> 16));
+                            mma_16816<S::kHalf>(sc[nb], q[c * 4 + j], fp8_pair_to_half2<S::kE5M2>(w[j], 0),
+                                                fp8_pair_to_half2<S::kE5M2>(w[j], 1));
                     }
             }
             // scales of the lane's four keys; V's also as exponents
@@ -446,9 +463,7 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                     const uint32_t v2 = *reinterpret_cast<const uint16_t*>(at + kKeys + 4 * x);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const uint32_t kb = (k2 >> (8 * y)) & 0xFFu;
-                        // a slot that nothing was written to may hold 255
-                        const uint32_t vb = min((v2 >> (8 * y)) & 0xFFu, 254u);
+                        const uint32_t kb = (k2 >> (8 * y)) & 0xFFu, vb = (v2 >> (8 * y)) & 0xFFu;
                         ks[x + y] = scale_value(kb);
                         vs[x + y] = scale_value(vb);
                         // at least -80, which bounds the sums of 2^(s-m)
@@ -458,6 +473,11 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
             }
             // scale, mask, running maximum
             const bool masked = pos0 < each.lo || pos0 + kKeys > each.hi;
+            if (S::kFp8 && masked) {
+                // a slot that nothing was written to may hold 255, and 0 times infinity is NaN
+#pragma unroll
+                for (int x = 0; x < 4; ++x) vs[x] = fminf(vs[x], 1.7014118e38f);
+            }
             float top[S::kRowsLane];
 #pragma unroll
             for (int r = 0; r < S::kRowsLane; ++r) {
@@ -575,8 +595,8 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                 for (int j = 0; j < D / 16; ++j) {
                     uint32_t vr[4];
                     ldmatrix4_trans(vr, v_at + S::place_v((lane & 7u) + ((lane >> 3) & 1u) * 8u, 2u * j + (lane >> 4)));
-                    mma_16816<S::kHalf, S::kUp>(o[2 * j], p, vr[0], vr[1]);
-                    mma_16816<S::kHalf, S::kUp>(o[2 * j + 1], p, vr[2], vr[3]);
+                    mma_16816<S::kHalf>(o[2 * j], p, vr[0], vr[1]);
+                    mma_16816<S::kHalf>(o[2 * j + 1], p, vr[2], vr[3]);
                 }
             } else {
                 // the lane's D / 8 bytes of each of its four keys
@@ -602,10 +622,10 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                         const uint32_t sel = h2 ? 0x7362u : 0x5140u;
                         const uint32_t ab = __byte_perm(w[0][y], w[1][y], sel);
                         const uint32_t cd = __byte_perm(w[2][y], w[3][y], sel);
-                        mma_16816<S::kHalf, S::kUp>(o[4 * y + 2 * h2], p, fp8x2_to_half2<S::kE5M2>(ab),
-                                                    fp8x2_to_half2<S::kE5M2>(cd));
-                        mma_16816<S::kHalf, S::kUp>(o[4 * y + 2 * h2 + 1], p, fp8x2_to_half2<S::kE5M2>(ab >> 16),
-                                                    fp8x2_to_half2<S::kE5M2>(cd >> 16));
+                        mma_16816<S::kHalf>(o[4 * y + 2 * h2], p, fp8_pair_to_half2<S::kE5M2>(ab, 0),
+                                            fp8_pair_to_half2<S::kE5M2>(cd, 0));
+                        mma_16816<S::kHalf>(o[4 * y + 2 * h2 + 1], p, fp8_pair_to_half2<S::kE5M2>(ab, 1),
+                                            fp8_pair_to_half2<S::kE5M2>(cd, 1));
                     }
             }
         }
@@ -708,7 +728,7 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                     float acc[W];
 #pragma unroll
                     for (int y = 0; y < W; ++y) acc[y] = 0.f;
-#pragma unroll 8
+#pragma unroll 16
                     for (int c = 0; c < parts; ++c) {
                         const float f = factor[c];
                         const float* from = slot(first + uint32_t(c)) + 2 * ROWS + row * D + col;
@@ -769,7 +789,8 @@ uint64_t step_part_floats(uint32_t head_dim) { return uint64_t(kStepRows) * (hea
 
 uint32_t step_ctas(uint64_t items_max, uint64_t keys_max) {
     const uint64_t units = items_max * ((keys_max + kUnit - 1) / kUnit + 1);
-    return uint32_t(std::min<uint64_t>(kStepCtas, std::max<uint64_t>(1, (units + kMinUnits - 1) / kMinUnits)));
+    return uint32_t(std::min<uint64_t>(
+        kStepCtas, std::max<uint64_t>(std::max<uint64_t>(1, items_max), (units + kMinUnits - 1) / kMinUnits)));
 }
 
 int launch_kv_step(const AttentionArgs& a, uint32_t ctas, cudaStream_t s) {
