@@ -102,7 +102,7 @@ struct Step {
     static constexpr int kScaleBytes = kFp8 ? kStages * 2 * kKeys : 0;  // of K and V for a stage's keys
     static constexpr int kMergeBytes = kWarps * ROWS * (D + 2) * 4;
     static constexpr int kRingBytes = kWarps * kRing > kMergeBytes ? kWarps * kRing : kMergeBytes;
-    static constexpr int kJoinBytes = kWarps * int(kStepCtas) * 4;  // a factor for each part of a warp's row
+    static constexpr int kJoinBytes = kWarps * int(kStepCtas) * 8;  // factor and sum of each part of a warp's row
     static constexpr int kSmem = kRingBytes + kWarps * kScaleBytes;
     static_assert(kRingBytes >= kJoinBytes, "join");
 
@@ -704,40 +704,54 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                 __threadfence();
                 // a warp a row: the parts' factors, then its columns, D / 32 a lane
                 const int parts = int(last - first) + 1;
-                float* factor = reinterpret_cast<float*>(smem) + warp * kStepCtas;
+                float* factor = reinterpret_cast<float*>(smem) + warp * 2 * kStepCtas;
                 for (int row = int(warp); row < rows; row += kWarps) {
-                    float mm = -INFINITY;
+                    constexpr int W = D / 32, kAhead = 16;
+                    const int col = int(lane) * W;
+                    float acc[W], ahead[kAhead][W];
+                    // the first columns are on their way while the factors are made
+                    const auto load = [&](int c, float* to) {
+                        const float* from = slot(first + uint32_t(c)) + 2 * ROWS + row * D + col;
+                        if (W == 4) {
+                            const float4 y = __ldcg(reinterpret_cast<const float4*>(from));
+                            to[0] = y.x, to[1] = y.y, to[W - 2] = y.z, to[W - 1] = y.w;
+                        } else {
+                            const float2 y = __ldcg(reinterpret_cast<const float2*>(from));
+                            to[0] = y.x, to[1] = y.y;
+                        }
+                    };
+#pragma unroll
+                    for (int c = 0; c < kAhead; ++c) load(min(c, parts - 1), ahead[c]);
+                    float mm = -INFINITY, ll = 0.f;
                     for (int c = int(lane); c < parts; c += 32) {
-                        const float mc = __ldcg(slot(first + uint32_t(c)) + 2 * row);
-                        factor[c] = mc;
-                        mm = fmaxf(mm, mc);
+                        const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot(first + uint32_t(c)) + 2 * row));
+                        factor[c] = ml.x;
+                        factor[kStepCtas + c] = ml.y;
+                        mm = fmaxf(mm, ml.x);
                     }
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
-                    float ll = 0.f;
                     for (int c = int(lane); c < parts; c += 32) {
                         const float f = factor[c] == mm ? 1.f : exp2_fast(factor[c] - mm);
                         factor[c] = f;
-                        ll += f * __ldcg(slot(first + uint32_t(c)) + 2 * row + 1);
+                        ll += f * factor[kStepCtas + c];
                     }
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(~0u, ll, d);
                     __syncwarp();
-                    constexpr int W = D / 32;
-                    const int col = int(lane) * W;
-                    float acc[W];
 #pragma unroll
                     for (int y = 0; y < W; ++y) acc[y] = 0.f;
-#pragma unroll 16
-                    for (int c = 0; c < parts; ++c) {
-                        const float f = factor[c];
-                        const float* from = slot(first + uint32_t(c)) + 2 * ROWS + row * D + col;
-                        if (W == 4) {
-                            const float4 y = __ldcg(reinterpret_cast<const float4*>(from));
-                            acc[0] += f * y.x, acc[1] += f * y.y, acc[W - 2] += f * y.z, acc[W - 1] += f * y.w;
-                        } else {
-                            const float2 y = __ldcg(reinterpret_cast<const float2*>(from));
-                            acc[0] += f * y.x, acc[1] += f * y.y;
+                    for (int c0 = 0; c0 < parts; c0 += kAhead) {
+#pragma unroll
+                        for (int c = 0; c < kAhead; ++c)
+                            if (c0 + c < parts) {
+                                const float f = factor[c0 + c];
+#pragma unroll
+                                for (int y = 0; y < W; ++y) acc[y] += f * ahead[c][y];
+                            }
+                        if (c0 + kAhead < parts) {
+#pragma unroll
+                            for (int c = 0; c < kAhead; ++c) load(min(c0 + kAhead + c, parts - 1), ahead[c]);
                         }
                     }
                     finish(row, col, acc, W, mm, ll);
