@@ -20,6 +20,9 @@ namespace splitzip {
 namespace {
 
 constexpr int kRwWarps = 4;
+// Rows of a call from which a warp takes eight passes instead of two.
+constexpr uint64_t kManyRows = 65536;
+constexpr int kManyPasses = 4;
 
 __global__ void kv_begin_kernel(int* status, uint32_t* words, uint32_t count) {
     release_successor();
@@ -61,24 +64,28 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     return H ? pack_half2(a, b) : pack_bf16x2(a, b);
 }
 
-// Eight elements of a row, quantised; lanes `mask` (LPR of them) hold the row.
+// Eight elements of a row, quantised; LPR lanes hold the row.  Whole warp.
 template <bool E5M2, bool H, int LPR>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t mask, uint32_t* scale) {
+__device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t* scale) {
     constexpr uint32_t kInf = H ? 0x7C00u : 0x7F80u;
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t top = 0;  // largest magnitude: 16-bit floats order as integers
+    // largest magnitude: 16-bit floats order as integers
+    uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                            __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
-    uint32_t most = __reduce_max_sync(mask, max(top & 0xFFFFu, top >> 16));
+    for (int d = 1; d < LPR; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, d));
+    uint32_t most = max(top & 0xFFFFu, top >> 16);
     const bool special = most >= kInf;  // the row has an infinity or a NaN
-    if (special) {
+    if (__any_sync(~0u, special)) {
         top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
             top = max(top, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
         }
-        most = __reduce_max_sync(mask, top);
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+        most = top;
     }
     const uint32_t bits = __float_as_uint(unpack16<H>(most).x);
     int k = int(bits >> 23) - 127 - (E5M2 ? 15 : 8) + ((bits & 0x7FFFFFu) > 0x600000u);
@@ -88,15 +95,18 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t mask, uint32
     uint32_t q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack16<H>(w[i]);
-        q[i] = float2_to_fp8x2<E5M2>(f.x * inv, f.y * inv);
-        if (special) {  // the conversion saturates infinities
+        const float2 f = mul2(unpack16<H>(w[i]), make_float2(inv, inv));
+        q[i] = float2_to_fp8x2<E5M2>(f.x, f.y);
+    }
+    if (special) {  // the conversion saturates infinities
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             if ((w[i] & 0x7FFFu) == kInf) q[i] = (q[i] & 0xFF00u) | (E5M2 ? 0x7Cu : 0x7Fu) | ((w[i] >> 8) & 0x80u);
             if (((w[i] >> 16) & 0x7FFFu) == kInf)
                 q[i] = (q[i] & 0x00FFu) | (E5M2 ? 0x7C00u : 0x7F00u) | ((w[i] >> 16) & 0x8000u);
         }
     }
-    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
 }
 
 template <bool E5M2, bool H>
@@ -105,36 +115,36 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& q, float scale) {
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = half2_to_float2(fp8x2_to_half2<E5M2>(w[i / 2] >> (16 * (i & 1))));
-        o[i] = pack16<H>(f.x * scale, f.y * scale);
+        const float2 f = mul2(half2_to_float2(fp8_pair_to_half2<E5M2>(w[i / 2], i & 1)), make_float2(scale, scale));
+        o[i] = pack16<H>(f.x, f.y);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// FMT 0: 16-bit cache, 1: E5M2, 2: E4M3.  LPR lanes hold a row, PASSES times
-// 32 / LPR rows a warp.
+// FMT 0: 16-bit cache, 1: E5M2, 2: E4M3.  LPR lanes hold a row; a warp takes K
+// and V of PASSES * 32 / LPR heads of one token.
 template <bool WRITE, int FMT, bool H, int LPR, int PASSES>
 __global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_constant__ RwArgs a) {
     constexpr uint32_t kRows = 32 / LPR;  // rows a pass
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint32_t items = 2 * a.c.kv_heads;  // rows of one token: K then V
-    const uint32_t parts = (items + kRows * PASSES - 1) / (kRows * PASSES);
+    const uint32_t lane = threadIdx.x & 31u, col = lane % LPR;
+    const uint32_t parts = (a.c.kv_heads + kRows * PASSES - 1) / (kRows * PASSES);
     const uint64_t warp = uint64_t(blockIdx.x) * kRwWarps + (threadIdx.x >> 5);
     const uint64_t token = warp / parts;
-    const uint32_t first = uint32_t(warp - token * parts) * (kRows * PASSES) + lane / LPR;
-    const uint32_t col = lane % LPR;
+    const uint32_t head0 = uint32_t(warp - token * parts) * (kRows * PASSES) + lane / LPR;
     bool bad = false;
     if (token < a.b.tokens) {
-        uint4 x[PASSES];
+        uint4 x[2][PASSES];
+        const uint16_t* rows[2] = {a.k.d + token * a.k.token_stride + head0 * a.k.head_stride + col * 8u,
+                                   a.v.d + token * a.v.token_stride + head0 * a.v.head_stride + col * 8u};
         if (WRITE) {
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                const uint32_t item = first + p * kRows;
-                if (item < items) {
-                    const bool is_v = item >= a.c.kv_heads;
-                    const KvRows& r = is_v ? a.v : a.k;
-                    const uint32_t head = item - (is_v ? a.c.kv_heads : 0u);
-                    x[p] = __ldcs(reinterpret_cast<const uint4*>(r.d + token * r.token_stride + head * r.head_stride) + col);
+            for (int side = 0; side < 2; ++side) {
+                const uint64_t step = (side ? a.v.head_stride : a.k.head_stride) * kRows;
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p) {
+                    x[side][p] = make_uint4(0, 0, 0, 0);
+                    if (head0 + p * kRows < a.c.kv_heads)
+                        x[side][p] = __ldcs(reinterpret_cast<const uint4*>(rows[side] + p * step));
                 }
             }
         }
@@ -158,47 +168,62 @@ __global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_const
                 }
             }
         }
+        // the same in all lanes
         if (mine && !bad && (placed || !WRITE)) {
+            const uint64_t at = page * a.c.page_stride + uint64_t(slot) * a.c.token_stride + head0 * a.c.head_stride +
+                                col * (FMT == 0 ? 16u : 8u);
+            const uint64_t step = a.c.head_stride * kRows;
+            const uint64_t scale_at = ((page * a.c.kv_heads + head0) << a.c.page_shift) + slot;
+            const uint64_t scale_step = uint64_t(kRows) << a.c.page_shift;
+            if (WRITE) {
 #pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                const uint32_t item = first + p * kRows;
-                if (item >= items) continue;
-                const bool is_v = item >= a.c.kv_heads;
-                const uint32_t head = item - (is_v ? a.c.kv_heads : 0u);
-                uint8_t* at = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + uint64_t(slot) * a.c.token_stride +
-                              head * a.c.head_stride;
-                uint8_t* scale_at = FMT == 0 ? nullptr
-                                             : (is_v ? a.c.v_scale : a.c.k_scale) +
-                                                   (((page * a.c.kv_heads + head) << a.c.page_shift) + slot);
-                if (WRITE) {
-                    if (FMT == 0) {
-                        reinterpret_cast<uint4*>(at)[col] = x[p];
-                    } else {
-                        const uint32_t mask = (LPR == 32 ? ~0u : ((1u << (LPR % 32)) - 1u)) << (lane / LPR * LPR);
-                        uint32_t scale;
-                        reinterpret_cast<uint2*>(at)[col] = quantise8<FMT == 1, H, LPR>(x[p], mask, &scale);
-                        if (col == 0) *scale_at = uint8_t(scale);
-                    }
-                } else {
-                    x[p] = make_uint4(0, 0, 0, 0);  // a row without a place reads as zeros
-                    if (placed) {
-                        if (FMT == 0)
-                            x[p] = __ldcs(reinterpret_cast<const uint4*>(at) + col);
-                        else
-                            x[p] = dequantise8<FMT == 1, H>(__ldcs(reinterpret_cast<const uint2*>(at) + col),
-                                                            scale_value(*scale_at));
+                for (int side = 0; side < 2; ++side) {
+                    uint8_t* to = (side ? a.c.v : a.c.k) + at;
+                    uint8_t* scales = FMT == 0 ? nullptr : (side ? a.c.v_scale : a.c.k_scale) + scale_at;
+#pragma unroll
+                    for (int p = 0; p < PASSES; ++p) {
+                        const bool there = head0 + p * kRows < a.c.kv_heads;
+                        if (FMT == 0) {
+                            if (there) *reinterpret_cast<uint4*>(to + p * step) = x[side][p];
+                        } else {
+                            uint32_t scale;
+                            const uint2 q = quantise8<FMT == 1, H, LPR>(x[side][p], &scale);
+                            if (there) *reinterpret_cast<uint2*>(to + p * step) = q;
+                            if (there && col == 0) scales[p * scale_step] = uint8_t(scale);
+                        }
                     }
                 }
-            }
-            if (!WRITE) {
+            } else {
+                // all loads before the first store; a row without a place reads as zeros
+                uint32_t scale[2][PASSES];
 #pragma unroll
-                for (int p = 0; p < PASSES; ++p) {
-                    const uint32_t item = first + p * kRows;
-                    if (item >= items) continue;
-                    const bool is_v = item >= a.c.kv_heads;
-                    const KvRows& r = is_v ? a.v : a.k;
-                    const uint32_t head = item - (is_v ? a.c.kv_heads : 0u);
-                    __stcs(reinterpret_cast<uint4*>(r.d + token * r.token_stride + head * r.head_stride) + col, x[p]);
+                for (int side = 0; side < 2; ++side)
+#pragma unroll
+                    for (int p = 0; p < PASSES; ++p) {
+                        const uint8_t* from = (side ? a.c.v : a.c.k) + at + p * step;
+                        x[side][p] = make_uint4(0, 0, 0, 0);
+                        scale[side][p] = 0;
+                        if (placed && head0 + p * kRows < a.c.kv_heads) {
+                            if (FMT == 0) {
+                                x[side][p] = __ldcs(reinterpret_cast<const uint4*>(from));
+                            } else {
+                                const uint2 q = __ldcs(reinterpret_cast<const uint2*>(from));
+                                x[side][p].x = q.x, x[side][p].y = q.y;
+                                scale[side][p] = ((side ? a.c.v_scale : a.c.k_scale) + scale_at)[p * scale_step];
+                            }
+                        }
+                    }
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    const uint64_t to_step = (side ? a.v.head_stride : a.k.head_stride) * kRows;
+#pragma unroll
+                    for (int p = 0; p < PASSES; ++p) {
+                        if (FMT != 0)
+                            x[side][p] = dequantise8<FMT == 1, H>(make_uint2(x[side][p].x, x[side][p].y),
+                                                                  scale_value(scale[side][p]));
+                        if (head0 + p * kRows < a.c.kv_heads)
+                            __stcs(reinterpret_cast<uint4*>(const_cast<uint16_t*>(rows[side]) + p * to_step), x[side][p]);
+                    }
                 }
             }
         }
@@ -207,16 +232,21 @@ __global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_const
     if (bad && lane == 0) report(a.status, SPLITZIP_ERR_INVALID_ARG);
 }
 
-template <bool WRITE, int FMT, bool H>
-cudaError_t launch_rw(const RwArgs& a, cudaStream_t s) {
-    constexpr int kPasses = 4;
-    const uint32_t lpr = a.c.head_dim / 8, rows = 32 / lpr * kPasses;
-    const uint64_t parts = (2 * a.c.kv_heads + rows - 1) / rows;
+template <bool WRITE, int FMT, bool H, int PASSES>
+cudaError_t launch_passes(const RwArgs& a, cudaStream_t s) {
+    const uint32_t lpr = a.c.head_dim / 8, heads = 32 / lpr * PASSES;
+    const uint64_t parts = (a.c.kv_heads + heads - 1) / heads;
     const uint64_t grid = (uint64_t(a.b.tokens) * parts + kRwWarps - 1) / kRwWarps;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
     ChainedLaunch l(dim3(uint32_t(grid)), dim3(kRwWarps * 32), 0, s);
-    return lpr == 16 ? cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 16, kPasses>, a)
-                     : cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 8, kPasses>, a);
+    return lpr == 16 ? cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 16, PASSES>, a)
+                     : cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 8, PASSES>, a);
+}
+
+template <bool WRITE, int FMT, bool H>
+cudaError_t launch_rw(const RwArgs& a, cudaStream_t s) {
+    const uint64_t rows = uint64_t(a.b.tokens) * 2 * a.c.kv_heads;
+    return rows >= kManyRows ? launch_passes<WRITE, FMT, H, kManyPasses>(a, s) : launch_passes<WRITE, FMT, H, 1>(a, s);
 }
 
 template <bool WRITE>
