@@ -8,21 +8,22 @@
 // comparison of mantissa bits, no division.  The scale being a power of two,
 // x_i / 2^k and q_i 2^k are exact and the only rounding is RN8.
 //
-// What bounds it: HBM.  Nothing is reused, so a row of head_dim elements goes
-// through the registers of head_dim / 8 lanes, 16 bytes of the 16-bit side
-// and 8 or 16 of the cache's side in each lane; the row's maximum is one
-// redux.sync over those lanes.  A warp takes up to 8 rows (K or V of several
-// heads) of one token, so the search for the token's sequence and its page is
-// done once for all of them while their loads are in flight.
+// What bounds it: HBM.  Nothing is reused, so a row goes through the registers
+// of head_dim / 16 lanes, two 16-byte pieces of the 16-bit side in each (fewer
+// lanes a row than one piece each: what is done once a row, its maximum and
+// scale, was a third of the instructions, and issue bound the kernel).  A warp
+// takes K and V of 4 or 8 heads of one token, so the search for the token's
+// sequence and page is done once for all of them while their loads are in
+// flight; more rows a warp (two passes) measured the same, with more
+// registers.  One GB300: a 32,768-token layer of 8 heads of 128 to E5M2 in
+// 34.9 us (5.8 TB/s, 85 % of the measured copy rate), 65,536 E5M2 tokens read
+// in 62.1 us (6.5 TB/s, 96 %).
 #include "kv_common.cuh"
 
 namespace splitzip {
 namespace {
 
 constexpr int kRwWarps = 4;
-// Rows of a call from which a warp takes eight passes instead of two.
-constexpr uint64_t kManyRows = 65536;
-constexpr int kManyPasses = 4;
 
 __global__ void kv_begin_kernel(int* status, uint32_t* words, uint32_t count) {
     release_successor();
@@ -64,14 +65,15 @@ __device__ __forceinline__ uint32_t pack16(float a, float b) {
     return H ? pack_half2(a, b) : pack_bf16x2(a, b);
 }
 
-// Eight elements of a row, quantised; LPR lanes hold the row.  Whole warp.
+// Sixteen elements of a row, quantised; LPR lanes hold the row.  Whole warp.
 template <bool E5M2, bool H, int LPR>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t* scale) {
+__device__ __forceinline__ void quantise16(const uint4 (&x)[2], uint2 (&out)[2], uint32_t* scale) {
     constexpr uint32_t kInf = H ? 0x7C00u : 0x7F80u;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     // largest magnitude: 16-bit floats order as integers
-    uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                            __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    uint32_t top = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
 #pragma unroll
     for (int d = 1; d < LPR; d <<= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, d));
     uint32_t most = max(top & 0xFFFFu, top >> 16);
@@ -79,7 +81,7 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t* scale) {
     if (__any_sync(~0u, special)) {
         top = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
             top = max(top, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
         }
@@ -92,21 +94,22 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t* scale) {
     k = most == 0 ? 0 : max(k, -126);
     *scale = uint32_t(k + 127);
     const float inv = __uint_as_float(uint32_t(127 - k) << 23);
-    uint32_t q[4];
+    uint32_t q[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const float2 f = mul2(unpack16<H>(w[i]), make_float2(inv, inv));
         q[i] = float2_to_fp8x2<E5M2>(f.x, f.y);
     }
     if (special) {  // the conversion saturates infinities
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             if ((w[i] & 0x7FFFu) == kInf) q[i] = (q[i] & 0xFF00u) | (E5M2 ? 0x7Cu : 0x7Fu) | ((w[i] >> 8) & 0x80u);
             if (((w[i] >> 16) & 0x7FFFu) == kInf)
                 q[i] = (q[i] & 0x00FFu) | (E5M2 ? 0x7C00u : 0x7F00u) | ((w[i] >> 16) & 0x8000u);
         }
     }
-    return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+    out[0] = make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+    out[1] = make_uint2(__byte_perm(q[4], q[5], 0x5410), __byte_perm(q[6], q[7], 0x5410));
 }
 
 template <bool E5M2, bool H>
@@ -121,30 +124,29 @@ __device__ __forceinline__ uint4 dequantise8(const uint2& q, float scale) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// FMT 0: 16-bit cache, 1: E5M2, 2: E4M3.  LPR lanes hold a row; a warp takes K
-// and V of PASSES * 32 / LPR heads of one token.
-template <bool WRITE, int FMT, bool H, int LPR, int PASSES>
+// FMT 0: 16-bit cache, 1: E5M2, 2: E4M3.  LPR lanes hold a row, two 16-byte
+// pieces each; a warp takes K and V of 32 / LPR heads of one token.
+template <bool WRITE, int FMT, bool H, int LPR>
 __global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_constant__ RwArgs a) {
-    constexpr uint32_t kRows = 32 / LPR;  // rows a pass
+    constexpr uint32_t kHeads = 32 / LPR;
     const uint32_t lane = threadIdx.x & 31u, col = lane % LPR;
-    const uint32_t parts = (a.c.kv_heads + kRows * PASSES - 1) / (kRows * PASSES);
+    const uint32_t parts = (a.c.kv_heads + kHeads - 1) / kHeads;
     const uint64_t warp = uint64_t(blockIdx.x) * kRwWarps + (threadIdx.x >> 5);
     const uint64_t token = warp / parts;
-    const uint32_t head0 = uint32_t(warp - token * parts) * (kRows * PASSES) + lane / LPR;
+    const uint32_t head = uint32_t(warp - token * parts) * kHeads + lane / LPR;
+    const bool there = head < a.c.kv_heads;
     bool bad = false;
     if (token < a.b.tokens) {
-        uint4 x[2][PASSES];
-        const uint16_t* rows[2] = {a.k.d + token * a.k.token_stride + head0 * a.k.head_stride + col * 8u,
-                                   a.v.d + token * a.v.token_stride + head0 * a.v.head_stride + col * 8u};
+        uint4 x[2][2];  // K and V
+        uint4* rows[2] = {reinterpret_cast<uint4*>(a.k.d + token * a.k.token_stride + head * a.k.head_stride) + col,
+                          reinterpret_cast<uint4*>(a.v.d + token * a.v.token_stride + head * a.v.head_stride) + col};
         if (WRITE) {
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
-                const uint64_t step = (side ? a.v.head_stride : a.k.head_stride) * kRows;
-#pragma unroll
-                for (int p = 0; p < PASSES; ++p) {
-                    x[side][p] = make_uint4(0, 0, 0, 0);
-                    if (head0 + p * kRows < a.c.kv_heads)
-                        x[side][p] = __ldcs(reinterpret_cast<const uint4*>(rows[side] + p * step));
+                x[side][0] = x[side][1] = make_uint4(0, 0, 0, 0);
+                if (there) {
+                    x[side][0] = __ldcs(rows[side]);
+                    x[side][1] = __ldcs(rows[side] + LPR);
                 }
             }
         }
@@ -170,60 +172,52 @@ __global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_const
         }
         // the same in all lanes
         if (mine && !bad && (placed || !WRITE)) {
-            const uint64_t at = page * a.c.page_stride + uint64_t(slot) * a.c.token_stride + head0 * a.c.head_stride +
+            const uint64_t at = page * a.c.page_stride + uint64_t(slot) * a.c.token_stride + head * a.c.head_stride +
                                 col * (FMT == 0 ? 16u : 8u);
-            const uint64_t step = a.c.head_stride * kRows;
-            const uint64_t scale_at = ((page * a.c.kv_heads + head0) << a.c.page_shift) + slot;
-            const uint64_t scale_step = uint64_t(kRows) << a.c.page_shift;
+            const uint64_t scale_at = ((page * a.c.kv_heads + head) << a.c.page_shift) + slot;
             if (WRITE) {
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
                     uint8_t* to = (side ? a.c.v : a.c.k) + at;
-                    uint8_t* scales = FMT == 0 ? nullptr : (side ? a.c.v_scale : a.c.k_scale) + scale_at;
-#pragma unroll
-                    for (int p = 0; p < PASSES; ++p) {
-                        const bool there = head0 + p * kRows < a.c.kv_heads;
-                        if (FMT == 0) {
-                            if (there) *reinterpret_cast<uint4*>(to + p * step) = x[side][p];
-                        } else {
-                            uint32_t scale;
-                            const uint2 q = quantise8<FMT == 1, H, LPR>(x[side][p], &scale);
-                            if (there) *reinterpret_cast<uint2*>(to + p * step) = q;
-                            if (there && col == 0) scales[p * scale_step] = uint8_t(scale);
-                        }
+                    if (FMT == 0) {
+                        uint4* row = reinterpret_cast<uint4*>(to);
+                        if (there) row[0] = x[side][0], row[LPR] = x[side][1];
+                    } else {
+                        uint2 q[2];
+                        uint32_t scale;
+                        quantise16<FMT == 1, H, LPR>(x[side], q, &scale);
+                        uint2* row = reinterpret_cast<uint2*>(to);
+                        if (there) row[0] = q[0], row[LPR] = q[1];
+                        if (there && col == 0) (side ? a.c.v_scale : a.c.k_scale)[scale_at] = uint8_t(scale);
                     }
                 }
-            } else {
+            } else if (there) {
                 // all loads before the first store; a row without a place reads as zeros
-                uint32_t scale[2][PASSES];
-#pragma unroll
-                for (int side = 0; side < 2; ++side)
-#pragma unroll
-                    for (int p = 0; p < PASSES; ++p) {
-                        const uint8_t* from = (side ? a.c.v : a.c.k) + at + p * step;
-                        x[side][p] = make_uint4(0, 0, 0, 0);
-                        scale[side][p] = 0;
-                        if (placed && head0 + p * kRows < a.c.kv_heads) {
-                            if (FMT == 0) {
-                                x[side][p] = __ldcs(reinterpret_cast<const uint4*>(from));
-                            } else {
-                                const uint2 q = __ldcs(reinterpret_cast<const uint2*>(from));
-                                x[side][p].x = q.x, x[side][p].y = q.y;
-                                scale[side][p] = ((side ? a.c.v_scale : a.c.k_scale) + scale_at)[p * scale_step];
-                            }
-                        }
-                    }
+                uint32_t scale[2] = {0, 0};
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
-                    const uint64_t to_step = (side ? a.v.head_stride : a.k.head_stride) * kRows;
-#pragma unroll
-                    for (int p = 0; p < PASSES; ++p) {
-                        if (FMT != 0)
-                            x[side][p] = dequantise8<FMT == 1, H>(make_uint2(x[side][p].x, x[side][p].y),
-                                                                  scale_value(scale[side][p]));
-                        if (head0 + p * kRows < a.c.kv_heads)
-                            __stcs(reinterpret_cast<uint4*>(const_cast<uint16_t*>(rows[side]) + p * to_step), x[side][p]);
+                    const uint8_t* from = (side ? a.c.v : a.c.k) + at;
+                    x[side][0] = x[side][1] = make_uint4(0, 0, 0, 0);
+                    if (placed && FMT == 0) {
+                        x[side][0] = __ldcs(reinterpret_cast<const uint4*>(from));
+                        x[side][1] = __ldcs(reinterpret_cast<const uint4*>(from) + LPR);
+                    } else if (placed) {
+                        const uint2 q0 = __ldcs(reinterpret_cast<const uint2*>(from));
+                        const uint2 q1 = __ldcs(reinterpret_cast<const uint2*>(from) + LPR);
+                        x[side][0] = make_uint4(q0.x, q0.y, q1.x, q1.y);
+                        scale[side] = (side ? a.c.v_scale : a.c.k_scale)[scale_at];
                     }
+                }
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    if (FMT != 0) {
+                        const uint4 q = x[side][0];
+                        const float f = scale_value(scale[side]);
+                        x[side][0] = dequantise8<FMT == 1, H>(make_uint2(q.x, q.y), f);
+                        x[side][1] = dequantise8<FMT == 1, H>(make_uint2(q.z, q.w), f);
+                    }
+                    __stcs(rows[side], x[side][0]);
+                    __stcs(rows[side] + LPR, x[side][1]);
                 }
             }
         }
@@ -232,21 +226,15 @@ __global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_const
     if (bad && lane == 0) report(a.status, SPLITZIP_ERR_INVALID_ARG);
 }
 
-template <bool WRITE, int FMT, bool H, int PASSES>
-cudaError_t launch_passes(const RwArgs& a, cudaStream_t s) {
-    const uint32_t lpr = a.c.head_dim / 8, heads = 32 / lpr * PASSES;
+template <bool WRITE, int FMT, bool H>
+cudaError_t launch_rw(const RwArgs& a, cudaStream_t s) {
+    const uint32_t lpr = a.c.head_dim / 16, heads = 32 / lpr;
     const uint64_t parts = (a.c.kv_heads + heads - 1) / heads;
     const uint64_t grid = (uint64_t(a.b.tokens) * parts + kRwWarps - 1) / kRwWarps;
     if (grid > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
     ChainedLaunch l(dim3(uint32_t(grid)), dim3(kRwWarps * 32), 0, s);
-    return lpr == 16 ? cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 16, PASSES>, a)
-                     : cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 8, PASSES>, a);
-}
-
-template <bool WRITE, int FMT, bool H>
-cudaError_t launch_rw(const RwArgs& a, cudaStream_t s) {
-    const uint64_t rows = uint64_t(a.b.tokens) * 2 * a.c.kv_heads;
-    return rows >= kManyRows ? launch_passes<WRITE, FMT, H, kManyPasses>(a, s) : launch_passes<WRITE, FMT, H, 1>(a, s);
+    return lpr == 8 ? cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 8>, a)
+                    : cudaLaunchKernelEx(&l.cfg, kv_rw_kernel<WRITE, FMT, H, 4>, a);
 }
 
 template <bool WRITE>
