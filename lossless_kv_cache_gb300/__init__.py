@@ -385,9 +385,12 @@ def _torch():
 
 
 def _stream_handle(stream):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream of the current device, without the Stream object that
+    # torch.cuda.current_stream() makes (3 us of a call)
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _bits_dtype(dtype):
@@ -628,7 +631,7 @@ def _kv_type_of(t):
 
 
 def _device_tensor(t, dtype, shape, what):
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if not t.is_cuda or t.dtype != dtype or t.shape != tuple(shape):
         raise ValueError("%s: expected a CUDA tensor of %s and shape %s, got %s %s on %s"
                          % (what, dtype, tuple(shape), t.dtype, tuple(t.shape), t.device))
     return t
@@ -660,6 +663,7 @@ class KVCache:
                     raise ValueError("%s: an FP8 cache needs a contiguous scale tensor" % what)
                 _device_tensor(s, torch.uint8, (pages, heads, page_tokens), what)
         self.k, self.v = k, v
+        self.page_tokens, self.kv_heads, self.head_dim = page_tokens, heads, dim
         self.k_scale, self.v_scale = (k_scale, v_scale) if fp8 else (None, None)
         self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if fp8 else None,
                                 v_scale.data_ptr() if fp8 else None, pages, k.stride(0), k.stride(1), k.stride(2),
@@ -698,37 +702,40 @@ class KVBatch:
         # a row's entries end where the table does, whatever the stride between rows
         self.table_pages = page_table.shape[1]
         self.cu_tokens, self.kv_len, self.page_table = cu_tokens, kv_len, page_table
-        self.tokens = tokens
+        self.tokens, self.max_kv_len = tokens, max_kv_len
         self.desc = KVBatchDesc(cu_tokens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.stride(0),
                                 batch, tokens, max_tokens, max_kv_len)
 
     def check(self, cache):
         """Raises where the page table is narrower than max_kv_len tokens need."""
-        if self.table_pages * cache.desc.page_tokens < self.desc.max_kv_len:
+        if self.table_pages * cache.page_tokens < self.max_kv_len:
             raise SplitZipError(ERR_INVALID_ARG, "page_table of %d pages for %d tokens"
-                                % (self.table_pages, self.desc.max_kv_len))
+                                % (self.table_pages, self.max_kv_len))
+
+
+_ROW_TYPES = {}
 
 
 def _kv_rows(t, tokens, heads, dim, what):
     """(KVRowsDesc, dtype constant) of a packed (tokens, heads, head_dim) tensor."""
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        dtype = BF16
-    elif t.dtype == torch.float16:
-        dtype = FP16
-    else:
+    if not _ROW_TYPES:
+        torch = _torch()
+        _ROW_TYPES.update({torch.bfloat16: BF16, torch.float16: FP16})
+    dtype = _ROW_TYPES.get(t.dtype)
+    if dtype is None:
         raise TypeError("%s: expected bfloat16 or float16, got %s" % (what, t.dtype))
     if not t.is_cuda or t.shape != (tokens, heads, dim) or t.stride(2) != 1:
         raise ValueError("%s: expected a CUDA tensor (%d, %d, %d) with a contiguous last axis, got %s of strides %s on %s"
                          % (what, tokens, heads, dim, tuple(t.shape), t.stride(), t.device))
-    return KVRowsDesc(t.data_ptr(), t.stride(0), t.stride(1)), dtype
+    token_stride, head_stride, _ = t.stride()
+    return KVRowsDesc(t.data_ptr(), token_stride, head_stride), dtype
 
 
 def _kv_rw(call, cache, batch, k, v, status, stream):
-    d = cache.desc
+    d, heads, dim = cache.desc, cache.kv_heads, cache.head_dim
     batch.check(cache)
-    rk, dtype = _kv_rows(k, batch.tokens, d.kv_heads, d.head_dim, "k")
-    rv, dtype_v = _kv_rows(v, batch.tokens, d.kv_heads, d.head_dim, "v")
+    rk, dtype = _kv_rows(k, batch.tokens, heads, dim, "k")
+    rv, dtype_v = _kv_rows(v, batch.tokens, heads, dim, "v")
     if dtype != dtype_v:
         raise TypeError("k and v: expected the same type")
     _check(call(d, batch.desc, rk, rv, dtype, status.data_ptr(), _stream_handle(stream)), call.__name__)
@@ -771,16 +778,16 @@ def kv_attention(cache, batch, q, out, bufs, scale, causal=True, window=0, lse=N
     """Enqueue the attention of the new tokens' queries over `cache`'s pages
     (asynchronous).  q, out: packed (tokens, q_heads, head_dim); lse: None or
     float32 (tokens, q_heads); bufs: KVAttentionBuffers."""
-    d = cache.desc
     batch.check(cache)
-    rq, dtype = _kv_rows(q, batch.tokens, bufs.q_heads, d.head_dim, "q")
-    ro, dtype_o = _kv_rows(out, batch.tokens, bufs.q_heads, d.head_dim, "out")
+    rq, dtype = _kv_rows(q, batch.tokens, bufs.q_heads, cache.head_dim, "q")
+    ro, dtype_o = _kv_rows(out, batch.tokens, bufs.q_heads, cache.head_dim, "out")
     if dtype != dtype_o:
         raise TypeError("q and out: expected the same type")
     if lse is not None:
         if not lse.is_contiguous():
             raise ValueError("lse: expected a contiguous tensor")
         _device_tensor(lse, _torch().float32, (batch.tokens, bufs.q_heads), "lse")
-    _check(splitzip_kv_attention(d, batch.desc, rq, ro, None if lse is None else lse.data_ptr(), dtype, bufs.q_heads,
-                                 scale, int(causal), window, bufs.ws.data_ptr(), bufs.ws_bytes, bufs.status.data_ptr(),
-                                 _stream_handle(stream)), "splitzip_kv_attention")
+        lse = lse.data_ptr()
+    _check(splitzip_kv_attention(cache.desc, batch.desc, rq, ro, lse, dtype, bufs.q_heads, scale, int(causal), window,
+                                 bufs.ws.data_ptr(), bufs.ws_bytes, bufs.status.data_ptr(), _stream_handle(stream)),
+           "splitzip_kv_attention")
