@@ -86,12 +86,15 @@ __device__ __forceinline__ Tile tile_of(const AttentionArgs& a, const KvSeq& s, 
 
 // Deals the units of all items to the CTAs (see kv_attention.cuh) and clears
 // the counters and the status word.  Items are in the order sequence, tile, kv
-// head.  One CTA: a thread sums a sequence of one or two tiles, a warp one of
-// more, then a scan over the sequences.
+// head.  One CTA: sequences are dealt to its warps, a lane sums one of one or
+// two tiles and the whole warp one of more; then a scan over the sequences,
+// and the same walk again to find where each CTA's share starts.
 __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __grid_constant__ AttentionArgs a,
                                                                      ChunkPlan* plan, uint32_t grid) {
     release_successor();
-    __shared__ uint64_t s_warp[kPlanThreads / 32];
+    constexpr uint32_t kPlanWarps = kPlanThreads / 32;
+    __shared__ uint64_t s_upto[kPlanThreads];  // of a round's sequences: units through each
+    __shared__ uint64_t s_warp[kPlanWarps];
     __shared__ int s_bad;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     if (tid == 0) s_bad = 0;
@@ -100,29 +103,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     const auto weight = [&](const KvSeq& s, int tile) -> uint64_t {
         return uint64_t(tile_of(a, s, tile).units + kItemCost) * a.c.kv_heads;
     };
-    // units of the lane's sequence (every lane of a warp at once)
-    const auto seq_units = [&](const KvSeq& s) -> uint64_t {
-        const int n = tile_count(a, s);
-        uint64_t w = 0;
-        for (int i = 0; i < n && n <= 2; ++i) w += weight(s, i);
-        uint32_t many = __ballot_sync(~0u, n > 2);
-        while (many) {
-            const int src = __ffs(many) - 1;
-            many &= many - 1;
-            KvSeq o;
-            o.row0 = 0;
-            o.ok = true;
-            o.t = __shfl_sync(~0u, s.t, src);
-            o.n = __shfl_sync(~0u, s.n, src);
-            uint64_t part = 0;
-            const int tiles = tile_count(a, o);
-            for (int i = int(lane); i < tiles; i += 32) part += weight(o, i);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(~0u, part, d);
-            if (int(lane) == src) w = part;
-        }
-        return w;
-    };
+    // the lane's sequence of a round
+    const uint32_t nth = lane * kPlanWarps + warp;
     const auto seq_at = [&](uint32_t b) -> KvSeq {
         KvSeq s{0, 0, 0, true};
         if (b < a.b.batch) {
@@ -131,70 +113,85 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
         }
         return s;
     };
-    // inclusive scan over the CTA; *total for all
-    const auto scan = [&](uint64_t x, uint64_t* total) -> uint64_t {
+    // Calls each(sequence, index in the round) by the whole warp for every sequence
+    // of more than two tiles.
+    const auto for_large = [&](const KvSeq& s, const auto& each) {
+        uint32_t many = __ballot_sync(~0u, tile_count(a, s) > 2);
+        while (many) {
+            const int src = __ffs(many) - 1;
+            many &= many - 1;
+            each(KvSeq{0, __shfl_sync(~0u, s.t, src), __shfl_sync(~0u, s.n, src), true},
+                 uint32_t(src) * kPlanWarps + warp);
+        }
+    };
+    // Units through each of the round's sequences into s_upto; returns the round's.
+    const auto round_units = [&](const KvSeq& s) -> uint64_t {
+        uint64_t w = 0;
+        const int n = tile_count(a, s);
+        for (int i = 0; i < n && n <= 2; ++i) w += weight(s, i);
+        __syncthreads();
+        if (n <= 2) s_upto[nth] = w;
+        for_large(s, [&](const KvSeq& o, uint32_t at) {
+            uint64_t part = 0;
+            for (int i = int(lane), tiles = tile_count(a, o); i < tiles; i += 32) part += weight(o, i);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(~0u, part, d);
+            if (lane == 0) s_upto[at] = part;
+        });
+        __syncthreads();
+        uint64_t x = s_upto[tid];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const uint64_t y = __shfl_up_sync(~0u, x, d);
             if (int(lane) >= d) x += y;
         }
-        __syncthreads();
         if (lane == 31) s_warp[warp] = x;
         __syncthreads();
-        uint64_t before = 0, all = 0;
-        for (int i = 0; i < kPlanThreads / 32; ++i) {
-            if (i < int(warp)) before += s_warp[i];
-            all += s_warp[i];
+        uint64_t all = s_warp[lane];  // as many warps as lanes
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t y = __shfl_up_sync(~0u, all, d);
+            if (int(lane) >= d) all += y;
         }
-        *total = all;
-        return x + before;
+        const uint64_t before = __shfl_sync(~0u, all, int(warp) - 1 + (warp == 0));
+        s_upto[tid] = x + (warp == 0 ? 0 : before);
+        const uint64_t total = __shfl_sync(~0u, all, 31);
+        __syncthreads();
+        return total;
     };
+    static_assert(kPlanWarps == 32, "the scan over warps");
     uint64_t units = 0;
-    const bool once = a.b.batch <= kPlanThreads;
     KvSeq s{0, 0, 0, true};
-    uint64_t w = 0, upto = 0;
     for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) {
-        s = seq_at(b0 + tid);
-        w = seq_units(s);
-        uint64_t total;
-        upto = scan(w, &total);
-        units += total;
+        s = seq_at(b0 + nth);
+        units += round_units(s);
     }
     const uint32_t ctas = uint32_t(min(uint64_t(grid), max(units, uint64_t(1))));
     uint64_t base = 0;
     for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) {
         uint64_t total = 0;
-        if (!once) {
-            s = seq_at(b0 + tid);
-            w = seq_units(s);
-            upto = scan(w, &total);
+        if (a.b.batch > kPlanThreads) {
+            s = seq_at(b0 + nth);
+            total = round_units(s);
         }
-        uint64_t from = base + upto - w;
         // the CTAs whose share starts within [lo, hi)
         const auto starts = [&](uint32_t b, uint32_t tile, uint64_t lo, uint64_t hi) {
             for (uint64_t c = (lo * ctas + units - 1) / units; c < ctas && share_start(units, ctas, c) < hi; ++c)
                 plan->start[c] = ChunkStart{b, tile, lo};
         };
+        const auto from_of = [&](uint32_t at) { return base + (at == 0 ? 0 : s_upto[at - 1]); };
         const int n = tile_count(a, s);
         if (n <= 2) {
+            uint64_t from = from_of(nth);
             for (int i = 0; i < n; ++i) {
                 const uint64_t x = weight(s, i);
-                starts(b0 + tid, uint32_t(i), from, from + x);
+                starts(b0 + nth, uint32_t(i), from, from + x);
                 from += x;
             }
         }
-        uint32_t many = __ballot_sync(~0u, n > 2);
-        while (many) {
-            const int src = __ffs(many) - 1;
-            many &= many - 1;
-            KvSeq o;
-            o.row0 = 0;
-            o.ok = true;
-            o.t = __shfl_sync(~0u, s.t, src);
-            o.n = __shfl_sync(~0u, s.n, src);
-            uint64_t at = __shfl_sync(~0u, from, src);
-            const int tiles = tile_count(a, o);
-            for (int i0 = 0; i0 < tiles; i0 += 32) {
+        for_large(s, [&](const KvSeq& o, uint32_t at) {
+            uint64_t from = from_of(at);
+            for (int i0 = 0, tiles = tile_count(a, o); i0 < tiles; i0 += 32) {
                 const int i = i0 + int(lane);
                 const uint64_t x = i < tiles ? weight(o, i) : 0;
                 uint64_t y = x;
@@ -203,10 +200,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
                     const uint64_t z = __shfl_up_sync(~0u, y, d);
                     if (int(lane) >= d) y += z;
                 }
-                if (x > 0) starts(b0 + warp * 32 + uint32_t(src), uint32_t(i), at + y - x, at + y);
-                at += __shfl_sync(~0u, y, 31);
+                if (x > 0) starts(b0 + at, uint32_t(i), from + y - x, from + y);
+                from += __shfl_sync(~0u, y, 31);
             }
-        }
+        });
         base += total;
     }
     __syncthreads();
@@ -367,35 +364,41 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
             const uint8_t* scales = (is_v ? sh.v_scale : sh.k_scale)[(x >> 1) & 3u];
             if (ok) {
 #pragma unroll
-                for (int i = 0; i < C::kChunks; ++i) {
-                    const uint32_t r = r0 + uint32_t(i) * C::kRowStep;
-                    const uint4 y =
-                        *reinterpret_cast<const uint4*>(sh.raw[x % 2] + (uint32_t(i) * 128u + lt) * 16u);
-                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-                    uint32_t o[8];
-                    if (C::kScoreScale && !is_v) {
+                for (int i0 = 0; i0 < C::kChunks; i0 += 4) {
+                    // loads first: to the compiler the stores could be to the same memory
+                    uint4 raw[4];
+                    uint32_t scale[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            o[2 * j] = fp8x2_to_half2<C::kE5M2>(w[j]);
-                            o[2 * j + 1] = fp8x2_to_half2<C::kE5M2>(w[j] >> 16);
-                        }
-                    } else {
-                        // exact: BF16 holds the value and its product with a power of two
-                        const uint32_t s16 = uint32_t(scales[r]) << 7;
-                        const __nv_bfloat162 s2 = __nv_bfloat162(__ushort_as_bfloat16(uint16_t(s16)),
-                                                                 __ushort_as_bfloat16(uint16_t(s16)));
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t v = fp8x2_to_bf16x2<C::kE5M2>(w[j / 2] >> (16 * (j & 1)));
-                            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), s2);
-                            o[j] = *reinterpret_cast<const uint32_t*>(&z);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        raw[i] = *reinterpret_cast<const uint4*>(sh.raw[x % 2] + (uint32_t(i0 + i) * 128u + lt) * 16u);
+                        scale[i] = scales[r0 + uint32_t(i0 + i) * C::kRowStep];
                     }
-                    uint8_t* row = sh.stage[st] + (c >> 2) * C::kBlockBytes + r * 128u;
-                    *reinterpret_cast<uint4*>(row + ((((2u * c) & 7u) ^ (r & 7u)) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(row + ((((2u * c + 1u) & 7u) ^ (r & 7u)) << 4)) =
-                        make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t r = r0 + uint32_t(i0 + i) * C::kRowStep;
+                        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                        uint32_t o[8];
+                        if (C::kScoreScale && !is_v) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] = fp8_pair_to_half2<C::kE5M2>(w[j / 2], j & 1);
+                        } else {
+                            // exact: BF16 holds the value and its product with a power of two
+                            const uint32_t s16 = scale[i] * 0x00800080u;
+                            const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&s16);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 f = half2_to_float2(fp8_pair_to_half2<C::kE5M2>(w[j / 2], j & 1));
+                                const uint32_t v = pack_bf16x2(f.x, f.y);
+                                const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), s2);
+                                o[j] = *reinterpret_cast<const uint32_t*>(&z);
+                            }
+                        }
+                        uint8_t* row = sh.stage[st] + (c >> 2) * C::kBlockBytes + r * 128u;
+                        *reinterpret_cast<uint4*>(row + ((((2u * c) & 7u) ^ (r & 7u)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(row + ((((2u * c + 1u) & 7u) ^ (r & 7u)) << 4)) =
+                            make_uint4(o[4], o[5], o[6], o[7]);
+                    }
                 }
             }
         }
