@@ -17,8 +17,11 @@
 // stages of 16 keys (K and V) in shared memory filled by its own 16-byte
 // cp.async copies, and no barrier between warps until an item ends.  The query
 // heads that share a kv head are rows of one tile, so the cache is read once
-// for all of them; tiles of up to 8 rows have kernels of their own, which hold
-// half the sums.
+// for all of them.  The products are S^T = K Q^T and O^T = V^T P^T, keys and
+// dims along the 16 of an m16n8k16 and rows along its 8: a tile of 8 rows, the
+// common one, wastes nothing, and P^T gets its place by transposing 8x8 blocks
+// (movmatrix).  (With rows along the 16, a step of 8 rows took half as many
+// products again, 48 more registers, and three CTAs an SM instead of four.)
 #include <algorithm>
 #include <atomic>
 
@@ -32,10 +35,8 @@ constexpr int kUnit = 64;      // keys of a unit: 16 for each of the four warps
 constexpr int kWarps = 4;
 constexpr int kKeys = 16;      // keys of a stage
 constexpr int kMinUnits = 2;   // least share of a CTA
-constexpr uint32_t kStepCtas = 456;  // three on each of 152 SMs, at most
+constexpr uint32_t kStepCtas = 608;  // four on each of 152 SMs, at most
 
-// d += a b over 16 rows (of a tile of 8, the other 8 are zeros in a and stay
-// zeros in d: registers that are always there cost less than clearing them).
 template <bool HALF>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (HALF)
@@ -64,6 +65,13 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
                  : "memory");
 }
 
+// The transpose of an 8x8 matrix of 16-bit elements, two a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
 // 16 bytes to shared memory, asynchronously; zeros where !there.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -83,7 +91,8 @@ template <int FMT, bool H, int D, int ROWS>
 struct Step {
     static constexpr bool kFp8 = FMT != 0;
     static constexpr bool kE5M2 = FMT == 1;
-    static constexpr int kRowsLane = ROWS / 8;         // rows of a lane: g, and g + 8
+    static constexpr int kBlocks = ROWS / 8;           // of 8 rows
+    static constexpr int kRowsLane = 2 * kBlocks;      // rows of a lane: 2 t, 2 t + 1 of each block
     static constexpr bool kHalf = kFp8 || H;           // products in FP16, else BF16
     // FP16 weights are 2^14 times the exponentials (at most 1), so that those
     // down to 2^-28 keep all bits; the factor cancels in o / l.
@@ -94,10 +103,10 @@ struct Step {
     static constexpr int kCopies = kKeys / kRowsACopy;
     static constexpr int kSideBytes = kKeys * kRowBytes;
     static constexpr int kStageBytes = 2 * kSideBytes;
-    // Bytes in flight: three CTAs an SM of 16 KB rings a warp, or (stages of
-    // 8 KB, or more registers than three CTAs have) two of 24 KB.
-    static constexpr int kCtasPerSm = kStageBytes > 4096 || (ROWS == 16 && kFp8 && D == 128) ? 2 : 3;
-    static constexpr int kStages = (kCtasPerSm == 2 ? 24576 : 16384) / kStageBytes;
+    // Bytes in flight: four CTAs an SM of 12 KB rings a warp, three of 16 KB where
+    // four have not the registers, or (stages of 8 KB) two of 24 KB.
+    static constexpr int kCtasPerSm = kStageBytes > 4096 ? 2 : ROWS == 16 && D == 128 ? 3 : 4;
+    static constexpr int kStages = 49152 / kCtasPerSm / kStageBytes;
     static constexpr int kRing = kStages * kStageBytes;  // a warp's
     static constexpr int kScaleBytes = kFp8 ? kStages * 2 * kKeys : 0;  // of K and V for a stage's keys
     static constexpr int kMergeBytes = kWarps * ROWS * (D + 2) * 4;
@@ -118,9 +127,10 @@ struct Step {
         if (D == 128) return r * kRowBytes + ((c ^ (r & 6u)) << 4);
         return (r >> 1) * 128u + ((((r & 1u) * 4u + c) ^ (((r >> 1) & 3u) << 1)) << 4);
     }
-    // Column of the output that accumulator j, element e of quad lane t holds.
-    static __device__ __forceinline__ int out_dim(int j, int t, int e) {
-        return kFp8 ? (D / 8) * (2 * t + e) + j : 8 * j + 2 * t + e;
+    // Column of the output that lane group g's accumulators c0, c1 (up 0) or c2,
+    // c3 (up 1) of block j are of.
+    static __device__ __forceinline__ int out_dim(int j, int g, int up) {
+        return kFp8 ? (D / 8) * g + 2 * j + up : 16 * j + 8 * up + g;
     }
 };
 
@@ -256,33 +266,25 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
         const KeyRange keys = visible(a, s, i0, i1);
         const int base = (all.lo / kUnit + int(u - item_start)) * kUnit + int(warp) * kKeys;
 
-        // queries, as the first operand of the products: rows g and g + 8
-        uint32_t q[D / 16][4];
-        KeyRange see[S::kRowsLane];
+        // queries, as the second operand: row g of each block
+        uint32_t q[S::kBlocks][D / 16][2];
         float row_scale[S::kRowsLane];
 #pragma unroll
-        for (int r2 = 0; r2 < 2; ++r2) {
-            if (r2 >= S::kRowsLane) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) q[k][1] = q[k][3] = 0u;
-                break;
-            }
-            const int r = g + 8 * r2;
+        for (int nb = 0; nb < S::kBlocks; ++nb) {
+            const int r = g + 8 * nb;
             const bool there = r < rows;
             const int i = (row_first + (there ? r : 0)) / int(a.group);
             const uint32_t qh = head * a.group + uint32_t((row_first + (there ? r : 0)) % int(a.group));
             const uint16_t* src = a.q.d + uint64_t(s.row0 + i) * a.q.token_stride + uint64_t(qh) * a.q.head_stride;
-            see[r2] = visible(a, s, i);
-            if (!there) see[r2].hi = 0;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 // FP8: dims are dealt so that a lane's share of a key is 16 contiguous bytes
                 const int d0 = S::kFp8 ? (k / 4) * 64 + t4 * 16 + (k % 4) * 4 : k * 16 + 2 * t4;
                 const int d1 = S::kFp8 ? d0 + 2 : d0 + 8;
-                q[k][r2] = there ? *reinterpret_cast<const uint32_t*>(src + d0) : 0u;
-                q[k][r2 + 2] = there ? *reinterpret_cast<const uint32_t*>(src + d1) : 0u;
+                q[nb][k][0] = there ? *reinterpret_cast<const uint32_t*>(src + d0) : 0u;
+                q[nb][k][1] = there ? *reinterpret_cast<const uint32_t*>(src + d1) : 0u;
             }
-            row_scale[r2] = a.scale_log2;
+            float scale = a.scale_log2;
             if (S::kFp8 && !a.q_half) {
                 // BF16 to FP16 by way of the power of two that brings the row's largest
                 // finite element to [2^14, 2^15): what FP16 loses of the small ones is
@@ -291,8 +293,8 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                    for (int y = 0; y < 4; y += 2) {
-                        const uint32_t lo = q[k][r2 + y] & 0x7FFFu, hi = (q[k][r2 + y] >> 16) & 0x7FFFu;
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t lo = q[nb][k][y] & 0x7FFFu, hi = (q[nb][k][y] >> 16) & 0x7FFFu;
                         top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
                     }
                 top = max(top, __shfl_xor_sync(~0u, top, 1));
@@ -300,24 +302,36 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                 // 2^up takes exponent e to 14, within what one normal factor can do
                 const int e = int(top >> 7) - 127, up = min(126, 14 - e);
                 const float f = __uint_as_float(uint32_t(127 + up) << 23);
-                row_scale[r2] *= __uint_as_float(uint32_t(127 - up) << 23);
+                scale *= __uint_as_float(uint32_t(127 - up) << 23);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                    for (int y = 0; y < 4; y += 2) {
-                        const float2 v = bf16x2_to_float2(q[k][r2 + y]);
-                        q[k][r2 + y] = pack_half2(v.x * f, v.y * f);
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 v = bf16x2_to_float2(q[nb][k][y]);
+                        q[nb][k][y] = pack_half2(v.x * f, v.y * f);
                     }
             }
+            // the scores' rows are the lane's 2 t and 2 t + 1
+            row_scale[2 * nb] = __shfl_sync(~0u, scale, 8 * t4);
+            row_scale[2 * nb + 1] = __shfl_sync(~0u, scale, 8 * t4 + 4);
+        }
+        KeyRange see[S::kRowsLane];
+#pragma unroll
+        for (int r = 0; r < S::kRowsLane; ++r) {
+            const int row = 8 * (r >> 1) + 2 * t4 + (r & 1);
+            see[r] = visible(a, s, (row_first + (row < rows ? row : 0)) / int(a.group));
+            if (row >= rows) see[r].hi = 0;
         }
         // positions that every row of the tile sees
         const KeyRange each{visible(a, s, i1).lo, visible(a, s, i0).hi};
 
-        float o[D / 8][4];
+        float o[D / 16][S::kBlocks][4];
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
+        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+            for (int nb = 0; nb < S::kBlocks; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][nb][e] = 0.f;
         float m[S::kRowsLane], l[S::kRowsLane];
 #pragma unroll
         for (int r = 0; r < S::kRowsLane; ++r) m[r] = -INFINITY, l[r] = 0.f;
@@ -425,111 +439,109 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
             const uint32_t k_at = smem_u32(stage), v_at = smem_u32(v_stage);
             const int pos0 = base + i * kUnit;
 
-            // scores of the rows by 16 keys
-            float sc[2][4];
+            // scores: keys g (c0, c1) and g + 8 (c2, c3) by rows 2 t and 2 t + 1 of each block
+            float sc[S::kBlocks][4];
 #pragma unroll
-            for (int nb = 0; nb < 2; ++nb)
+            for (int nb = 0; nb < S::kBlocks; ++nb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[nb][e] = 0.f;
             if (!S::kFp8) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t kr[4];
-                    ldmatrix4(kr, k_at + S::place_k((lane & 7u) + (lane >> 4) * 8u, 2u * k + ((lane >> 3) & 1u)));
-                    mma_16816<S::kHalf>(sc[0], q[k], kr[0], kr[1]);
-                    mma_16816<S::kHalf>(sc[1], q[k], kr[2], kr[3]);
+                    ldmatrix4(kr, k_at + S::place_k((lane & 7u) + ((lane >> 3) & 1u) * 8u, 2u * k + (lane >> 4)));
+#pragma unroll
+                    for (int nb = 0; nb < S::kBlocks; ++nb) mma_16816<S::kHalf>(sc[nb], kr, q[nb][k][0], q[nb][k][1]);
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 w0 = *reinterpret_cast<const uint4*>(stage + S::place_k(uint32_t(g), uint32_t(c * 4 + t4)));
+                    const uint4 w8 =
+                        *reinterpret_cast<const uint4*>(stage + S::place_k(uint32_t(g + 8), uint32_t(c * 4 + t4)));
+                    const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, up[4] = {w8.x, w8.y, w8.z, w8.w};
 #pragma unroll
-                    for (int nb = 0; nb < 2; ++nb) {
-                        const uint4 w4 = *reinterpret_cast<const uint4*>(
-                            stage + S::place_k(uint32_t(nb * 8 + g), uint32_t(c * 4 + t4)));
-                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t kr[4] = {fp8_pair_to_half2<S::kE5M2>(lo[j], 0), fp8_pair_to_half2<S::kE5M2>(up[j], 0),
+                                                fp8_pair_to_half2<S::kE5M2>(lo[j], 1), fp8_pair_to_half2<S::kE5M2>(up[j], 1)};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_16816<S::kHalf>(sc[nb], q[c * 4 + j], fp8_pair_to_half2<S::kE5M2>(w[j], 0),
-                                                fp8_pair_to_half2<S::kE5M2>(w[j], 1));
+                        for (int nb = 0; nb < S::kBlocks; ++nb)
+                            mma_16816<S::kHalf>(sc[nb], kr, q[nb][c * 4 + j][0], q[nb][c * 4 + j][1]);
                     }
+                }
             }
-            // scales of the lane's four keys; V's also as exponents
-            float ks[4], vs[4], ve[4];
+            // scales of the lane's two keys; V's also as exponents
+            float ks[2], vs[2], ve[2];
             if (S::kFp8) {
-                const uint8_t* at = scale_ring + uint32_t(i) % S::kStages * 2 * kKeys + 2 * t4;
+                const uint8_t* at = scale_ring + uint32_t(i) % S::kStages * 2 * kKeys + g;
 #pragma unroll
-                for (int x = 0; x < 4; x += 2) {
-                    const uint32_t k2 = *reinterpret_cast<const uint16_t*>(at + 4 * x);
-                    const uint32_t v2 = *reinterpret_cast<const uint16_t*>(at + kKeys + 4 * x);
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint32_t kb = (k2 >> (8 * y)) & 0xFFu, vb = (v2 >> (8 * y)) & 0xFFu;
-                        ks[x + y] = scale_value(kb);
-                        vs[x + y] = scale_value(vb);
-                        // at least -80, which bounds the sums of 2^(s-m)
-                        ve[x + y] = __uint_as_float(0x4B000000u | max(vb, 47u)) - 8388735.f;
-                    }
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t kb = at[8 * x], vb = at[kKeys + 8 * x];
+                    ks[x] = scale_value(kb);
+                    vs[x] = scale_value(vb);
+                    // at least -80, which bounds the sums of 2^(s-m)
+                    ve[x] = __uint_as_float(0x4B000000u | max(vb, 47u)) - 8388735.f;
                 }
             }
             // scale, mask, running maximum
             const bool masked = pos0 < each.lo || pos0 + kKeys > each.hi;
             if (S::kFp8 && masked) {
                 // a slot that nothing was written to may hold 255, and 0 times infinity is NaN
-#pragma unroll
-                for (int x = 0; x < 4; ++x) vs[x] = fminf(vs[x], 1.7014118e38f);
+                vs[0] = fminf(vs[0], 1.7014118e38f);
+                vs[1] = fminf(vs[1], 1.7014118e38f);
             }
             float top[S::kRowsLane];
+            bool grew = false;
 #pragma unroll
             for (int r = 0; r < S::kRowsLane; ++r) {
                 top[r] = -INFINITY;
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = sc[nb][2 * r + e] * row_scale[r];
-                        if (S::kFp8) x *= ks[nb * 2 + e];
-                        if (masked) {
-                            const int pos = pos0 + nb * 8 + 2 * t4 + e;
-                            x = pos >= see[r].lo && pos < see[r].hi ? x : -INFINITY;
-                        }
-                        sc[nb][2 * r + e] = x;
-                        top[r] = fmaxf(top[r], S::kFp8 ? x + ve[nb * 2 + e] : x);
+                for (int x = 0; x < 2; ++x) {
+                    float y = sc[r >> 1][2 * x + (r & 1)] * row_scale[r];
+                    if (S::kFp8) y *= ks[x];
+                    if (masked) {
+                        const int pos = pos0 + g + 8 * x;
+                        y = pos >= see[r].lo && pos < see[r].hi ? y : -INFINITY;
                     }
-            }
-            bool grew = false;
+                    sc[r >> 1][2 * x + (r & 1)] = y;
+                    top[r] = fmaxf(top[r], S::kFp8 ? y + ve[x] : y);
+                }
 #pragma unroll
-            for (int r = 0; r < S::kRowsLane; ++r) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+                for (int d = 4; d < 32; d <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], d));
                 grew |= top[r] > m[r];
             }
             if (__any_sync(~0u, grew)) {
+                float f[S::kRowsLane];
 #pragma unroll
                 for (int r = 0; r < S::kRowsLane; ++r) {
                     const float now = fmaxf(top[r], m[r]);
-                    const float f = now == m[r] ? 1.f : exp2_fast(m[r] - now);
-                    l[r] *= f;
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        o[j][2 * r] *= f;
-                        o[j][2 * r + 1] *= f;
-                    }
+                    f[r] = now == m[r] ? 1.f : exp2_fast(m[r] - now);
+                    l[r] *= f[r];
                     m[r] = now;
                 }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int nb = 0; nb < S::kBlocks; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[j][nb][e] *= f[2 * nb + (e & 1)];
             }
-            uint32_t p[4] = {0u, 0u, 0u, 0u};
+            uint32_t p[S::kBlocks][2];
 #pragma unroll
-            for (int r = 0; r < S::kRowsLane; ++r) {
-                const float low = m[r] == -INFINITY ? 0.f : m[r] - S::kShift;
+            for (int nb = 0; nb < S::kBlocks; ++nb) {
+                float low[2];
 #pragma unroll
-                for (int nb = 0; nb < 2; ++nb) {
-                    float e0 = exp2_fast(sc[nb][2 * r] - low), e1 = exp2_fast(sc[nb][2 * r + 1] - low);
-                    l[r] += e0 + e1;
+                for (int e = 0; e < 2; ++e) low[e] = m[2 * nb + e] == -INFINITY ? 0.f : m[2 * nb + e] - S::kShift;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float e0 = exp2_fast(sc[nb][2 * x] - low[0]), e1 = exp2_fast(sc[nb][2 * x + 1] - low[1]);
+                    l[2 * nb] += e0;
+                    l[2 * nb + 1] += e1;
                     if (S::kFp8) {
-                        e0 *= vs[nb * 2];
-                        e1 *= vs[nb * 2 + 1];
+                        e0 *= vs[x];
+                        e1 *= vs[x];
                     }
-                    p[nb * 2 + r] = S::kHalf ? pack_half2(e0, e1) : pack_bf16x2(e0, e1);
+                    p[nb][x] = transpose8(S::kHalf ? pack_half2(e0, e1) : pack_bf16x2(e0, e1));
                 }
             }
 
@@ -548,10 +560,10 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                     for (int x = 0; x < kKeys; ++x) {
                         const int pos = pos0 + x;
 #pragma unroll
-                        for (int j = 0; j < D / 8; ++j)
+                        for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t byte = uint32_t(S::out_dim(j, t4, e)) * (S::kFp8 ? 1u : 2u);
+                            for (int up = 0; up < 2; ++up) {
+                                const uint32_t byte = uint32_t(S::out_dim(j, g, up)) * (S::kFp8 ? 1u : 2u);
                                 const uint8_t* at = v_stage + S::place_v(uint32_t(x), byte >> 4) + (byte & 15u);
                                 float v;
                                 if (S::kFp8)
@@ -563,7 +575,7 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                                 if (!(fabsf(v) < INFINITY)) {
 #pragma unroll
                                     for (int r = 0; r < S::kRowsLane; ++r)
-                                        if (pos >= see[r].lo && pos < see[r].hi) o[j][2 * r + e] += v;
+                                        if (pos >= see[r].lo && pos < see[r].hi) o[j][r >> 1][2 * up + (r & 1)] += v;
                                 }
                             }
                     }
@@ -589,14 +601,14 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                 }
             }
 
-            // weights times values
+            // values times weights
             if (!S::kFp8) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     uint32_t vr[4];
-                    ldmatrix4_trans(vr, v_at + S::place_v((lane & 7u) + ((lane >> 3) & 1u) * 8u, 2u * j + (lane >> 4)));
-                    mma_16816<S::kHalf>(o[2 * j], p, vr[0], vr[1]);
-                    mma_16816<S::kHalf>(o[2 * j + 1], p, vr[2], vr[3]);
+                    ldmatrix4_trans(vr, v_at + S::place_v((lane & 7u) + (lane >> 4) * 8u, 2u * j + ((lane >> 3) & 1u)));
+#pragma unroll
+                    for (int nb = 0; nb < S::kBlocks; ++nb) mma_16816<S::kHalf>(o[j][nb], vr, p[nb][0], p[nb][1]);
                 }
             } else {
                 // the lane's D / 8 bytes of each of its four keys
@@ -615,39 +627,37 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                     }
                 }
 #pragma unroll
-                for (int y = 0; y < W; ++y)
+                for (int j = 0; j < D / 16; ++j) {
+                    // bytes 2 j and 2 j + 1 of keys (0, 1) and of keys (2, 3), key pairs together
+                    const uint32_t sel = j & 1 ? 0x7362u : 0x5140u;
+                    const uint32_t ab = __byte_perm(w[0][j / 2], w[1][j / 2], sel);
+                    const uint32_t cd = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
+                    const uint32_t vr[4] = {fp8_pair_to_half2<S::kE5M2>(ab, 0), fp8_pair_to_half2<S::kE5M2>(ab, 1),
+                                            fp8_pair_to_half2<S::kE5M2>(cd, 0), fp8_pair_to_half2<S::kE5M2>(cd, 1)};
 #pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        // bytes 2 h2 and 2 h2 + 1 of keys (0, 1) and of keys (2, 3), key pairs together
-                        const uint32_t sel = h2 ? 0x7362u : 0x5140u;
-                        const uint32_t ab = __byte_perm(w[0][y], w[1][y], sel);
-                        const uint32_t cd = __byte_perm(w[2][y], w[3][y], sel);
-                        mma_16816<S::kHalf>(o[4 * y + 2 * h2], p, fp8_pair_to_half2<S::kE5M2>(ab, 0),
-                                            fp8_pair_to_half2<S::kE5M2>(cd, 0));
-                        mma_16816<S::kHalf>(o[4 * y + 2 * h2 + 1], p, fp8_pair_to_half2<S::kE5M2>(ab, 1),
-                                            fp8_pair_to_half2<S::kE5M2>(cd, 1));
-                    }
+                    for (int nb = 0; nb < S::kBlocks; ++nb) mma_16816<S::kHalf>(o[j][nb], vr, p[nb][0], p[nb][1]);
+                }
             }
         }
         copy_wait<0>();
 
-        // Join the four warps.  The sums l are still one quad lane's; m is the row's.
+        // Join the four warps.  The sums l are still of the lane's keys; m is the row's.
         __syncthreads();
         float* m_o = reinterpret_cast<float*>(smem);      // [warp][row][D]
         float* m_ml = m_o + kWarps * ROWS * D;            // [warp][row][m, l]
 #pragma unroll
         for (int r = 0; r < S::kRowsLane; ++r) {
-            l[r] += __shfl_xor_sync(~0u, l[r], 1);
-            l[r] += __shfl_xor_sync(~0u, l[r], 2);
-            const int row = int(warp) * ROWS + g + 8 * r;
-            if (t4 == 0) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], d);
+            const int row = int(warp) * ROWS + 8 * (r >> 1) + 2 * t4 + (r & 1);
+            if (g == 0) {
                 m_ml[2 * row] = m[r];
                 m_ml[2 * row + 1] = l[r];
             }
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
+            for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) m_o[row * D + S::out_dim(j, t4, e)] = o[j][2 * r + e];
+                for (int up = 0; up < 2; ++up) m_o[row * D + S::out_dim(j, g, up)] = o[j][r >> 1][2 * up + (r & 1)];
         }
         __syncthreads();
         const bool whole = u == item_start && stop == item_end;
