@@ -207,14 +207,16 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
         if (tid == 0) s_scan[kWarps] = total;
         return x + before;
     };
-    uint64_t units = 0;
+    constexpr uint64_t kUnitsMask = (uint64_t(1) << kItemsAt) - 1;
+    uint64_t units = 0, mine = 0, upto_mine = 0;  // mine: of the last round, the only one of up to 128 sequences
     for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kWarps * 32) {
-        scan(b0 + tid < a.b.batch ? weight_of(b0 + tid) + items_of(b0 + tid) : 0);
+        mine = b0 + tid < a.b.batch ? weight_of(b0 + tid) : 0;
+        upto_mine = scan(mine + (mine > 0 ? items_of(b0 + tid) : 0)) & kUnitsMask;
         __syncthreads();
         units += s_scan[kWarps];
     }
     const uint64_t items = units >> kItemsAt;
-    units &= (uint64_t(1) << kItemsAt) - 1;
+    units &= kUnitsMask;
     const uint64_t most = max(items, (units + kMinUnits - 1) / kMinUnits);
     const uint32_t ctas = most < gridDim.x ? uint32_t(most) : gridDim.x;
     uint64_t u = 0, end = 0;
@@ -230,14 +232,17 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
         __shared__ uint64_t s_start;
         uint64_t base = 0;
         for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kWarps * 32) {
-            const uint64_t w = b0 + tid < a.b.batch ? weight_of(b0 + tid) : 0;
-            const uint64_t upto = base + scan(w);
+            uint64_t w = mine, upto = upto_mine;
+            if (a.b.batch > kWarps * 32) {
+                w = b0 + tid < a.b.batch ? weight_of(b0 + tid) : 0;
+                upto = base + scan(w);
+            }
             if (w > 0 && u >= upto - w && u < upto) {
                 s_b = b0 + tid;
                 s_start = upto - w;
             }
             __syncthreads();
-            base += s_scan[kWarps];
+            if (a.b.batch > kWarps * 32) base += s_scan[kWarps];
             if (base > u) break;
         }
         b = s_b;
@@ -265,76 +270,6 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
         const int i0 = row_first / int(a.group), i1 = (row_first + rows - 1) / int(a.group);
         const KeyRange keys = visible(a, s, i0, i1);
         const int base = (all.lo / kUnit + int(u - item_start)) * kUnit + int(warp) * kKeys;
-
-        // queries, as the second operand: row g of each block
-        uint32_t q[S::kBlocks][D / 16][2];
-        float row_scale[S::kRowsLane];
-#pragma unroll
-        for (int nb = 0; nb < S::kBlocks; ++nb) {
-            const int r = g + 8 * nb;
-            const bool there = r < rows;
-            const int i = (row_first + (there ? r : 0)) / int(a.group);
-            const uint32_t qh = head * a.group + uint32_t((row_first + (there ? r : 0)) % int(a.group));
-            const uint16_t* src = a.q.d + uint64_t(s.row0 + i) * a.q.token_stride + uint64_t(qh) * a.q.head_stride;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                // FP8: dims are dealt so that a lane's share of a key is 16 contiguous bytes
-                const int d0 = S::kFp8 ? (k / 4) * 64 + t4 * 16 + (k % 4) * 4 : k * 16 + 2 * t4;
-                const int d1 = S::kFp8 ? d0 + 2 : d0 + 8;
-                q[nb][k][0] = there ? *reinterpret_cast<const uint32_t*>(src + d0) : 0u;
-                q[nb][k][1] = there ? *reinterpret_cast<const uint32_t*>(src + d1) : 0u;
-            }
-            float scale = a.scale_log2;
-            if (S::kFp8 && !a.q_half) {
-                // BF16 to FP16 by way of the power of two that brings the row's largest
-                // finite element to [2^14, 2^15): what FP16 loses of the small ones is
-                // below 2^-39 of it
-                uint32_t top = 0;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint32_t lo = q[nb][k][y] & 0x7FFFu, hi = (q[nb][k][y] >> 16) & 0x7FFFu;
-                        top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-                    }
-                top = max(top, __shfl_xor_sync(~0u, top, 1));
-                top = max(top, __shfl_xor_sync(~0u, top, 2));
-                // 2^up takes exponent e to 14, within what one normal factor can do
-                const int e = int(top >> 7) - 127, up = min(126, 14 - e);
-                const float f = __uint_as_float(uint32_t(127 + up) << 23);
-                scale *= __uint_as_float(uint32_t(127 - up) << 23);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float2 v = bf16x2_to_float2(q[nb][k][y]);
-                        q[nb][k][y] = pack_half2(v.x * f, v.y * f);
-                    }
-            }
-            // the scores' rows are the lane's 2 t and 2 t + 1
-            row_scale[2 * nb] = __shfl_sync(~0u, scale, 8 * t4);
-            row_scale[2 * nb + 1] = __shfl_sync(~0u, scale, 8 * t4 + 4);
-        }
-        KeyRange see[S::kRowsLane];
-#pragma unroll
-        for (int r = 0; r < S::kRowsLane; ++r) {
-            const int row = 8 * (r >> 1) + 2 * t4 + (r & 1);
-            see[r] = visible(a, s, (row_first + (row < rows ? row : 0)) / int(a.group));
-            if (row >= rows) see[r].hi = 0;
-        }
-        // positions that every row of the tile sees
-        const KeyRange each{visible(a, s, i1).lo, visible(a, s, i0).hi};
-
-        float o[D / 16][S::kBlocks][4];
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-            for (int nb = 0; nb < S::kBlocks; ++nb)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[j][nb][e] = 0.f;
-        float m[S::kRowsLane], l[S::kRowsLane];
-#pragma unroll
-        for (int r = 0; r < S::kRowsLane; ++r) m[r] = -INFINITY, l[r] = 0.f;
 
         // Copies start kStages - 1 stages ahead of their use, and the page of a
         // stage's keys is looked up a stage before that: by lane i (mod 16) for key
@@ -427,6 +362,76 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
             page = page_next;
             page_next = page_of(i + 2);
         }
+
+        // queries, as the second operand: row g of each block
+        uint32_t q[S::kBlocks][D / 16][2];
+        float row_scale[S::kRowsLane];
+#pragma unroll
+        for (int nb = 0; nb < S::kBlocks; ++nb) {
+            const int r = g + 8 * nb;
+            const bool there = r < rows;
+            const int i = (row_first + (there ? r : 0)) / int(a.group);
+            const uint32_t qh = head * a.group + uint32_t((row_first + (there ? r : 0)) % int(a.group));
+            const uint16_t* src = a.q.d + uint64_t(s.row0 + i) * a.q.token_stride + uint64_t(qh) * a.q.head_stride;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                // FP8: dims are dealt so that a lane's share of a key is 16 contiguous bytes
+                const int d0 = S::kFp8 ? (k / 4) * 64 + t4 * 16 + (k % 4) * 4 : k * 16 + 2 * t4;
+                const int d1 = S::kFp8 ? d0 + 2 : d0 + 8;
+                q[nb][k][0] = there ? *reinterpret_cast<const uint32_t*>(src + d0) : 0u;
+                q[nb][k][1] = there ? *reinterpret_cast<const uint32_t*>(src + d1) : 0u;
+            }
+            float scale = a.scale_log2;
+            if (S::kFp8 && !a.q_half) {
+                // BF16 to FP16 by way of the power of two that brings the row's largest
+                // finite element to [2^14, 2^15): what FP16 loses of the small ones is
+                // below 2^-39 of it
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t lo = q[nb][k][y] & 0x7FFFu, hi = (q[nb][k][y] >> 16) & 0x7FFFu;
+                        top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                    }
+                top = max(top, __shfl_xor_sync(~0u, top, 1));
+                top = max(top, __shfl_xor_sync(~0u, top, 2));
+                // 2^up takes exponent e to 14, within what one normal factor can do
+                const int e = int(top >> 7) - 127, up = min(126, 14 - e);
+                const float f = __uint_as_float(uint32_t(127 + up) << 23);
+                scale *= __uint_as_float(uint32_t(127 - up) << 23);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 v = bf16x2_to_float2(q[nb][k][y]);
+                        q[nb][k][y] = pack_half2(v.x * f, v.y * f);
+                    }
+            }
+            // the scores' rows are the lane's 2 t and 2 t + 1
+            row_scale[2 * nb] = __shfl_sync(~0u, scale, 8 * t4);
+            row_scale[2 * nb + 1] = __shfl_sync(~0u, scale, 8 * t4 + 4);
+        }
+        KeyRange see[S::kRowsLane];
+#pragma unroll
+        for (int r = 0; r < S::kRowsLane; ++r) {
+            const int row = 8 * (r >> 1) + 2 * t4 + (r & 1);
+            see[r] = visible(a, s, (row_first + (row < rows ? row : 0)) / int(a.group));
+            if (row >= rows) see[r].hi = 0;
+        }
+        // positions that every row of the tile sees
+        const KeyRange each{visible(a, s, i1).lo, visible(a, s, i0).hi};
+
+        float o[D / 16][S::kBlocks][4];
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int nb = 0; nb < S::kBlocks; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][nb][e] = 0.f;
+        float m[S::kRowsLane], l[S::kRowsLane];
+#pragma unroll
+        for (int r = 0; r < S::kRowsLane; ++r) m[r] = -INFINITY, l[r] = 0.f;
 
         for (int i = 0; i < n_units; ++i) {
             copy_wait<S::kStages - 2>();
