@@ -233,12 +233,16 @@ struct Chunk {
     static constexpr bool kTma = FMT == 3;
     static constexpr bool kFp8 = FMT == 1 || FMT == 2;
     static constexpr bool kE5M2 = FMT == 1;
-    // Scores are products in the queries' type, the sums over V in FP16 for an
-    // FP16 cache and else in BF16, which holds FP8 values times their scales.
-    static constexpr bool kPvHalf = !kFp8 && H;
-    // K's scales fold into K in BF16; FP16 has not their range, so there the
-    // scores' columns take them.
+    // Both products are in the queries' type.  BF16 holds FP8 values times their
+    // scales exactly.  FP16 has not their range: there K goes without its scales,
+    // which the scores' columns take, and V is held by halves, which the last
+    // division makes good: what was written from FP16 can be 65,536 after its
+    // rounding to FP8.  Up to 131,008 that is exact, but for a half of FP16's
+    // least step below its normal numbers; larger values are infinite, as they
+    // are for a read in FP16.
+    static constexpr bool kPvHalf = H;
     static constexpr bool kScoreScale = kFp8 && H;
+    static constexpr float kValueScale = kFp8 && H ? 0.5f : 1.f;
     // FP16 weights are up to 2^kLag above 2^7, within FP16's range, so that
     // those down to 2^-28 of the largest are not lost.
     static constexpr float kShift = kPvHalf ? 7.f : 0.f;
@@ -381,6 +385,14 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
                         if (C::kScoreScale && !is_v) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) o[j] = fp8_pair_to_half2<C::kE5M2>(w[j / 2], j & 1);
+                        } else if (H) {
+                            const float f = C::kValueScale * scale_value(scale[i]);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 v = half2_to_float2(fp8_pair_to_half2<C::kE5M2>(w[j / 2], j & 1));
+                                const float2 z = mul2(v, make_float2(f, f));
+                                o[j] = pack_half2(z.x, z.y);
+                            }
                         } else {
                             // exact: BF16 holds the value and its product with a power of two
                             const uint32_t s16 = scale[i] * 0x00800080u;
@@ -909,7 +921,7 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
                              : ((m == -INFINITY ? 0.f : m * scale) - C::kShift + log2f(l)) * 0.693147180559945309f;
             }
         };
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float inv = sum == 0.f ? 0.f : 1.f / (C::kValueScale * sum);
         float* mine = slot(blockIdx.x);
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
@@ -958,7 +970,7 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
 #pragma unroll
                     for (int y = 0; y < D; ++y) o[y] += f * __ldcg(part + y * kTileRows);
                 }
-                const float joined = l == 0.f ? 0.f : 1.f / l;
+                const float joined = l == 0.f ? 0.f : 1.f / (C::kValueScale * l);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) stage32(k, o + 32 * k, joined);
                 put(m, l);

@@ -109,14 +109,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return r;
 }
 
-// Two FP8 values as BF16, exactly (FP16 holds both types, BF16 their 3- and
-// 4-bit significands over FP16's range).
-template <bool E5M2>
-__device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t two) {
-    const float2 f = half2_to_float2(fp8x2_to_half2<E5M2>(two));
-    return pack_bf16x2(f.x, f.y);
-}
-
 // Two 32-bit operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 r;

@@ -68,29 +68,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Whether the phase is complete, without suspending the thread as try_wait may.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// The same wait as mbar_wait by asking again and again, for a thread on whose
-// way back from a suspension others wait.
-__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity) {
-    if (mbar_test(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!mbar_test(bar, parity)) {
-        if (clock64() - t0 > kWaitLimitCycles) return false;
-    }
-    return true;
-}
-
 // Global -> shared bulk copy; completes `bytes` of the barrier's transaction
 // count.  dst, src and bytes must be multiples of 16.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

@@ -292,3 +292,22 @@ def test_offsets_past_32_bits():
     out, lse, status = run(small, q, 0.1)
     assert status == sz.OK
     check_attention(small, out, lse, attention(small, q, 0.1), BF16)
+
+
+@pytest.mark.parametrize("dtype", [E5M2, E4M3])
+@pytest.mark.parametrize("lens", [[(1, 300), (2, 35)], [(40, 300), (20, 150)]])
+def test_largest_fp16_values_in_fp8_pages(dtype, lens):
+    """65,504 is 65,536 after its rounding to FP8, which FP16 does not hold;
+    the sums over V, of both signs, do fit the result."""
+    step = Step(dtype, lens, x=FP16)
+    top, k = (32768.0, 1) if dtype == E5M2 else (256.0, 8)
+    sign = torch.randint(0, 2, step.host["v"].shape, generator=step.gen).double() * 2 - 1
+    step.cache.v.copy_((sign * top).float().to(dtype))
+    step.cache.v_scale.fill_(127 + k)
+    step.host["v"] = torch.ldexp(sign * top, torch.tensor(k))
+    q = (torch.randn(step.tokens, 8, 128, generator=step.gen) * 0.1).to(FP16)
+    out, lse, status = run(step, q, 0.05, causal=False)
+    assert status == sz.OK
+    ref = attention(step, q, 0.05, causal=False)
+    assert bool((ref[0].abs() < 65504).all())
+    check_attention(step, out, lse, ref, FP16)
