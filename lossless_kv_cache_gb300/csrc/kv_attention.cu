@@ -36,7 +36,7 @@ int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, Plan* p) {
     p->chunk = uint64_t(b.max_tokens) * p->group > kStepRowsMax;
     if (p->chunk) {
         p->ctas = chunk_ctas(rows, b.batch, c.kv_heads, b.max_kv_len);
-        size_of(p, chunk_plan_bytes(p->ctas), 2ull * p->ctas, chunk_part_floats(c.head_dim));
+        size_of(p, chunk_plan_bytes(p->ctas), 0, chunk_part_floats(c.head_dim));
     } else {
         // tiles of rows over all sequences: each has a partial one at most
         const uint64_t tiles = std::min<uint64_t>((rows + 7) / 8 + b.batch, rows);

@@ -9,8 +9,9 @@
 // end, and a share ends in the middle of an item where it has to.  The parts
 // of such an item (maximum m, sum l and unnormalised sums o of each row) go
 // to the workspace, at most two a CTA: the first CTA's part in its slot 1, a
-// continuation in slot 0.  Whichever CTA counts the last part joins them, in
-// the order of the parts, so the result does not depend on the timing.
+// continuation in slot 0.  They are joined in the order of the parts, so that
+// the result does not depend on the timing: by whichever CTA counts the last
+// one in a step, where parts are small, and by a kernel of its own in a chunk.
 #pragma once
 
 #include "kv_common.cuh"
@@ -31,7 +32,7 @@ struct AttentionArgs {
     float lag;  // chunk kernel: how far the reference may lag the maximum, before the scale
     int causal;
     uint32_t window;
-    uint32_t* counters;  // workspace, one (chunk kernel: two) a CTA
+    uint32_t* counters;  // workspace, one a CTA (step kernel)
     float* parts;        // workspace, two slots a CTA
     int* status;
 };

@@ -59,6 +59,13 @@ struct ChunkStart {
     uint64_t group_start;  // first unit of the (sequence, tile)'s kv heads
 };
 
+// The item that a CTA begins and others go on with: what their parts' join has
+// to know of it.  rows = 0: none.
+struct alignas(16) ChunkSplit {
+    int row0, row_first, rows;
+    uint32_t head, last_cta;
+};
+
 struct ChunkPlan {
     uint64_t units;
     uint32_t ctas, pad;
@@ -85,7 +92,7 @@ __device__ __forceinline__ Tile tile_of(const AttentionArgs& a, const KvSeq& s, 
 }
 
 // Deals the units of all items to the CTAs (see kv_attention.cuh) and clears
-// the counters and the status word.  Items are in the order sequence, tile, kv
+// the status word.  Items are in the order sequence, tile, kv
 // head.  One CTA: sequences are dealt to its warps, a lane sums one of one or
 // two tiles and the whole warp one of more; then a scan over the sequences,
 // and the same walk again to find where each CTA's share starts.
@@ -98,7 +105,6 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     __shared__ int s_bad;
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     if (tid == 0) s_bad = 0;
-    for (uint32_t i = tid; i < 2 * grid; i += kPlanThreads) a.counters[i] = 0;
     __syncthreads();
     const auto weight = [&](const KvSeq& s, int tile) -> uint64_t {
         return uint64_t(tile_of(a, s, tile).units + kItemCost) * a.c.kv_heads;
@@ -161,49 +167,59 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     };
     static_assert(kPlanWarps == 32, "the scan over warps");
     uint64_t units = 0;
-    KvSeq s{0, 0, 0, true};
-    for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) {
-        s = seq_at(b0 + nth);
-        units += round_units(s);
-    }
+    for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) units += round_units(seq_at(b0 + nth));
     const uint32_t ctas = uint32_t(min(uint64_t(grid), max(units, uint64_t(1))));
     uint64_t base = 0;
     for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) {
-        uint64_t total = 0;
-        if (a.b.batch > kPlanThreads) {
-            s = seq_at(b0 + nth);
-            total = round_units(s);
-        }
-        // the CTAs whose share starts within [lo, hi)
-        const auto starts = [&](uint32_t b, uint32_t tile, uint64_t lo, uint64_t hi) {
-            for (uint64_t c = (lo * ctas + units - 1) / units; c < ctas && share_start(units, ctas, c) < hi; ++c)
-                plan->start[c] = ChunkStart{b, tile, lo};
-        };
-        const auto from_of = [&](uint32_t at) { return base + (at == 0 ? 0 : s_upto[at - 1]); };
-        const int n = tile_count(a, s);
-        if (n <= 2) {
-            uint64_t from = from_of(nth);
-            for (int i = 0; i < n; ++i) {
-                const uint64_t x = weight(s, i);
-                starts(b0 + nth, uint32_t(i), from, from + x);
-                from += x;
+        uint64_t total = units;
+        if (a.b.batch > kPlanThreads) total = round_units(seq_at(b0 + nth));
+        // a lane finds the sequence that a share starts in, and its tile where they are one or two
+        const uint64_t u = nth < ctas ? share_start(units, ctas, nth) : ~uint64_t(0);
+        uint64_t from = 0;  // the units before the sequence or tile
+        uint32_t at = 0;
+        KvSeq o{0, 0, 0, true};
+        if (u >= base && u < base + total) {
+            uint32_t last = kPlanThreads - 1;
+            while (at < last) {
+                const uint32_t mid = (at + last) / 2;
+                if (s_upto[mid] > u - base)
+                    last = mid;
+                else
+                    at = mid + 1;
             }
+            from = base + (at == 0 ? 0 : s_upto[at - 1]);
+            o = load_seq(a.b, b0 + at);
         }
-        for_large(s, [&](const KvSeq& o, uint32_t at) {
-            uint64_t from = from_of(at);
-            for (int i0 = 0, tiles = tile_count(a, o); i0 < tiles; i0 += 32) {
+        const int n = tile_count(a, o);
+        if (n > 0 && n <= 2) {
+            const uint64_t x = weight(o, 0);
+            const uint32_t tile = n == 2 && u >= from + x ? 1 : 0;
+            plan->start[nth] = ChunkStart{b0 + at, tile, from + tile * x};
+        }
+        // the warp finds the tile among more
+        uint32_t many = __ballot_sync(~0u, n > 2);
+        while (many) {
+            const int src = __ffs(many) - 1;
+            many &= many - 1;
+            const KvSeq p{0, __shfl_sync(~0u, o.t, src), __shfl_sync(~0u, o.n, src), true};
+            const uint64_t v = __shfl_sync(~0u, u, src);
+            const uint32_t b = b0 + __shfl_sync(~0u, at, src);
+            uint64_t f = __shfl_sync(~0u, from, src);
+            for (int i0 = 0, tiles = tile_count(a, p); i0 < tiles; i0 += 32) {
                 const int i = i0 + int(lane);
-                const uint64_t x = i < tiles ? weight(o, i) : 0;
+                const uint64_t x = i < tiles ? weight(p, i) : 0;
                 uint64_t y = x;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const uint64_t z = __shfl_up_sync(~0u, y, d);
                     if (int(lane) >= d) y += z;
                 }
-                if (x > 0) starts(b0 + at, uint32_t(i), from + y - x, from + y);
-                from += __shfl_sync(~0u, y, 31);
+                if (v >= f + y - x && v < f + y)
+                    plan->start[uint32_t(src) * kPlanWarps + warp] = ChunkStart{b, uint32_t(i), f + y - x};
+                f += __shfl_sync(~0u, y, 31);
+                if (v < f) break;
             }
-        });
+        }
         base += total;
     }
     __syncthreads();
@@ -226,6 +242,14 @@ struct Segment {
 
 constexpr int kSegments = 4;  // ring of pieces
 
+// Weights are 2^shift times the exponentials: FP16 ones are then up to 2^8, the
+// lag, above 2^7, within FP16's range, and those down to 2^-28 of the largest
+// are not lost.
+template <bool H>
+__host__ __device__ constexpr float weight_shift() {
+    return H ? 7.f : 0.f;
+}
+
 // FMT 0: cache of the queries' 16-bit type, 1: E5M2, 2: E4M3, 3: as 0, read
 // through tensor maps (pages of 8 tokens and more).
 template <int FMT, bool H, int D>
@@ -243,9 +267,7 @@ struct Chunk {
     static constexpr bool kPvHalf = H;
     static constexpr bool kScoreScale = kFp8 && H;
     static constexpr float kValueScale = kFp8 && H ? 0.5f : 1.f;
-    // FP16 weights are up to 2^kLag above 2^7, within FP16's range, so that
-    // those down to 2^-28 of the largest are not lost.
-    static constexpr float kShift = kPvHalf ? 7.f : 0.f;
+    static constexpr float kShift = weight_shift<H>();
     static constexpr int kHalves = D / 64;                 // blocks of 64 columns, 128 bytes a row
     static constexpr int kBlockBytes = 128 * 128;
     static constexpr int kTileBytes = kHalves * kBlockBytes;
@@ -259,7 +281,6 @@ struct Chunk {
     static constexpr int kRawBytes = 128 * D;
     static constexpr int kChunks = kFp8 ? D / 16 : D / 8;  // 16-byte pieces of a cache row
     static constexpr int kRowStep = 128 / kChunks;         // rows that the loaders copy at a time
-    static constexpr int kPartFloats = kTileRows * (D + 2);  // of one group
 
     struct Shared {
         uint8_t q[2][kTileBytes];
@@ -272,7 +293,7 @@ struct Chunk {
         uint64_t freed[kDepth];          // K of unit u and V of unit u - 1 are no longer read
         uint64_t q_full[2], s_full[2], p_full[2], o_full[2], noted, drained;
         uint64_t seg_full[kSegments], seg_empty[kSegments];
-        uint32_t tmem, joined[2];
+        uint32_t tmem;
         Segment seg[kSegments];
     };
     static constexpr int kSmem = int(sizeof(Shared));
@@ -281,7 +302,9 @@ struct Chunk {
 // Walks the CTA's share and describes its pieces to the other roles (one
 // thread, ahead of them by up to kSegments).
 template <class Shared>
-__device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh, const ChunkPlan* plan, bool& ok) {
+__device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh, const ChunkPlan* plan, ChunkSplit* splits,
+                                             bool& ok) {
+    splits[blockIdx.x] = ChunkSplit{};
     const uint64_t units = __ldcg(&plan->units);
     const uint32_t ctas = __ldcg(&plan->ctas);
     uint64_t u = 0, end = 0, group_start = 0;
@@ -331,6 +354,8 @@ __device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh,
             g.b = b, g.head = head;
             g.first_cta = share_of(units, ctas, keys_start);
             g.last_cta = share_of(units, ctas, item_end - 1);
+            if (g.first_cta == blockIdx.x && g.last_cta != blockIdx.x)
+                splits[blockIdx.x] = ChunkSplit{g.row0, g.row_first, g.rows, head, g.last_cta};
         }
         if (i >= uint32_t(kSegments)) ok = mbar_wait(&sh.seg_empty[i % kSegments], (i / kSegments - 1) & 1u);
         if (!ok) break;
@@ -683,6 +708,19 @@ __device__ __noinline__ void note_special(const uint8_t* v, int from, int to, Re
     }
 }
 
+// Where a CTA's part of an item that CTA `first` begins is, of tile g: columns
+// o[0] .. o[D - 1], reference, sum of kTileRows floats each.
+template <int D>
+__device__ __forceinline__ float* part_at(const AttentionArgs& a, uint32_t cta, uint32_t first, uint32_t g) {
+    return a.parts + ((uint64_t(cta) * 2 + (cta == first ? 1 : 0)) * 2 + g) * (kTileRows * (D + 2));
+}
+
+// The natural logarithm of a row's sum of exponentials l against reference m.
+template <bool H>
+__device__ __forceinline__ float log_sum(float m, float l, float scale) {
+    return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m * scale) - weight_shift<H>() + log2f(l)) * 0.693147180559945309f;
+}
+
 template <int FMT, bool H, int D>
 __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Chunk<FMT, H, D>::Shared& sh,
                                              uint32_t tmem, bool& ok) {
@@ -888,9 +926,6 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
         await(&sh.o_full[g], segments++);
         const uint32_t first = w.first_cta, last = w.last_cta;
         const bool whole = first == last;
-        const auto slot = [&](uint32_t cta) {
-            return a.parts + ((uint64_t(cta) * 2 + (cta == first ? 1 : 0)) * 2 + uint32_t(g)) * C::kPartFloats + row;
-        };
         // 32 columns of the row, divided, to the stage
         const auto stage32 = [&](int k, const float* o, float f) {
 #pragma unroll
@@ -917,12 +952,12 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             if (a.lse && mine >= 0) {
                 const int r = w.row_first + int(row) + g * kTileRows, i = r / int(a.group);
                 a.lse[uint64_t(w.row0 + i) * a.q_heads + w.head * a.group + uint32_t(r - i * int(a.group))] =
-                    l == 0.f ? -INFINITY
-                             : ((m == -INFINITY ? 0.f : m * scale) - C::kShift + log2f(l)) * 0.693147180559945309f;
+                    log_sum<H>(m, l, scale);
             }
         };
         const float inv = sum == 0.f ? 0.f : 1.f / (C::kValueScale * sum);
-        float* mine = slot(blockIdx.x);
+        const bool live = int(row) + g * kTileRows < w.rows;
+        float* mine = part_at<D>(a, blockIdx.x, first, uint32_t(g)) + row;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
             uint32_t bits[32];
@@ -941,40 +976,16 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             }
             if (whole) {
                 stage32(k, o, inv);
-            } else {
+            } else if (live) {
 #pragma unroll
                 for (int y = 0; y < 32; ++y) mine[(32 * k + y) * kTileRows] = o[y];
             }
         }
         if (whole) {
             put(low, sum);
-        } else {
+        } else if (live) {
             mine[D * kTileRows] = low;
             mine[(D + 1) * kTileRows] = sum;
-            __threadfence();
-            named_barrier(2 + uint32_t(g), 128);
-            if (row == 0) sh.joined[g] = atomicAdd(a.counters + 2 * first + uint32_t(g), 1u) == last - first;
-            named_barrier(2 + uint32_t(g), 128);
-            if (sh.joined[g]) {
-                __threadfence();
-                float m = -INFINITY, l = 0.f;
-                for (uint32_t cta = first; cta <= last; ++cta) m = fmaxf(m, __ldcg(slot(cta) + D * kTileRows));
-                float o[D];
-#pragma unroll
-                for (int y = 0; y < D; ++y) o[y] = 0.f;
-                for (uint32_t cta = first; cta <= last; ++cta) {
-                    const float* part = slot(cta);
-                    const float mc = __ldcg(part + D * kTileRows);
-                    const float f = mc == m ? 1.f : exp2_fast((mc - m) * scale);
-                    l += f * __ldcg(part + (D + 1) * kTileRows);
-#pragma unroll
-                    for (int y = 0; y < D; ++y) o[y] += f * __ldcg(part + y * kTileRows);
-                }
-                const float joined = l == 0.f ? 0.f : 1.f / (C::kValueScale * l);
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) stage32(k, o + 32 * k, joined);
-                put(m, l);
-            }
         }
         // the loads of O are done before the next piece's product overwrites it
         tc_fence_before();
@@ -984,7 +995,7 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
 
 template <int FMT, bool H, int D>
 __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
-    kv_chunk_kernel(const __grid_constant__ AttentionArgs a, const ChunkPlan* plan,
+    kv_chunk_kernel(const __grid_constant__ AttentionArgs a, const ChunkPlan* plan, ChunkSplit* splits,
                     const __grid_constant__ ChunkMaps maps) {
     using C = Chunk<FMT, H, D>;
     extern __shared__ __align__(1024) uint8_t smem_chunk[];  // the swizzle goes by address bits below 1024
@@ -1014,7 +1025,8 @@ __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    wait_predecessor();  // the plan is written, counters and status clear
+    wait_predecessor();  // the plan is written, the status clear
+    release_successor();
     bool ok = true, bad = false;
     // registers of the launch: 384 threads of 168, 2 * 216 + 72 = 3 * 168, or 512 of 128,
     // 2 * 200 + 72 + 40 = 4 * 128
@@ -1034,7 +1046,7 @@ __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
         if (warp == 8) load_tma_role<C>(a, sh, &maps.k, &maps.v, ok, bad);
     }
     if (warp == C::kProductWarp) product_role<FMT, H, D>(sh, tmem, ok);
-    if (threadIdx.x == C::kSegmentWarp * 32u) segment_role(a, sh, plan, ok);
+    if (threadIdx.x == C::kSegmentWarp * 32u) segment_role(a, sh, plan, splits, ok);
     if (bad) report(a.status, SPLITZIP_ERR_INVALID_ARG);
     if (!ok) report(a.status, SPLITZIP_ERR_TIMEOUT);
     __syncwarp();
@@ -1045,6 +1057,80 @@ __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
         tmem_free(tmem, 512);
     }
 }
+
+// Joins the parts of the item that CTA blockIdx.x of the kernel above began, if
+// others went on with it.  A CTA has 32 rows, a lane a row; four warps share
+// the columns and four of each take every fourth part, joined in that order.
+// A kernel of its own, since the parts of a long context (for one sequence and
+// 8 kv heads 19 of up to 132 KB an item) are then read by many SMs, and not by
+// the one that wrote the last of them.
+constexpr int kJoinParts = 4, kJoinThreads = kJoinParts * 4 * 32;
+
+template <bool H, int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    kv_chunk_join_kernel(const __grid_constant__ AttentionArgs a, const ChunkSplit* splits, float value_scale) {
+    constexpr int kColumns = D / 4;
+    __shared__ float s_o[kJoinParts / 2][D][32], s_l[kJoinParts / 2][4][32];
+    wait_predecessor();
+    const uint32_t first = blockIdx.x, lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const int part0 = int(warp >> 2), col0 = int(warp & 3u) * kColumns;
+    const ChunkSplit w = splits[first];
+    if (int(blockIdx.y) * 32 >= w.rows) return;
+    const int row = int(blockIdx.y * 32u + lane);  // those past the last read what is there, and write nothing
+    const uint32_t g = uint32_t(row) / kTileRows, at = uint32_t(row) % kTileRows;
+    const float scale = a.scale_log2;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 8
+    for (uint32_t cta = first; cta <= w.last_cta; ++cta) m = fmaxf(m, part_at<D>(a, cta, first, g)[D * kTileRows + at]);
+    float o[kColumns];
+#pragma unroll
+    for (int y = 0; y < kColumns; ++y) o[y] = 0.f;
+#pragma unroll 2
+    for (uint32_t cta = first + uint32_t(part0); cta <= w.last_cta; cta += kJoinParts) {
+        const float* part = part_at<D>(a, cta, first, g) + at;
+        float x[kColumns];
+#pragma unroll
+        for (int y = 0; y < kColumns; ++y) x[y] = part[(col0 + y) * kTileRows];
+        // parts of no reference (a scale of about zero leaves it there) count as they are
+        const float mc = part[D * kTileRows], e = exp2_fast((mc - m) * scale), f = mc == m ? 1.f : e;
+        l += f * part[(D + 1) * kTileRows];
+#pragma unroll
+        for (int y = 0; y < kColumns; ++y) o[y] += f * x[y];
+    }
+#pragma unroll
+    for (int half = kJoinParts / 2; half > 0; half /= 2) {
+        if (part0 >= half && part0 < 2 * half) {
+#pragma unroll
+            for (int y = 0; y < kColumns; ++y) s_o[part0 - half][col0 + y][lane] = o[y];
+            s_l[part0 - half][warp & 3u][lane] = l;
+        }
+        __syncthreads();
+        if (part0 < half) {
+#pragma unroll
+            for (int y = 0; y < kColumns; ++y) o[y] += s_o[part0][col0 + y][lane];
+            l += s_l[part0][warp & 3u][lane];
+        }
+        __syncthreads();
+    }
+    if (part0 != 0 || row >= w.rows) return;
+    const float inv = l == 0.f ? 0.f : 1.f / (value_scale * l);
+    const int r = w.row_first + row, i = r / int(a.group);
+    const uint32_t head = w.head * a.group + uint32_t(r - i * int(a.group));
+    uint16_t* out = a.out.d + uint64_t(w.row0 + i) * a.out.token_stride + uint64_t(head) * a.out.head_stride + col0;
+#pragma unroll
+    for (int k = 0; k < kColumns / 8; ++k) {
+        uint32_t z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x = o[8 * k + 2 * e] * inv, y = o[8 * k + 2 * e + 1] * inv;
+            z[e] = H ? pack_half2(x, y) : pack_bf16x2(x, y);
+        }
+        reinterpret_cast<uint4*>(out)[k] = make_uint4(z[0], z[1], z[2], z[3]);
+    }
+    if (a.lse && col0 == 0) a.lse[uint64_t(w.row0 + i) * a.q_heads + head] = log_sum<H>(m, l, scale);
+}
+
+uint64_t plan_bytes(uint32_t ctas) { return sizeof(ChunkPlan) + uint64_t(ctas) * sizeof(ChunkStart); }
 
 template <int FMT, bool H, int D>
 int launch(const AttentionArgs& a, ChunkPlan* plan, const ChunkMaps& maps, uint32_t ctas, cudaStream_t s) {
@@ -1062,8 +1148,12 @@ int launch(const AttentionArgs& a, ChunkPlan* plan, const ChunkMaps& maps, uint3
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     }
     ChainedLaunch l(dim3(ctas), dim3(C::kThreads), C::kSmem, s);
-    if (cudaLaunchKernelEx(&l.cfg, kv_chunk_kernel<FMT, H, D>, a, static_cast<const ChunkPlan*>(plan), maps) !=
-        cudaSuccess) {
+    ChunkSplit* splits = reinterpret_cast<ChunkSplit*>(reinterpret_cast<uint8_t*>(plan) + plan_bytes(ctas));
+    ChainedLaunch join(dim3(ctas, kRows / 32), dim3(kJoinThreads), 0, s);
+    if (cudaLaunchKernelEx(&l.cfg, kv_chunk_kernel<FMT, H, D>, a, static_cast<const ChunkPlan*>(plan), splits, maps) !=
+            cudaSuccess ||
+        cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<H, D>, a, static_cast<const ChunkSplit*>(splits),
+                           C::kValueScale) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }
@@ -1097,7 +1187,7 @@ uint32_t chunk_ctas(uint64_t rows, uint64_t batch, uint64_t kv_heads, uint64_t k
 
 uint64_t chunk_part_floats(uint32_t head_dim) { return uint64_t(kRows) * (head_dim + 2); }
 
-uint64_t chunk_plan_bytes(uint32_t ctas) { return sizeof(ChunkPlan) + uint64_t(ctas) * sizeof(ChunkStart); }
+uint64_t chunk_plan_bytes(uint32_t ctas) { return plan_bytes(ctas) + uint64_t(ctas) * sizeof(ChunkSplit); }
 
 int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan_at, uint32_t ctas, cudaStream_t s) {
     ChunkPlan* plan = static_cast<ChunkPlan*>(plan_at);
