@@ -59,8 +59,8 @@ struct ChunkStart {
     uint64_t group_start;  // first unit of the (sequence, tile)'s kv heads
 };
 
-// The item that a CTA begins and others go on with: what their parts' join has
-// to know of it.  rows = 0: none.
+// The item that a CTA begins and others go on with: what the join of its parts
+// has to know of it.  rows = 0: none.
 struct alignas(16) ChunkSplit {
     int row0, row_first, rows;
     uint32_t head, last_cta;
@@ -94,8 +94,9 @@ __device__ __forceinline__ Tile tile_of(const AttentionArgs& a, const KvSeq& s, 
 // Deals the units of all items to the CTAs (see kv_attention.cuh) and clears
 // the status word.  Items are in the order sequence, tile, kv
 // head.  One CTA: sequences are dealt to its warps, a lane sums one of one or
-// two tiles and the whole warp one of more; then a scan over the sequences,
-// and the same walk again to find where each CTA's share starts.
+// two tiles and the whole warp one of more; then a scan over the sequences, and
+// where each CTA's share starts: by a search for the sequence and, where it has
+// more tiles than two, the same walk again.
 __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __grid_constant__ AttentionArgs a,
                                                                      ChunkPlan* plan, uint32_t grid) {
     release_successor();
@@ -167,19 +168,29 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     };
     static_assert(kPlanWarps == 32, "the scan over warps");
     uint64_t units = 0;
-    for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) units += round_units(seq_at(b0 + nth));
+    KvSeq s{0, 0, 0, true};
+    for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) {
+        s = seq_at(b0 + nth);
+        units += round_units(s);
+    }
     const uint32_t ctas = uint32_t(min(uint64_t(grid), max(units, uint64_t(1))));
     uint64_t base = 0;
     for (uint32_t b0 = 0; b0 < a.b.batch; b0 += kPlanThreads) {
         uint64_t total = units;
-        if (a.b.batch > kPlanThreads) total = round_units(seq_at(b0 + nth));
-        // a lane finds the sequence that a share starts in, and its tile where they are one or two
+        if (a.b.batch > kPlanThreads) {
+            s = seq_at(b0 + nth);
+            total = round_units(s);
+        }
+        // the CTAs whose share starts within [lo, hi); share_start(c) < hi without its division
+        const auto starts = [&](uint32_t b, uint32_t tile, uint64_t lo, uint64_t hi) {
+            for (uint64_t c = (lo * ctas + units - 1) / units; c < ctas && units * c < hi * ctas; ++c)
+                plan->start[c] = ChunkStart{b, tile, lo};
+        };
+        const auto from_of = [&](uint32_t at) { return base + (at == 0 ? 0 : s_upto[at - 1]); };
+        // shares that start in a sequence of one or two tiles: a lane each
         const uint64_t u = nth < ctas ? share_start(units, ctas, nth) : ~uint64_t(0);
-        uint64_t from = 0;  // the units before the sequence or tile
-        uint32_t at = 0;
-        KvSeq o{0, 0, 0, true};
         if (u >= base && u < base + total) {
-            uint32_t last = kPlanThreads - 1;
+            uint32_t at = 0, last = kPlanThreads - 1;
             while (at < last) {
                 const uint32_t mid = (at + last) / 2;
                 if (s_upto[mid] > u - base)
@@ -187,39 +198,29 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
                 else
                     at = mid + 1;
             }
-            from = base + (at == 0 ? 0 : s_upto[at - 1]);
-            o = load_seq(a.b, b0 + at);
+            const KvSeq o = load_seq(a.b, b0 + at);
+            const int n = tile_count(a, o);
+            if (n <= 2) {
+                const uint64_t from = from_of(at), x = weight(o, 0);
+                const uint32_t tile = n == 2 && u >= from + x ? 1 : 0;
+                plan->start[nth] = ChunkStart{b0 + at, tile, from + tile * x};
+            }
         }
-        const int n = tile_count(a, o);
-        if (n > 0 && n <= 2) {
-            const uint64_t x = weight(o, 0);
-            const uint32_t tile = n == 2 && u >= from + x ? 1 : 0;
-            plan->start[nth] = ChunkStart{b0 + at, tile, from + tile * x};
-        }
-        // the warp finds the tile among more
-        uint32_t many = __ballot_sync(~0u, n > 2);
-        while (many) {
-            const int src = __ffs(many) - 1;
-            many &= many - 1;
-            const KvSeq p{0, __shfl_sync(~0u, o.t, src), __shfl_sync(~0u, o.n, src), true};
-            const uint64_t v = __shfl_sync(~0u, u, src);
-            const uint32_t b = b0 + __shfl_sync(~0u, at, src);
-            uint64_t f = __shfl_sync(~0u, from, src);
-            for (int i0 = 0, tiles = tile_count(a, p); i0 < tiles; i0 += 32) {
+        for_large(s, [&](const KvSeq& o, uint32_t at) {
+            uint64_t from = from_of(at);
+            for (int i0 = 0, tiles = tile_count(a, o); i0 < tiles; i0 += 32) {
                 const int i = i0 + int(lane);
-                const uint64_t x = i < tiles ? weight(p, i) : 0;
+                const uint64_t x = i < tiles ? weight(o, i) : 0;
                 uint64_t y = x;
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
                     const uint64_t z = __shfl_up_sync(~0u, y, d);
                     if (int(lane) >= d) y += z;
                 }
-                if (v >= f + y - x && v < f + y)
-                    plan->start[uint32_t(src) * kPlanWarps + warp] = ChunkStart{b, uint32_t(i), f + y - x};
-                f += __shfl_sync(~0u, y, 31);
-                if (v < f) break;
+                if (x > 0) starts(b0 + at, uint32_t(i), from + y - x, from + y);
+                from += __shfl_sync(~0u, y, 31);
             }
-        }
+        });
         base += total;
     }
     __syncthreads();
@@ -354,7 +355,7 @@ __device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh,
             g.b = b, g.head = head;
             g.first_cta = share_of(units, ctas, keys_start);
             g.last_cta = share_of(units, ctas, item_end - 1);
-            if (g.first_cta == blockIdx.x && g.last_cta != blockIdx.x)
+            if (g.first_cta == blockIdx.x && g.last_cta > g.first_cta)
                 splits[blockIdx.x] = ChunkSplit{g.row0, g.row_first, g.rows, head, g.last_cta};
         }
         if (i >= uint32_t(kSegments)) ok = mbar_wait(&sh.seg_empty[i % kSegments], (i / kSegments - 1) & 1u);
@@ -955,13 +956,9 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
                     log_sum<H>(m, l, scale);
             }
         };
-        const float inv = sum == 0.f ? 0.f : 1.f / (C::kValueScale * sum);
-        const bool live = int(row) + g * kTileRows < w.rows;
-        float* mine = part_at<D>(a, blockIdx.x, first, uint32_t(g)) + row;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
+        // 32 columns of the row's sums
+        const auto sums32 = [&](int k, float* o) {
             uint32_t bits[32];
-            float o[32];
             tmem_load32(bits, o_at + 32u * uint32_t(k));
             tmem_wait_load();
             tmem_loaded32(bits);
@@ -974,18 +971,32 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
                     if (reached.minus[k] >> y & 1u) o[y] += -INFINITY;
                 }
             }
-            if (whole) {
-                stage32(k, o, inv);
-            } else if (live) {
-#pragma unroll
-                for (int y = 0; y < 32; ++y) mine[(32 * k + y) * kTileRows] = o[y];
-            }
-        }
+        };
         if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / (C::kValueScale * sum);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                float o[32];
+                sums32(k, o);
+                stage32(k, o, inv);
+            }
             put(low, sum);
-        } else if (live) {
-            mine[D * kTileRows] = low;
-            mine[(D + 1) * kTileRows] = sum;
+        } else {
+            const bool live = int(row) + g * kTileRows < w.rows;
+            float* mine = part_at<D>(a, blockIdx.x, first, uint32_t(g)) + row;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                float o[32];
+                sums32(k, o);
+                if (live) {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) mine[(32 * k + y) * kTileRows] = o[y];
+                }
+            }
+            if (live) {
+                mine[D * kTileRows] = low;
+                mine[(D + 1) * kTileRows] = sum;
+            }
         }
         // the loads of O are done before the next piece's product overwrites it
         tc_fence_before();
@@ -1059,21 +1070,21 @@ __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
 }
 
 // Joins the parts of the item that CTA blockIdx.x of the kernel above began, if
-// others went on with it.  A CTA has 32 rows, a lane a row; four warps share
-// the columns and four of each take every fourth part, joined in that order.
+// others went on with it.  A CTA has 32 rows, a lane a row; eight warps share
+// the columns and two of each take every other part, joined in that order.
 // A kernel of its own, since the parts of a long context (for one sequence and
 // 8 kv heads 19 of up to 132 KB an item) are then read by many SMs, and not by
 // the one that wrote the last of them.
-constexpr int kJoinParts = 4, kJoinThreads = kJoinParts * 4 * 32;
+constexpr int kJoinParts = 2, kJoinColumns = 8, kJoinThreads = kJoinParts * kJoinColumns * 32;
 
 template <bool H, int D>
 __global__ void __launch_bounds__(kJoinThreads)
     kv_chunk_join_kernel(const __grid_constant__ AttentionArgs a, const ChunkSplit* splits, float value_scale) {
-    constexpr int kColumns = D / 4;
-    __shared__ float s_o[kJoinParts / 2][D][32], s_l[kJoinParts / 2][4][32];
+    constexpr int kColumns = D / kJoinColumns;
+    __shared__ float s_o[D][32], s_l[kJoinColumns][32];
     wait_predecessor();
     const uint32_t first = blockIdx.x, lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const int part0 = int(warp >> 2), col0 = int(warp & 3u) * kColumns;
+    const int part0 = int(warp / kJoinColumns), col0 = int(warp % kJoinColumns) * kColumns;
     const ChunkSplit w = splits[first];
     if (int(blockIdx.y) * 32 >= w.rows) return;
     const int row = int(blockIdx.y * 32u + lane);  // those past the last read what is there, and write nothing
@@ -1097,22 +1108,16 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
         for (int y = 0; y < kColumns; ++y) o[y] += f * x[y];
     }
+    if (part0 == 1) {
 #pragma unroll
-    for (int half = kJoinParts / 2; half > 0; half /= 2) {
-        if (part0 >= half && part0 < 2 * half) {
-#pragma unroll
-            for (int y = 0; y < kColumns; ++y) s_o[part0 - half][col0 + y][lane] = o[y];
-            s_l[part0 - half][warp & 3u][lane] = l;
-        }
-        __syncthreads();
-        if (part0 < half) {
-#pragma unroll
-            for (int y = 0; y < kColumns; ++y) o[y] += s_o[part0][col0 + y][lane];
-            l += s_l[part0][warp & 3u][lane];
-        }
-        __syncthreads();
+        for (int y = 0; y < kColumns; ++y) s_o[col0 + y][lane] = o[y];
+        s_l[warp % kJoinColumns][lane] = l;
     }
+    __syncthreads();
     if (part0 != 0 || row >= w.rows) return;
+#pragma unroll
+    for (int y = 0; y < kColumns; ++y) o[y] += s_o[col0 + y][lane];
+    l += s_l[warp][lane];
     const float inv = l == 0.f ? 0.f : 1.f / (value_scale * l);
     const int r = w.row_first + row, i = r / int(a.group);
     const uint32_t head = w.head * a.group + uint32_t(r - i * int(a.group));
