@@ -506,11 +506,11 @@ int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* cache, const
  * q, out: q_heads heads (a multiple of kv_heads, at most 64 times as many) of
  * `dtype` (BF16 or FP16; a 16-bit cache has to be of that type); out may be
  * q.  d_lse: float [tokens][q_heads] or null.  scale: finite.
- * Statistics and sums are held in 32 bits; for the product with V each exp() is
- * rounded to 16 bits, those of BF16 queries to BF16 at the least and those of
- * FP16 queries to FP16.  FP16 queries over an FP8 cache take values
- * of V beyond 131,008 as infinite where a sequence can have more than 64 rows
- * (max_tokens by the query heads of a group).
+ * Statistics and sums are held in 32 bits; each exp() is rounded for the
+ * product with V: to FP16 for FP16 queries, and for an FP8 cache where no
+ * sequence has more than 32 rows (max_tokens by the query heads of a group),
+ * else to BF16.  With more rows, FP16 queries over an FP8 cache take values of
+ * V beyond 131,008 as infinite.
  * d_ws: ws_bytes >= splitzip_kv_attention_workspace_size, 16-byte aligned,
  * contents need not be initialised; calls that share it must not overlap on
  * the GPU.  Results do not depend on the order in which blocks run. */

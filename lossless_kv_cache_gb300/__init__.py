@@ -6,7 +6,8 @@ pointers as Python ints, a CUDA stream handle as an int) and return the same
 status codes.  Every step of the codec runs in the CUDA kernels of
 ``libsplitzip.so``; this module only marshals arguments.  The torch helpers at
 the end (``calibrate``, ``encode``, ``decode``) allocate device memory with
-torch and call the same entry points.
+torch and call the same entry points.  ``kv_write``, ``kv_read`` and
+``kv_attention`` are the operators over the paged cache that the codec moves.
 
 Method: "SplitZip: Ultra Fast Lossless KV Compression for Disaggregated LLM
 Serving", section "Method: SplitZip".

@@ -13,8 +13,17 @@ uint64_t align256(uint64_t x) { return (x + 255u) & ~uint64_t(255); }
 
 // Rows of a sequence (new tokens by query heads of a group) up to which a step
 // takes the kernel of 16-row tiles, which is bound by the bytes of the cache,
-// rather than the tensor cores' 128-row tiles.
-constexpr uint64_t kStepRowsMax = 64;
+// rather than the tensor cores' 128-row tiles.  It reads the keys again for
+// each tile, so its time grows with the rows where the other's does not.  In us
+// for 8 kv heads of 128 and pages of 16, the first kernel by 16 / 32 / 64 rows,
+// then the second at any of them:
+//   BF16, 1 sequence of 16,384    27 / 30 / 46     34
+//   BF16, 8 of 4,096              38 / 48 / 76     51
+//   BF16, 32 of 2,048             57 / 97 / 170    91
+//   E5M2, 1 of 16,384             33 / 36 / 48     40
+//   E5M2, 8 of 4,096              34 / 49 / 80     70
+//   E5M2, 32 of 2,048             55 / 88 / 156    130
+constexpr uint64_t kStepRowsMax = 32;
 
 struct Plan {
     uint32_t group, ctas;
