@@ -34,7 +34,7 @@
 // One GB300, 32 query heads of 128 over 8: 2,048 new tokens over 32,768 of BF16
 // in 835 us (1.28 PFLOP/s, 67 % of the measured library product), a prompt of
 // 8,192 tokens of FP16 in 449 us (1.22 PFLOP/s, 64 %), six chunks of up to 777
-// over up to 5,000 of E4M3 in 136 us (0.5 PFLOP/s).  A unit of 256 rows by 128
+// over up to 5,000 of E4M3 in 138 us (0.5 PFLOP/s).  A unit of 256 rows by 128
 // keys takes about 3,500 cycles of which the products are 2,048: a tile's next
 // scores wait for its weights (its softmax takes 1,600 and its two hand-overs
 // 650), and what K and V cost of the shared memory's bandwidth slows the
@@ -309,7 +309,8 @@ struct Chunk {
         uint8_t raw[kRaw > 0 ? kRaw : 1][kRaw > 0 ? kRawBytes : 16];
         // of a unit's keys: byte offset in the pools, or page (FP8, which has no room); -1: none
         std::conditional_t<kFp8, int32_t, int64_t> place[2][kTma ? 1 : kUnit];
-        uint8_t k_scale[4][kFp8 ? kUnit : 4], v_scale[4][kFp8 ? kUnit : 4];
+        alignas(16) uint16_t k_factor[4][kScoreScale ? kUnit : 8];  // K's scales in BF16, for the scores
+        uint8_t k_scale[4][kFp8 && !kScoreScale ? kUnit : 4], v_scale[4][kFp8 ? kUnit : 4];
         uint64_t kv_full[kStages];
         uint64_t freed[kDepth];          // K of unit u and V of unit u - 1 are no longer read
         uint64_t q_full[2], s_full[2], p_full[2], o_full[2], noted, drained;
@@ -411,7 +412,8 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
         if (C::kFp8) {
             await_empty(x);
             const bool is_v = x & 1u;
-            const uint8_t* scales = (is_v ? sh.v_scale : sh.k_scale)[(x >> 1) & 3u];
+            const uint32_t ring = (x >> 1) & 3u;
+            const uint8_t* scales = is_v || C::kScoreScale ? sh.v_scale[ring] : sh.k_scale[ring];
             if (ok) {
 #pragma unroll
                 for (int i0 = 0; i0 < C::kChunks; i0 += 4) {
@@ -482,7 +484,20 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
             return pg;
         };
         const uint32_t slots = (1u << a.c.page_shift) - 1u;
-        int32_t page = page_of(0);
+        // A unit's pages are looked up two units before it, its scales one, so that neither is
+        // waited for (2,048 tokens over 8,192 of E4M3: 277 -> 261 us).
+        const auto scales_at = [&](int j, int32_t pg, uint32_t& k, uint32_t& v) {
+            k = v = 127;
+            if (C::kFp8 && pg >= 0) {
+                const uint32_t slot = (uint32_t(w.first_unit + j) * kUnit + lt) & slots;
+                const uint64_t at = ((uint64_t(uint32_t(pg)) * a.c.kv_heads + w.head) << a.c.page_shift) + slot;
+                k = __ldg(a.c.k_scale + at);
+                v = __ldg(a.c.v_scale + at);
+            }
+        };
+        int32_t page = page_of(0), next_page = page_of(1);
+        uint32_t k_scale, v_scale;
+        scales_at(0, page, k_scale, v_scale);
         for (int j = 0; j < w.n; ++j) {
             const uint32_t unit = made >> 1;  // of the share
             const int pos0 = (w.first_unit + j) * kUnit;
@@ -494,13 +509,16 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
                                                                  uint64_t(slot) * a.c.token_stride);
                 } else {
                     sh.place[unit & 1u][lt] = page;
-                    const uint64_t at =
-                        ((uint64_t(uint32_t(page)) * a.c.kv_heads + w.head) << a.c.page_shift) + slot;
-                    sh.k_scale[unit & 3u][lt] = page < 0 ? 127 : a.c.k_scale[at];
-                    sh.v_scale[unit & 3u][lt] = page < 0 ? 127 : a.c.v_scale[at];
+                    if (C::kScoreScale)
+                        sh.k_factor[unit & 3u][lt] = uint16_t(k_scale << 7);
+                    else
+                        sh.k_scale[unit & 3u][lt] = uint8_t(k_scale);
+                    sh.v_scale[unit & 3u][lt] = uint8_t(v_scale);
                 }
             }
-            page = page_of(j + 1);
+            page = next_page;
+            next_page = page_of(j + 2);
+            scales_at(j + 1, page, k_scale, v_scale);
             named_barrier(1, 128);
 #pragma unroll
             for (int side = 0; side < 2; ++side) {
@@ -831,9 +849,19 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
 #pragma unroll
             for (int k = 0; k < 4; ++k) tmem_loaded32(x + 32 * k);
             if (C::kScoreScale) {
-                const uint8_t* ks = sh.k_scale[((first_tile >> 1) + uint32_t(j)) & 3u];
+                const uint4* ks = reinterpret_cast<const uint4*>(sh.k_factor[((first_tile >> 1) + uint32_t(j)) & 3u]);
 #pragma unroll
-                for (int k = 0; k < 128; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * scale_value(ks[k]));
+                for (int k = 0; k < 16; ++k) {
+                    const uint4 f8 = ks[k];
+                    const uint32_t f[4] = {f8.x, f8.y, f8.z, f8.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int at = 8 * k + 2 * y;
+                        const float2 z = mul2(make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1])),
+                                              bf16x2_to_float2(f[y]));
+                        x[at] = __float_as_uint(z.x), x[at + 1] = __float_as_uint(z.y);
+                    }
+                }
             }
             const int from = see.lo - pos0, to = see.hi - pos0;
             if (!__all_sync(~0u, from <= 0 && to >= kUnit)) {
