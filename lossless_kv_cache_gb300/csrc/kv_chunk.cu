@@ -302,6 +302,12 @@ struct Chunk {
     static constexpr int kRawBytes = 128 * D;
     static constexpr int kChunks = kFp8 ? D / 16 : D / 8;  // 16-byte pieces of a cache row
     static constexpr int kRowStep = 128 / kChunks;         // rows that the loaders copy at a time
+    // Slots of the scores' factors, a unit each.  Nothing but the stages holds the
+    // loaders back: unit u is described when K of unit u - 1 has a stage, so when the
+    // scores of unit u - 1 - kDepth are done, and the softmax may still be about to
+    // read the factors of that unit and of all after it.
+    static constexpr uint32_t kFactors = kDepth > 2 ? 8 : 4;
+    static_assert(kFactors >= kDepth + 2, "factors of units in flight");
 
     struct Shared {
         uint8_t q[2][kTileBytes];
@@ -309,7 +315,7 @@ struct Chunk {
         uint8_t raw[kRaw > 0 ? kRaw : 1][kRaw > 0 ? kRawBytes : 16];
         // of a unit's keys: byte offset in the pools, or page (FP8, which has no room); -1: none
         std::conditional_t<kFp8, int32_t, int64_t> place[2][kTma ? 1 : kUnit];
-        alignas(16) uint16_t k_factor[4][kScoreScale ? kUnit : 8];  // K's scales in BF16, for the scores
+        alignas(16) uint16_t k_factor[kScoreScale ? kFactors : 1][kScoreScale ? kUnit : 8];  // K's scales in BF16, for the scores
         uint8_t k_scale[4][kFp8 && !kScoreScale ? kUnit : 4], v_scale[4][kFp8 ? kUnit : 4];
         uint64_t kv_full[kStages];
         uint64_t freed[kDepth];          // K of unit u and V of unit u - 1 are no longer read
@@ -510,7 +516,7 @@ __device__ __forceinline__ void load_role(const AttentionArgs& a, typename Chunk
                 } else {
                     sh.place[unit & 1u][lt] = page;
                     if (C::kScoreScale)
-                        sh.k_factor[unit & 3u][lt] = uint16_t(k_scale << 7);
+                        sh.k_factor[unit % C::kFactors][lt] = uint16_t(k_scale << 7);
                     else
                         sh.k_scale[unit & 3u][lt] = uint8_t(k_scale);
                     sh.v_scale[unit & 3u][lt] = uint8_t(v_scale);
@@ -849,7 +855,7 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
 #pragma unroll
             for (int k = 0; k < 4; ++k) tmem_loaded32(x + 32 * k);
             if (C::kScoreScale) {
-                const uint4* ks = reinterpret_cast<const uint4*>(sh.k_factor[((first_tile >> 1) + uint32_t(j)) & 3u]);
+                const uint4* ks = reinterpret_cast<const uint4*>(sh.k_factor[((first_tile >> 1) + uint32_t(j)) % C::kFactors]);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const uint4 f8 = ks[k];
