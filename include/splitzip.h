@@ -509,8 +509,12 @@ int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* cache, const
  * Statistics and sums are held in 32 bits; each exp() is rounded for the
  * product with V: to FP16 for FP16 queries, and for an FP8 cache where no
  * sequence has more than 32 rows (max_tokens by the query heads of a group),
- * else to BF16.  With more rows, FP16 queries over an FP8 cache take values of
- * V beyond 131,008 as infinite.
+ * else to BF16.  Over an FP8 cache with up to 32 rows these are weights by
+ * V's scales, and keep all bits down to 2^-28 of a row's largest such product
+ * (rows of zeros aside), with scales under 2^-80 counted as 2^-80: V rows
+ * smaller than that (elements below 1e-20) lose bits, and vanish from 2^-119
+ * on.  With more rows, FP16 queries over an FP8 cache take values of V beyond
+ * 131,008 as infinite.
  * d_ws: ws_bytes >= splitzip_kv_attention_workspace_size, 16-byte aligned,
  * contents need not be initialised; calls that share it must not overlap on
  * the GPU.  Results do not depend on the order in which blocks run. */

@@ -8,7 +8,9 @@
 // FP8 values are exact in FP16 and are multiplied there without their scales:
 // K's go to the scores, V's, 2^e, to the weights, and m is the maximum of s + e,
 // so that the weights 2^(s+e-m) are at most 1 whatever the scales' range
-// (l sums 2^(s-m), and the difference cancels in o / l).  BF16 queries get a
+// (l sums 2^(s-m), and the difference cancels in o / l).  That takes e for the
+// size of the row, which it is as splitzip_kv_write stores it but for a row of
+// zeros: those are looked for where they would raise m.  BF16 queries get a
 // power of two for each row that brings them into FP16's range.
 //
 // What bounds it: HBM.  A tile of 16 rows does 64 operations a byte of a BF16
@@ -504,11 +506,8 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                 vs[0] = fminf(vs[0], 1.7014118e38f);
                 vs[1] = fminf(vs[1], 1.7014118e38f);
             }
-            float top[S::kRowsLane];
-            bool grew = false;
 #pragma unroll
-            for (int r = 0; r < S::kRowsLane; ++r) {
-                top[r] = -INFINITY;
+            for (int r = 0; r < S::kRowsLane; ++r)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     float y = sc[r >> 1][2 * x + (r & 1)] * row_scale[r];
@@ -518,13 +517,50 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
                         y = pos >= see[r].lo && pos < see[r].hi ? y : -INFINITY;
                     }
                     sc[r >> 1][2 * x + (r & 1)] = y;
-                    top[r] = fmaxf(top[r], S::kFp8 ? y + ve[x] : y);
                 }
+            float top[S::kRowsLane];
+            // the rows' largest of the stage; whether some row's maximum grows
+            const auto find_top = [&]() -> bool {
+                bool grew = false;
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], d));
-                grew |= top[r] > m[r];
+                for (int r = 0; r < S::kRowsLane; ++r) {
+                    top[r] = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float y = sc[r >> 1][2 * x + (r & 1)];
+                        top[r] = fmaxf(top[r], S::kFp8 ? y + ve[x] : y);
+                    }
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], d));
+                    grew |= top[r] > m[r];
+                }
+                return __any_sync(~0u, grew);
+            };
+            bool grew = find_top();
+            if (S::kFp8 && grew && __any_sync(~0u, vs[0] == 1.f || vs[1] == 1.f)) {
+                // A row of zeros has the scale 2^0, which says nothing of its size: against a
+                // maximum with that exponent the weights of rows of small scale, all of the
+                // result, would lose bits or vanish.  It takes the least exponent instead, and
+                // as its weight is then beyond FP16, the weight 0.
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint4 w =
+                            *reinterpret_cast<const uint4*>(v_stage + S::place_v(uint32_t(g + 8 * x), uint32_t(c * 4 + t4)));
+                        any |= w.x | w.y | w.z | w.w;
+                    }
+                    any |= __shfl_xor_sync(~0u, any, 1);
+                    any |= __shfl_xor_sync(~0u, any, 2);
+                    if ((any & 0x7F7F7F7Fu) == 0) {
+                        ve[x] = -80.f;
+                        vs[x] = 0.f;
+                    }
+                }
+                grew = find_top();
             }
-            if (__any_sync(~0u, grew)) {
+            if (grew) {
                 float f[S::kRowsLane];
 #pragma unroll
                 for (int r = 0; r < S::kRowsLane; ++r) {
