@@ -31,10 +31,11 @@ struct Plan {
     uint64_t plan_off, parts_off, ws_bytes;
 };
 
-void size_of(Plan* p, uint64_t plan_bytes, uint64_t counters, uint64_t part_floats) {
+// Places the parts of the workspace; returns its size.
+uint64_t lay_out(Plan* p, uint64_t plan_bytes, uint64_t counters, uint64_t part_floats) {
     p->plan_off = align256(4ull * counters);
     p->parts_off = align256(p->plan_off + plan_bytes);
-    p->ws_bytes = align256(p->parts_off + 4ull * 2 * p->ctas * part_floats);
+    return align256(p->parts_off + 4ull * 2 * p->ctas * part_floats);
 }
 
 int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, Plan* p) {
@@ -43,14 +44,15 @@ int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, Plan* p) {
     if (p->group > 64) return SPLITZIP_ERR_UNSUPPORTED;
     const uint64_t rows = uint64_t(b.tokens) * p->group;
     p->chunk = uint64_t(b.max_tokens) * p->group > kStepRowsMax;
+    // tiles of rows over all sequences: each has a partial one at most
+    const uint64_t tiles = std::min<uint64_t>((rows + 7) / 8 + b.batch, rows);
+    p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);
+    p->ws_bytes = lay_out(p, 0, p->ctas, step_part_floats(c.head_dim));
     if (p->chunk) {
+        // a step of the same rows, but fewer of a sequence, takes the other kernel:
+        // the size is enough for both
         p->ctas = chunk_ctas(rows, b.batch, c.kv_heads, b.max_kv_len);
-        size_of(p, chunk_plan_bytes(p->ctas), 0, chunk_part_floats(c.head_dim));
-    } else {
-        // tiles of rows over all sequences: each has a partial one at most
-        const uint64_t tiles = std::min<uint64_t>((rows + 7) / 8 + b.batch, rows);
-        p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);
-        size_of(p, 0, p->ctas, step_part_floats(c.head_dim));
+        p->ws_bytes = std::max(p->ws_bytes, lay_out(p, chunk_plan_bytes(p->ctas), 0, chunk_part_floats(c.head_dim)));
     }
     return SPLITZIP_OK;
 }

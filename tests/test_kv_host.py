@@ -138,3 +138,24 @@ def test_helpers_refuse_wrong_tensors(splitzip_lib):
     i32 = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(ValueError):
         sz.KVBatch(i32, i32[:2], i32[None, :2], 1, 1, 1)      # not on a GPU
+
+
+def test_workspace_covers_steps_of_fewer_new_tokens_with_rows_to_spare(splitzip_lib):
+    """The same packed rows, but fewer new tokens of a sequence at most: such a step takes the
+    kernel for few rows, whatever the kernel of the larger one."""
+    cache = desc(sz.KVCacheDesc, CACHE, dict(kv_heads=1, token_stride=128, page_stride=16 * 128))
+
+    def size(heads, **kw):
+        out = ctypes.c_uint64(0)
+        b = desc(sz.KVBatchDesc, BATCH, dict(table_stride=1 << 20, **kw))
+        assert sz.splitzip_kv_attention_workspace_size(cache, b, heads, out) == sz.OK
+        return out.value
+
+    for heads in (1, 4, 8, 33):
+        for tokens in (2, 33, 121, 500, 4000):
+            for batch in (1, 7, 64):
+                for kv in (0, 1, 490, 20000, 1 << 20):
+                    sizes = dict(tokens=tokens, batch=batch, max_kv_len=kv)
+                    most = size(heads, max_tokens=tokens, **sizes)
+                    for t in (0, 1, 2, 3, 8, 9, 32, 33):
+                        assert size(heads, max_tokens=min(t, tokens), **sizes) <= most, (heads, sizes, t)
