@@ -110,7 +110,8 @@ extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const spl
     if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
     if (p.chunk && a.b.tokens > 0)
         return launch_kv_chunk(a, a.q_half != 0, static_cast<uint8_t*>(d_ws) + p.plan_off, p.ctas, stream);
-    if (launch_kv_begin(d_status, a.counters, p.ctas, stream) != cudaSuccess) {
+    // the step kernel looks at all sequences itself, to share out their units
+    if (launch_kv_begin(a.b.tokens > 0 ? KvBatch{} : a.b, d_status, a.counters, p.ctas, stream) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }

@@ -150,9 +150,11 @@ int check_rows(const splitzip_kv_rows_t* r, const KvBatch& b, uint32_t heads, ui
 // Whether rows of `dtype` go with a cache of `type`.
 bool kv_dtype_fits(int type, int dtype);
 
-// Clears the status word and `words` 32-bit words of a workspace, as the
-// predecessor that the operators' kernels are chained to.
-cudaError_t launch_kv_begin(int* status, uint32_t* words, uint32_t count, cudaStream_t s);
+// Sets the status word, by the entries of all sequences (also of those that no
+// packed row belongs to, which the kernels after it never look at), and clears
+// `count` 32-bit words of a workspace, as the predecessor that the operators'
+// kernels are chained to.
+cudaError_t launch_kv_begin(const KvBatch& b, int* status, uint32_t* words, uint32_t count, cudaStream_t s);
 
 // Launch configuration of a kernel chained to its predecessor.
 struct ChainedLaunch {

@@ -25,10 +25,19 @@ namespace {
 
 constexpr int kRwWarps = 4;
 
-__global__ void kv_begin_kernel(int* status, uint32_t* words, uint32_t count) {
+constexpr int kBeginThreads = 1024;
+
+// Runs beside its successor, which waits for it before its own reports (64 tokens
+// are written in 3.08 us, 2.91 if nothing is looked at here; 128 threads: the same).
+__global__ void __launch_bounds__(kBeginThreads)
+    kv_begin_kernel(const __grid_constant__ KvBatch batch, int* status, uint32_t* words, uint32_t count) {
     release_successor();
-    if (threadIdx.x == 0) *status = SPLITZIP_OK;
-    for (uint32_t i = threadIdx.x; i < count; i += blockDim.x) words[i] = 0;
+    for (uint32_t i = threadIdx.x; i < count; i += kBeginThreads) words[i] = 0;
+    bool bad = false;
+#pragma unroll 4
+    for (uint32_t b = threadIdx.x; b < batch.batch; b += kBeginThreads) bad |= !load_seq(batch, b).ok;
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *status = bad ? SPLITZIP_ERR_INVALID_ARG : SPLITZIP_OK;
 }
 
 // The last sequence b with cu[b] <= row, 32 candidates a step; every lane gets
@@ -250,7 +259,7 @@ int kv_rw_call(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batc
     a.status = d_status;
     int sms;
     if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
-    cudaError_t e = launch_kv_begin(d_status, nullptr, 0, stream);
+    cudaError_t e = launch_kv_begin(a.b, d_status, nullptr, 0, stream);
     if (e == cudaSuccess && a.b.tokens > 0) {
         const bool h = dtype == SPLITZIP_FP16;
         if (a.c.type == SPLITZIP_KV_FP8_E5M2)
@@ -268,8 +277,8 @@ bool multiple_of(uint64_t x, uint64_t m) { return x % m == 0; }
 
 }  // namespace
 
-cudaError_t launch_kv_begin(int* status, uint32_t* words, uint32_t count, cudaStream_t s) {
-    kv_begin_kernel<<<1, 256, 0, s>>>(status, words, count);
+cudaError_t launch_kv_begin(const KvBatch& b, int* status, uint32_t* words, uint32_t count, cudaStream_t s) {
+    kv_begin_kernel<<<1, kBeginThreads, 0, s>>>(b, status, words, count);
     return cudaGetLastError();
 }
 

@@ -1,0 +1,74 @@
+"""GPU: steps whose integer arrays are wrong.  Every call reports them, also
+where no packed row belongs to the sequence."""
+import pytest
+import torch
+
+import lossless_kv_cache_gb300 as sz
+from tests.kv_reference import Step
+
+pytestmark = pytest.mark.gpu
+
+BF16, E5M2 = torch.bfloat16, torch.float8_e5m2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(splitzip_lib):
+    assert torch.cuda.is_available()
+    return splitzip_lib
+
+
+def write(step):
+    x = step.new_rows().cuda()
+    sz.kv_write(step.cache, step.batch, x, x, step.status)
+    return int(step.status[0])
+
+
+def read(step):
+    x = step.new_rows().cuda()
+    sz.kv_read(step.cache, step.batch, x, x.clone(), step.status)
+    return int(step.status[0])
+
+
+def attend(step):
+    q = torch.randn(step.tokens, 8, step.dim, generator=step.gen).to(step.x).cuda()
+    bufs = sz.KVAttentionBuffers(step.cache, step.batch, 8)
+    sz.kv_attention(step.cache, step.batch, q, torch.empty_like(q), bufs, 0.1)
+    return int(bufs.status[0])
+
+
+CALLS = pytest.mark.parametrize("call", [write, read, attend])
+
+
+@CALLS
+@pytest.mark.parametrize("lens", [[(3, 40), (0, 20), (2, 9)], [(40, 40), (0, 20), (2, 9)], [(0, 40), (0, 20)]])
+@pytest.mark.parametrize("bad", [-1, 41, 1 << 29, -(1 << 31)])
+def test_a_bad_length_without_new_tokens_is_reported(call, lens, bad):
+    for dtype in (BF16, E5M2):
+        step = Step(dtype, lens)
+        assert call(step) == sz.OK
+        step.batch.kv_len[1] = bad
+        assert call(step) == sz.ERR_INVALID_ARG
+        step.batch.kv_len[1] = 20
+        assert call(step) == sz.OK
+
+
+@CALLS
+def test_a_bad_length_far_into_a_large_batch_is_reported(call):
+    lens = [(1 if b % 7 == 0 else 0, 5 + b % 11) for b in range(3000)]
+    step = Step(BF16, lens, kv_heads=1, dim=64)
+    assert call(step) == sz.OK
+    for b in (1, 1025, 2999):
+        step.batch.kv_len[b] = 16
+        assert call(step) == sz.ERR_INVALID_ARG
+        step.batch.kv_len[b] = lens[b][1]
+    assert call(step) == sz.OK
+
+
+@CALLS
+@pytest.mark.parametrize("cu", [[0, 5, 8, 3, 9], [0, 5, 3, 8, 9], [0, 9, 9, 9, 8], [0, 3, 6, 10, 9], [4, 2, 9, 9, 9]])
+def test_offsets_that_descend_are_reported(call, cu):
+    step = Step(BF16, [(3, 40), (2, 30), (2, 20), (2, 10)])
+    step.batch.desc.max_tokens = 9
+    assert call(step) == sz.OK
+    step.batch.cu_tokens.copy_(torch.tensor(cu, dtype=torch.int32))
+    assert call(step) == sz.ERR_INVALID_ARG
