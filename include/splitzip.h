@@ -417,7 +417,9 @@ int splitzip_merge(const void* const* h_parts, const uint64_t* part_bytes, uint3
  * than max_tokens new tokens, kv_len outside 0 .. max_kv_len) is left out, a
  * page outside [0, pool_pages) is neither read nor written, and both are
  * reported in *d_status as SPLITZIP_ERR_INVALID_ARG (the outputs of that
- * sequence are then unspecified).  *d_status is cleared by each call.
+ * sequence are then unspecified, and where cu_tokens descends those of any
+ * sequence; writes go to new positions of a sequence all the same, or
+ * nowhere).  *d_status is cleared by each call.
  */
 typedef enum {
     SPLITZIP_KV_BF16 = 0,

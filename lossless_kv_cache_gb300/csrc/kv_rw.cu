@@ -41,7 +41,8 @@ __global__ void __launch_bounds__(kBeginThreads)
 }
 
 // The last sequence b with cu[b] <= row, 32 candidates a step; every lane gets
-// the same answer (-1: none).
+// the same answer (-1: none).  Where cu descends it may be one that row is not
+// of, on either side.
 __device__ __forceinline__ int find_seq(const KvBatch& B, int row, uint32_t lane) {
     int lo = 0, n = int(B.batch);
     while (true) {
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_const
         uint32_t slot = 0;
         if (mine) {
             const int c1 = a.b.cu[b + 1];
-            mine = int(token) < c1;
+            mine = a.b.cu[b] <= int(token) && int(token) < c1;
             if (mine) {
                 const KvSeq s = load_seq(a.b, uint32_t(b));
                 bad = !s.ok;

@@ -1,10 +1,11 @@
 """GPU: steps whose integer arrays are wrong.  Every call reports them, also
-where no packed row belongs to the sequence."""
+where no packed row belongs to the sequence, and nothing is written but to new
+positions of sequences whose own entries are in range."""
 import pytest
 import torch
 
 import lossless_kv_cache_gb300 as sz
-from tests.kv_reference import Step
+from tests.kv_reference import RAW, Step
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,27 @@ def test_offsets_that_descend_are_reported(call, cu):
     assert call(step) == sz.OK
     step.batch.cu_tokens.copy_(torch.tensor(cu, dtype=torch.int32))
     assert call(step) == sz.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("cu", [[0, 5, 8, 3, 9], [0, 5, 3, 8, 9], [0, 9, 9, 9, 8], [4, 2, 9, 9, 9], [0, 6, 7, 2, 9]])
+def test_offsets_that_descend_write_to_new_positions_only(dtype, cu):
+    """Rows between descending offsets are in no sequence or in several: they go to a
+    place that one of these has for them, or nowhere."""
+    lens = [(3, 40), (2, 30), (2, 20), (2, 10)]
+    step = Step(dtype, lens)
+    step.batch.desc.max_tokens = 9
+    step.batch.cu_tokens.copy_(torch.tensor(cu, dtype=torch.int32))
+    before = {n: getattr(step.cache, n).view(RAW[dtype]).cpu().clone() for n in "kv"}
+    scales = {n: getattr(step.cache, n + "_scale").cpu().clone() for n in "kv"} if step.fp8 else {}
+    allowed = torch.zeros(step.pages, step.page, dtype=torch.bool)
+    for b, (_, n) in enumerate(lens):
+        for pos in range(max(0, n - max(0, cu[b + 1] - cu[b])), n):
+            allowed[step.place(b, pos)] = True
+    assert write(step) == sz.ERR_INVALID_ARG
+    for n in "kv":
+        changed = (getattr(step.cache, n).view(RAW[dtype]).cpu() != before[n]).flatten(2).any(-1)
+        assert not bool((changed & ~allowed).any())
+        if step.fp8:
+            changed = (getattr(step.cache, n + "_scale").cpu() != scales[n]).any(1)
+            assert not bool((changed & ~allowed).any())
