@@ -631,10 +631,13 @@ def _kv_type_of(t):
     return types[t.dtype]
 
 
-def _device_tensor(t, dtype, shape, what):
+def _device_tensor(t, dtype, shape, what, device=None):
+    """device: the index of the device that t has to be on (None: any)."""
     if not t.is_cuda or t.dtype != dtype or t.shape != tuple(shape):
         raise ValueError("%s: expected a CUDA tensor of %s and shape %s, got %s %s on %s"
                          % (what, dtype, tuple(shape), t.dtype, tuple(t.shape), t.device))
+    if device is not None and t.get_device() != device:
+        raise ValueError("%s: expected a tensor on cuda:%d, got one on %s" % (what, device, t.device))
     return t
 
 
@@ -654,7 +657,8 @@ class KVCache:
             raise ValueError("k: expected (pages, page_tokens, kv_heads, head_dim), got %s" % (tuple(k.shape),))
         pages, page_tokens, heads, dim = k.shape
         _device_tensor(k, k.dtype, k.shape, "k")
-        _device_tensor(v, k.dtype, k.shape, "v")
+        self.device = k.get_device()
+        _device_tensor(v, k.dtype, k.shape, "v", self.device)
         if k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("k and v: expected the same strides and a contiguous last axis, got %s and %s"
                              % (k.stride(), v.stride()))
@@ -662,7 +666,7 @@ class KVCache:
             for s, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
                 if s is None or not s.is_contiguous():
                     raise ValueError("%s: an FP8 cache needs a contiguous scale tensor" % what)
-                _device_tensor(s, torch.uint8, (pages, heads, page_tokens), what)
+                _device_tensor(s, torch.uint8, (pages, heads, page_tokens), what, self.device)
         self.k, self.v = k, v
         self.page_tokens, self.kv_heads, self.head_dim = page_tokens, heads, dim
         self.k_scale, self.v_scale = (k_scale, v_scale) if fp8 else (None, None)
@@ -694,10 +698,11 @@ class KVBatch:
         torch = _torch()
         batch = kv_len.numel()
         _device_tensor(cu_tokens, torch.int32, (batch + 1,), "cu_tokens")
-        _device_tensor(kv_len, torch.int32, (batch,), "kv_len")
+        self.device = cu_tokens.get_device()
+        _device_tensor(kv_len, torch.int32, (batch,), "kv_len", self.device)
         if page_table.dim() != 2 or page_table.stride(1) != 1:
             raise ValueError("page_table: expected (batch, pages) with a contiguous last axis")
-        _device_tensor(page_table, torch.int32, (batch, page_table.shape[1]), "page_table")
+        _device_tensor(page_table, torch.int32, (batch, page_table.shape[1]), "page_table", self.device)
         if not (cu_tokens.is_contiguous() and kv_len.is_contiguous()):
             raise ValueError("cu_tokens and kv_len: expected contiguous tensors")
         # a row's entries end where the table does, whatever the stride between rows
@@ -708,7 +713,10 @@ class KVBatch:
                                 batch, tokens, max_tokens, max_kv_len)
 
     def check(self, cache):
-        """Raises where the page table is narrower than max_kv_len tokens need."""
+        """Raises where the step is on another device than the cache, and where the page
+        table is narrower than max_kv_len tokens need."""
+        if self.device != cache.device:
+            raise ValueError("cache on cuda:%d and step on cuda:%d: expected one device" % (cache.device, self.device))
         if self.table_pages * cache.page_tokens < self.max_kv_len:
             raise SplitZipError(ERR_INVALID_ARG, "page_table of %d pages for %d tokens"
                                 % (self.table_pages, self.max_kv_len))
@@ -717,7 +725,17 @@ class KVBatch:
 _ROW_TYPES = {}
 
 
-def _kv_rows(t, tokens, heads, dim, what):
+def _kv_stream(stream, device):
+    """Handle of a stream of `device`, which has to be the current device."""
+    c = _torch()._C
+    current = c._cuda_getDevice()
+    if current != device or (stream is not None and stream.device.index != device):
+        raise ValueError("tensors on cuda:%d: expected it to be the current device (cuda:%d) and the stream's (%s)"
+                         % (device, current, "cuda:%d" % current if stream is None else stream.device))
+    return c._cuda_getCurrentRawStream(current) if stream is None else stream.cuda_stream
+
+
+def _kv_rows(t, tokens, heads, dim, device, what):
     """(KVRowsDesc, dtype constant) of a packed (tokens, heads, head_dim) tensor."""
     if not _ROW_TYPES:
         torch = _torch()
@@ -725,21 +743,29 @@ def _kv_rows(t, tokens, heads, dim, what):
     dtype = _ROW_TYPES.get(t.dtype)
     if dtype is None:
         raise TypeError("%s: expected bfloat16 or float16, got %s" % (what, t.dtype))
-    if not t.is_cuda or t.shape != (tokens, heads, dim) or t.stride(2) != 1:
-        raise ValueError("%s: expected a CUDA tensor (%d, %d, %d) with a contiguous last axis, got %s of strides %s on %s"
-                         % (what, tokens, heads, dim, tuple(t.shape), t.stride(), t.device))
-    token_stride, head_stride, _ = t.stride()
-    return KVRowsDesc(t.data_ptr(), token_stride, head_stride), dtype
+    strides = t.stride()
+    if t.get_device() != device or t.shape != (tokens, heads, dim) or strides[2] != 1:
+        raise ValueError("%s: expected a tensor (%d, %d, %d) on cuda:%d with a contiguous last axis, got %s of strides "
+                         "%s on %s" % (what, tokens, heads, dim, device, tuple(t.shape), strides, t.device))
+    return KVRowsDesc(t.data_ptr(), strides[0], strides[1]), dtype
+
+
+def _kv_status(t, device):
+    """Address of a status word; the kernels write to it."""
+    if t.get_device() != device or t.dtype != _torch().int32 or t.numel() < 1:
+        raise ValueError("status: expected an int32 tensor on cuda:%d, got %s %s on %s"
+                         % (device, t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr()
 
 
 def _kv_rw(call, cache, batch, k, v, status, stream):
-    d, heads, dim = cache.desc, cache.kv_heads, cache.head_dim
+    d, heads, dim, device = cache.desc, cache.kv_heads, cache.head_dim, cache.device
     batch.check(cache)
-    rk, dtype = _kv_rows(k, batch.tokens, heads, dim, "k")
-    rv, dtype_v = _kv_rows(v, batch.tokens, heads, dim, "v")
+    rk, dtype = _kv_rows(k, batch.tokens, heads, dim, device, "k")
+    rv, dtype_v = _kv_rows(v, batch.tokens, heads, dim, device, "v")
     if dtype != dtype_v:
         raise TypeError("k and v: expected the same type")
-    _check(call(d, batch.desc, rk, rv, dtype, status.data_ptr(), _stream_handle(stream)), call.__name__)
+    _check(call(d, batch.desc, rk, rv, dtype, _kv_status(status, device), _kv_stream(stream, device)), call.__name__)
 
 
 def kv_write(cache, batch, k, v, status, stream=None):
@@ -769,7 +795,7 @@ class KVAttentionBuffers:
     def __init__(self, cache, batch, q_heads):
         torch = _torch()
         device = batch.kv_len.device
-        self.q_heads = q_heads
+        self.q_heads, self.device = q_heads, batch.device
         self.ws_bytes = kv_attention_workspace_size(cache, batch, q_heads)
         self.ws = torch.empty(max(self.ws_bytes, 16), dtype=torch.uint8, device=device)
         self.status = torch.zeros(4, dtype=torch.int32, device=device)  # [0] = status
@@ -780,15 +806,18 @@ def kv_attention(cache, batch, q, out, bufs, scale, causal=True, window=0, lse=N
     (asynchronous).  q, out: packed (tokens, q_heads, head_dim); lse: None or
     float32 (tokens, q_heads); bufs: KVAttentionBuffers."""
     batch.check(cache)
-    rq, dtype = _kv_rows(q, batch.tokens, bufs.q_heads, cache.head_dim, "q")
-    ro, dtype_o = _kv_rows(out, batch.tokens, bufs.q_heads, cache.head_dim, "out")
+    device = cache.device
+    if bufs.device != device:
+        raise ValueError("bufs: expected buffers on cuda:%d, got cuda:%d" % (device, bufs.device))
+    rq, dtype = _kv_rows(q, batch.tokens, bufs.q_heads, cache.head_dim, device, "q")
+    ro, dtype_o = _kv_rows(out, batch.tokens, bufs.q_heads, cache.head_dim, device, "out")
     if dtype != dtype_o:
         raise TypeError("q and out: expected the same type")
     if lse is not None:
         if not lse.is_contiguous():
             raise ValueError("lse: expected a contiguous tensor")
-        _device_tensor(lse, _torch().float32, (batch.tokens, bufs.q_heads), "lse")
+        _device_tensor(lse, _torch().float32, (batch.tokens, bufs.q_heads), "lse", device)
         lse = lse.data_ptr()
     _check(splitzip_kv_attention(cache.desc, batch.desc, rq, ro, lse, dtype, bufs.q_heads, scale, int(causal), window,
-                                 bufs.ws.data_ptr(), bufs.ws_bytes, bufs.status.data_ptr(), _stream_handle(stream)),
+                                 bufs.ws.data_ptr(), bufs.ws_bytes, bufs.status.data_ptr(), _kv_stream(stream, device)),
            "splitzip_kv_attention")

@@ -97,3 +97,24 @@ def test_offsets_that_descend_write_to_new_positions_only(dtype, cu):
         if step.fp8:
             changed = (getattr(step.cache, n + "_scale").cpu() != scales[n]).any(1)
             assert not bool((changed & ~allowed).any())
+
+
+def test_tensors_off_the_device_are_refused():
+    step = Step(BF16, [(3, 40), (1, 20)])
+    x = step.new_rows()
+    for status in (torch.zeros(4, dtype=torch.int32), torch.zeros(4, dtype=torch.int64, device="cuda"),
+                   torch.zeros(0, dtype=torch.int32, device="cuda")):
+        for call in (sz.kv_write, sz.kv_read):
+            with pytest.raises(ValueError):
+                call(step.cache, step.batch, x.cuda(), x.cuda(), status)
+    for call in (sz.kv_write, sz.kv_read):
+        with pytest.raises(ValueError):
+            call(step.cache, step.batch, x, x.cuda(), step.status)
+        with pytest.raises(ValueError):
+            call(step.cache, step.batch, x.cuda(), x, step.status)
+    q = torch.randn(step.tokens, 8, step.dim).to(BF16)
+    bufs = sz.KVAttentionBuffers(step.cache, step.batch, 8)
+    for args, lse in (((q, q.cuda()), None), ((q.cuda(), q), None), ((q.cuda(), q.cuda()), torch.zeros(step.tokens, 8))):
+        with pytest.raises(ValueError):
+            sz.kv_attention(step.cache, step.batch, *args, bufs, 0.1, lse=lse)
+    assert write(step) == sz.OK and attend(step) == sz.OK

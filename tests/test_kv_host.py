@@ -2,6 +2,7 @@
 any GPU work, and workspace sizes."""
 import ctypes
 import math
+import types
 
 import pytest
 import torch
@@ -159,3 +160,64 @@ def test_workspace_covers_steps_of_fewer_new_tokens_with_rows_to_spare(splitzip_
                     most = size(heads, max_tokens=tokens, **sizes)
                     for t in (0, 1, 2, 3, 8, 9, 32, 33):
                         assert size(heads, max_tokens=min(t, tokens), **sizes) <= most, (heads, sizes, t)
+
+
+def test_helpers_take_no_status_word_or_rows_off_the_device(splitzip_lib):
+    """A CPU tensor's address, or another device's, is never handed to a kernel."""
+    good = dict(status=torch.zeros(4, dtype=torch.int32), rows=torch.zeros(5, 2, 128, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        sz._kv_status(good["status"], 0)
+    with pytest.raises(ValueError):
+        sz._kv_rows(good["rows"], 5, 2, 128, 0, "k")
+    with pytest.raises(ValueError):
+        sz._device_tensor(torch.zeros(5, 8), torch.float32, (5, 8), "lse", 0)
+
+
+class OnDevice:
+    """What the helpers look at of a tensor, on a device that is not there."""
+    is_cuda = True
+
+    def __init__(self, t, index):
+        self.t, self.index, self.device = t, index, "cuda:%d" % index
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_helpers_refuse_tensors_of_several_devices(splitzip_lib, monkeypatch):
+    def on(index, *shape, dtype=torch.int32):
+        return OnDevice(torch.zeros(*shape, dtype=dtype), index)
+
+    def cache(k, v, *scales, dtype=torch.float8_e5m2):
+        return sz.KVCache(on(k, 4, 16, 2, 128, dtype=dtype), on(v, 4, 16, 2, 128, dtype=dtype),
+                          *(on(i, 4, 2, 16, dtype=torch.uint8) for i in scales))
+
+    def batch(cu, n, table):
+        return sz.KVBatch(on(cu, 4), on(n, 3), on(table, 3, 2), 5, 5, 32)
+
+    assert cache(1, 1, 1, 1).device == 1 and batch(1, 1, 1).device == 1
+    for devices in ((0, 1, 0, 0), (0, 0, 1, 0), (0, 0, 0, 1)):
+        with pytest.raises(ValueError):
+            cache(*devices)
+    for devices in ((1, 0, 0), (0, 1, 0), (0, 0, 1)):
+        with pytest.raises(ValueError):
+            batch(*devices)
+    for c, b in ((0, 1), (1, 0)):
+        with pytest.raises(ValueError):
+            batch(b, b, b).check(cache(c, c, c, c))
+    batch(1, 1, 1).check(cache(1, 1, 1, 1))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 70 + d)
+    stream = types.SimpleNamespace(device=torch.device("cuda:0"), cuda_stream=9)
+    assert sz._kv_stream(None, 0) == 70 and sz._kv_stream(stream, 0) == 9
+    stream.device = torch.device("cuda:1")
+    for s, device in ((None, 1), (stream, 0), (stream, 1)):  # not the current device, not the tensors'
+        with pytest.raises(ValueError):
+            sz._kv_stream(s, device)
+    assert sz._kv_status(on(1, 4), 1) > 0
+    for bad in (on(0, 4), on(1, 4, dtype=torch.int64), on(1, 0)):
+        with pytest.raises(ValueError):
+            sz._kv_status(bad, 1)
