@@ -804,7 +804,10 @@ class KVAttentionBuffers:
 def kv_attention(cache, batch, q, out, bufs, scale, causal=True, window=0, lse=None, stream=None):
     """Enqueue the attention of the new tokens' queries over `cache`'s pages
     (asynchronous).  q, out: packed (tokens, q_heads, head_dim); lse: None or
-    float32 (tokens, q_heads); bufs: KVAttentionBuffers."""
+    float32 (tokens, q_heads); bufs: KVAttentionBuffers; window: how many positions a
+    row sees up to its own, 0: all."""
+    if not 0 <= window < 1 << 32:
+        raise ValueError("window: expected 0 (none) or a number of positions, got %d" % window)
     batch.check(cache)
     device = cache.device
     if bufs.device != device:

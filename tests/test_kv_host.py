@@ -221,3 +221,9 @@ def test_helpers_refuse_tensors_of_several_devices(splitzip_lib, monkeypatch):
     for bad in (on(0, 4), on(1, 4, dtype=torch.int64), on(1, 0)):
         with pytest.raises(ValueError):
             sz._kv_status(bad, 1)
+
+
+@pytest.mark.parametrize("window", [-1, -5000, 1 << 32, (1 << 32) + 5])
+def test_windows_that_are_no_unsigned_32_bit_number_are_refused(splitzip_lib, window):
+    with pytest.raises(ValueError, match="window"):
+        sz.kv_attention(None, None, None, None, None, 0.1, window=window)
