@@ -309,7 +309,7 @@ int check_kv(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
     // keeps every byte offset below 2^62
     const uint64_t limit = uint64_t(1) << 40;
     if (cache->page_stride > limit || cache->token_stride > limit || cache->head_stride > limit ||
-        cache->page_stride * cache->pool_pages > (uint64_t(1) << 48))
+        cache->page_stride > (uint64_t(1) << 48) / cache->pool_pages)
         return SPLITZIP_ERR_UNSUPPORTED;
     if (need_ptrs) {
         if (!cache->d_k || !cache->d_v || (addr(cache->d_k) & 15u) || (addr(cache->d_v) & 15u))

@@ -227,3 +227,10 @@ def test_helpers_refuse_tensors_of_several_devices(splitzip_lib, monkeypatch):
 def test_windows_that_are_no_unsigned_32_bit_number_are_refused(splitzip_lib, window):
     with pytest.raises(ValueError, match="window"):
         sz.kv_attention(None, None, None, None, None, 0.1, window=window)
+
+
+@pytest.mark.parametrize("call", [write, read, attend])
+def test_pools_past_the_address_space_are_refused(splitzip_lib, call):
+    """Pages by stride is looked at without wrapping past 64 bits."""
+    for pages, stride in ((1 << 24, 1 << 40), (1 << 30, 1 << 34), ((1 << 31) - 1, 1 << 40), (3 << 24, 1 << 40)):
+        assert call(cache=dict(pool_pages=pages, page_stride=stride)) == sz.ERR_UNSUPPORTED, (pages, stride)
