@@ -505,9 +505,9 @@ int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* cache, const
  * values have to be in the cache (splitzip_kv_write).  A row that sees
  * nothing gets out = 0 and lse = -infinity; what a position holds that a row
  * does not see (NaN and infinities included) has no part in that row.
- * q, out: q_heads heads (a multiple of kv_heads, at most 64 times as many) of
- * `dtype` (BF16 or FP16; a 16-bit cache has to be of that type); out may be
- * q.  d_lse: float [tokens][q_heads] or null.  scale: finite.
+ * q, out: q_heads heads (a multiple of kv_heads, at most 64 times as many; by
+ * max_tokens at most 2^31 - 256 for a kv head) of `dtype` (BF16 or FP16; a
+ * 16-bit cache has to be of that type); out may be q.  d_lse: float [tokens][q_heads] or null.  scale: finite.
  * Statistics and sums are held in 32 bits; each exp() is rounded for the
  * product with V: to FP16 for FP16 queries, and for an FP8 cache where no
  * sequence has more than 32 rows (max_tokens by the query heads of a group),

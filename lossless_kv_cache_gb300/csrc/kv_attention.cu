@@ -41,7 +41,8 @@ uint64_t lay_out(Plan* p, uint64_t plan_bytes, uint64_t counters, uint64_t part_
 int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, Plan* p) {
     if (q_heads == 0 || q_heads % c.kv_heads != 0) return SPLITZIP_ERR_INVALID_ARG;
     p->group = q_heads / c.kv_heads;
-    if (p->group > 64) return SPLITZIP_ERR_UNSUPPORTED;
+    // the kernels count a sequence's rows, and up to a tile past them, in an int
+    if (p->group > 64 || uint64_t(b.max_tokens) * p->group > 0x7FFFFF00u) return SPLITZIP_ERR_UNSUPPORTED;
     const uint64_t rows = uint64_t(b.tokens) * p->group;
     p->chunk = uint64_t(b.max_tokens) * p->group > kStepRowsMax;
     // tiles of rows over all sequences: each has a partial one at most

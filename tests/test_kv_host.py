@@ -234,3 +234,15 @@ def test_pools_past_the_address_space_are_refused(splitzip_lib, call):
     """Pages by stride is looked at without wrapping past 64 bits."""
     for pages, stride in ((1 << 24, 1 << 40), (1 << 30, 1 << 34), ((1 << 31) - 1, 1 << 40), (3 << 24, 1 << 40)):
         assert call(cache=dict(pool_pages=pages, page_stride=stride)) == sz.ERR_UNSUPPORTED, (pages, stride)
+
+
+def test_rows_past_31_bits_are_refused(splitzip_lib):
+    """Rows of a sequence (new tokens by query heads of a group) are counted in 31 bits."""
+    q = dict(token_stride=128 * 128)
+    for tokens in (1 << 25, (1 << 25) + 1, 1 << 26, (1 << 30) - 1):
+        assert attend(batch=dict(tokens=tokens, max_tokens=tokens), q=q, out=q, q_heads=2 * 64) == sz.ERR_UNSUPPORTED
+        out = ctypes.c_uint64(0)
+        b = desc(sz.KVBatchDesc, BATCH, dict(tokens=tokens, max_tokens=tokens))
+        assert sz.splitzip_kv_attention_workspace_size(desc(sz.KVCacheDesc, CACHE, {}), b, 2 * 64, out) == sz.ERR_UNSUPPORTED
+        b = desc(sz.KVBatchDesc, BATCH, dict(tokens=tokens, max_tokens=(1 << 25) - 8))
+        assert sz.splitzip_kv_attention_workspace_size(desc(sz.KVCacheDesc, CACHE, {}), b, 2 * 64, out) == sz.OK
