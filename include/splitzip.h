@@ -454,7 +454,7 @@ typedef struct {
 typedef struct {
     const int32_t* d_cu_tokens;   /* batch + 1 */
     const int32_t* d_kv_len;      /* batch */
-    const int32_t* d_page_table;  /* batch rows of table_stride entries */
+    const int32_t* d_page_table;  /* batch rows of table_stride entries (null will do if max_kv_len is 0) */
     uint64_t table_stride;        /* >= ceil(max_kv_len / page_tokens) */
     uint32_t batch;               /* 1 .. 65536 */
     uint32_t tokens;              /* rows of the packed tensors */
@@ -505,9 +505,10 @@ int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* cache, const
  * values have to be in the cache (splitzip_kv_write).  A row that sees
  * nothing gets out = 0 and lse = -infinity; what a position holds that a row
  * does not see (NaN and infinities included) has no part in that row.
- * q, out: q_heads heads (a multiple of kv_heads, at most 64 times as many; by
- * max_tokens at most 2^31 - 256 for a kv head) of `dtype` (BF16 or FP16; a
- * 16-bit cache has to be of that type); out may be q.  d_lse: float [tokens][q_heads] or null.  scale: finite.
+ * q, out: q_heads heads (a multiple of kv_heads; at most 64 for each, and these
+ * by max_tokens at most 2^31 - 256) of `dtype` (BF16 or FP16; a 16-bit cache
+ * has to be of that type); out may be q.  d_lse: float [tokens][q_heads] or
+ * null.  scale: finite.
  * Statistics and sums are held in 32 bits; each exp() is rounded for the
  * product with V: to FP16 for FP16 queries, and for an FP8 cache where no
  * sequence has more than 32 rows (max_tokens by the query heads of a group),

@@ -315,8 +315,8 @@ int check_kv(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
         if (!cache->d_k || !cache->d_v || (addr(cache->d_k) & 15u) || (addr(cache->d_v) & 15u))
             return SPLITZIP_ERR_INVALID_ARG;
         if (fp8 && (!cache->d_k_scale || !cache->d_v_scale)) return SPLITZIP_ERR_INVALID_ARG;
-        if (!batch->d_cu_tokens || !batch->d_kv_len || !batch->d_page_table || (addr(batch->d_cu_tokens) & 3u) ||
-            (addr(batch->d_kv_len) & 3u) || (addr(batch->d_page_table) & 3u))
+        if (!batch->d_cu_tokens || !batch->d_kv_len || (!batch->d_page_table && batch->max_kv_len > 0) ||
+            (addr(batch->d_cu_tokens) & 3u) || (addr(batch->d_kv_len) & 3u) || (addr(batch->d_page_table) & 3u))
             return SPLITZIP_ERR_INVALID_ARG;
     }
     if (batch->batch == 0 || batch->max_tokens > batch->tokens) return SPLITZIP_ERR_INVALID_ARG;

@@ -1,6 +1,8 @@
 """GPU: steps whose integer arrays are wrong.  Every call reports them, also
 where no packed row belongs to the sequence, and nothing is written but to new
 positions of sequences whose own entries are in range."""
+import math
+
 import pytest
 import torch
 
@@ -118,3 +120,22 @@ def test_tensors_off_the_device_are_refused():
         with pytest.raises(ValueError):
             sz.kv_attention(step.cache, step.batch, *args, bufs, 0.1, lse=lse)
     assert write(step) == sz.OK and attend(step) == sz.OK
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+def test_a_step_that_holds_nothing_needs_no_page_table(dtype, new):
+    step = Step(dtype, [(new, 0), (0, 0), (new, 0)])
+    step.batch = sz.KVBatch(step.batch.cu_tokens, step.batch.kv_len, torch.empty(3, 0, dtype=torch.int32, device="cuda"),
+                            step.tokens, new, 0)
+    assert write(step) == sz.OK
+    k, v = (torch.full((step.tokens, 2, 128), 7.0, dtype=BF16, device="cuda") for _ in range(2))
+    sz.kv_read(step.cache, step.batch, k, v, step.status)
+    assert int(step.status[0]) == sz.OK and not bool(k.any()) and not bool(v.any())
+    q = torch.randn(step.tokens, 8, 128, generator=step.gen).to(BF16).cuda()
+    out, lse = torch.full_like(q, 7.0), torch.zeros(step.tokens, 8, device="cuda")
+    bufs = sz.KVAttentionBuffers(step.cache, step.batch, 8)
+    sz.kv_attention(step.cache, step.batch, q, out, bufs, 0.1, lse=lse)
+    assert int(bufs.status[0]) == sz.OK and not bool(out.any()) and bool((lse == -math.inf).all())
+    step.batch.kv_len[1] = 1  # past max_kv_len
+    assert write(step) == read(step) == attend(step) == sz.ERR_INVALID_ARG

@@ -246,3 +246,11 @@ def test_rows_past_31_bits_are_refused(splitzip_lib):
         assert sz.splitzip_kv_attention_workspace_size(desc(sz.KVCacheDesc, CACHE, {}), b, 2 * 64, out) == sz.ERR_UNSUPPORTED
         b = desc(sz.KVBatchDesc, BATCH, dict(tokens=tokens, max_tokens=(1 << 25) - 8))
         assert sz.splitzip_kv_attention_workspace_size(desc(sz.KVCacheDesc, CACHE, {}), b, 2 * 64, out) == sz.OK
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU error path")
+@pytest.mark.parametrize("call", [write, read, attend])
+def test_a_step_that_holds_nothing_needs_no_page_table(splitzip_lib, call):
+    assert call(batch=dict(max_kv_len=0, table_stride=0, d_page_table=None)) in (sz.ERR_CUDA, sz.ERR_UNSUPPORTED)
+    assert call(batch=dict(max_kv_len=1, table_stride=1, d_page_table=None)) == sz.ERR_INVALID_ARG
+    assert call(batch=dict(max_kv_len=0, table_stride=0, d_page_table=A + 2)) == sz.ERR_INVALID_ARG
