@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import lossless_kv_cache_gb300 as sz
-from tests.kv_long_reference import attention64, vary_scales
-from tests.kv_reference import Step, check_attention
+from tests.kv_long_reference import LongStep, attention64, vary_scales
+from tests.kv_reference import check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -61,7 +61,7 @@ MANY = [(33, 100 + 2 * b) for b in range(150)]
 def test_chunks_with_a_scale_for_each_key(dtype, dim, lens):
     """FP16 queries over FP8 pages, whose scores take K's scales after the product: each key's
     has to be its own for as long as a unit waits for its softmax."""
-    step = Step(dtype, lens, kv_heads=8, dim=dim, x=FP16, spread=0.3)
+    step = LongStep(dtype, lens, dim=dim, x=FP16)
     vary_scales(step, "k", -3, 3)
     check(step)
     # NaN at positions that only some rows see hold the softmax up, while the loaders go on
@@ -70,3 +70,65 @@ def test_chunks_with_a_scale_for_each_key(dtype, dim, lens):
         step.set_value("v", b, n - 1, b % 8, 9, math.nan)
     check(step)
     check(step, window=500)
+
+
+TYPES = [(BF16, BF16), (FP16, FP16), (E5M2, BF16), (E5M2, FP16), (E4M3, BF16), (E4M3, FP16)]
+
+
+def plant_nan(step, every):
+    """NaN in V where some of a sequence's rows see it, and before all of its rows for some."""
+    for b, (t, n) in enumerate(step.lens):
+        if b % every == 0 and t > 0:
+            step.set_value("v", b, max(0, n - t + b % 3), b % step.kv_heads, 5, math.nan)
+            step.set_value("v", b, n - 1, (b + 1) % step.kv_heads, 9, math.nan)
+            if b % (2 * every) == 0:
+                step.set_value("v", b, n // 3, (b + 2) % step.kv_heads, 11, math.nan)
+
+
+@pytest.mark.parametrize("lens", [LONG, SEVERAL, MANY], ids=["long", "several", "many"])
+@pytest.mark.parametrize("page", [16, 4])
+@pytest.mark.parametrize("dtype,x", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_chunks(dtype, x, dim, page, lens):
+    """Every instance of the chunk kernel: 16-bit pages of eight tokens and more are read by tensor
+    maps, smaller ones row by row."""
+    step = LongStep(dtype, lens, dim=dim, x=x, page=page)
+    if step.fp8:
+        vary_scales(step, "k", -2, 2)
+        vary_scales(step, "v", -2, 2)
+    check(step)
+    plant_nan(step, 1 if page == 16 else 7)
+    check(step, window=900)
+
+
+@pytest.mark.parametrize("dtype,x", TYPES)
+@pytest.mark.parametrize("page", [8, 256])
+def test_chunks_without_causality_and_other_pages(dtype, x, page):
+    step = LongStep(dtype, [(300, 4001), (129, 2600), (40, 3333)], x=x, page=page)
+    check(step, causal=False)
+    check(step, causal=False, window=1000)
+    check(step, group=3)
+
+
+# Shares of the step kernel, 64 keys a unit, over up to 608 blocks: about 11 units of one item or
+# two; 12 of several items; 12 of one item that 76 blocks share.
+STEP_LONG = [(1, 3500 + 11 * b) for b in range(16)]
+STEP_MANY = [(1, 190 + 4 * b) for b in range(130)]
+STEP_ONE = [(1, 60007)]
+
+
+@pytest.mark.parametrize("lens", [STEP_LONG, STEP_MANY, STEP_ONE], ids=["long", "many", "one"])
+@pytest.mark.parametrize("page", [16, 4])
+@pytest.mark.parametrize("dtype,x", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_steps(dtype, x, dim, page, lens):
+    """Every instance of the step kernel, by 4, 16 and 32 rows a sequence."""
+    for new in (1, 4, 8):
+        step = LongStep(dtype, [(new, n) for _, n in lens], dim=dim, x=x, page=page)
+        if step.fp8:
+            vary_scales(step, "k", -2, 2)
+            vary_scales(step, "v", -2, 2)
+        check(step)
+        if new > 1:
+            plant_nan(step, 1 if page == 16 else 7)
+            check(step, window=1500)
