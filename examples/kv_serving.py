@@ -35,7 +35,12 @@ class Side:
         self.cu_tokens = torch.zeros(2, dtype=torch.int32, device=device)
         self.kv_len = torch.zeros(1, dtype=torch.int32, device=device)
         self.status = torch.zeros(4, dtype=torch.int32, device=device)
+        self.worst = torch.zeros(1, dtype=torch.int32, device=device)
         self.buffers = {}
+
+    def note(self, status):
+        """Keeps a call's status, in stream order: the next call clears the word."""
+        torch.maximum(self.worst, status[:1], out=self.worst)
 
     def step(self, q, k, v):
         """The next tokens of the sequence: into the cache, then over it.  Returns
@@ -48,7 +53,9 @@ class Side:
             self.buffers[new] = sz.KVAttentionBuffers(self.cache, batch, HEADS)
         out = torch.empty_like(q)
         sz.kv_write(self.cache, batch, k, v, self.status)
+        self.note(self.status)
         sz.kv_attention(self.cache, batch, q, out, self.buffers[new], 1.0 / math.sqrt(HEAD_DIM))
+        self.note(self.buffers[new].status)
         return out
 
     def read(self, tokens):
@@ -59,6 +66,7 @@ class Side:
         k, v = (torch.empty(tokens, KV_HEADS, HEAD_DIM, dtype=torch.bfloat16, device=self.pages.device)
                 for _ in range(2))
         sz.kv_read(self.cache, batch, k, v, self.status)
+        self.note(self.status)
         return k, v
 
 
@@ -80,6 +88,7 @@ def send(sender, receiver, used):
         assert status == sz.OK
         container = bufs.out[:size].clone()  # what the link carries
         sz.decode_paged_into(container, size, to, receiver.pages[:used], page_elems, sz.FP8_E5M2, receiver.status)
+        receiver.note(receiver.status)
         scale_from, scale_to = (getattr(s.cache, name + "_scale") for s in (sender, receiver))
         scale_to[receiver.pages[:used].long()] = scale_from[sender.pages[:used].long()]
         raw += n
@@ -111,9 +120,7 @@ def run(prompt=1000, chunk=384, steps=8, seed=0, device="cuda"):
     k, v = decode.read(prompt + steps)
     k2, v2 = prefill.read(prompt + steps)
     assert torch.equal(k, k2) and torch.equal(v, v2)
-    assert int(prefill.status[0]) == sz.OK and int(decode.status[0]) == sz.OK
-    for side in (prefill, decode):
-        assert all(int(b.status[0]) == sz.OK for b in side.buffers.values())
+    assert int(prefill.worst) == sz.OK and int(decode.worst) == sz.OK  # of every call
     return torch.cat(outs), raw, link
 
 

@@ -36,3 +36,16 @@ def test_chunks_and_steps_agree_within_roundings(splitzip_lib):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
     assert torch.equal(one.cache.k_scale, many.cache.k_scale)
     assert float((a.float() - b.float()).abs().max()) <= 4 * 2.0 ** -8 * float(v.float().abs().max())
+
+
+def test_an_early_failure_is_not_lost(splitzip_lib):
+    """Each call clears its status word; the example keeps the worst of all calls."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    qkv = [torch.randn(20, h, 128, generator=g, device="cuda").bfloat16() for h in (32, 8, 8)]
+    side = kv_serving.Side(4, [3, 1], "cuda")
+    side.pages[1] = 9  # past the pool
+    side.step(*qkv)
+    side.pages[1] = 1
+    side.step(*(x[:1] for x in qkv))
+    assert int(side.status[0]) == sz.OK
+    assert int(side.worst) == sz.ERR_INVALID_ARG
