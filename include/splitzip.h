@@ -504,7 +504,10 @@ int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* cache, const
  * 0, and j > p - window unless `window` is 0.  The new tokens' own keys and
  * values have to be in the cache (splitzip_kv_write).  A row that sees
  * nothing gets out = 0 and lse = -infinity; what a position holds that a row
- * does not see (NaN and infinities included) has no part in that row.
+ * does not see (NaN and infinities included) has no part in that row.  What it
+ * does see has: a NaN or an infinity of V makes its column infinite or NaN, a
+ * score of NaN or +infinity makes the row and its lse NaN; one of -infinity has
+ * the weight 0, and a row of nothing else sees nothing.
  * q, out: q_heads heads (a multiple of kv_heads; at most 64 for each, and these
  * by max_tokens at most 2^31 - 256) of `dtype` (BF16 or FP16; a 16-bit cache
  * has to be of that type); out may be q.  d_lse: float [tokens][q_heads] or

@@ -8,7 +8,7 @@ import torch
 
 import lossless_kv_cache_gb300 as sz
 from tests.kv_long_reference import attention64
-from tests.kv_reference import RAW, Step, half_step
+from tests.kv_reference import RAW, Step, check_attention, half_step
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,43 @@ def test_rows_of_zeros_in_v_leave_the_others_their_weights(dtype, dim, small, le
     tol = tol + keys * 2.0 ** -38 * most_weight(step, q, scale)[..., None]
     worst = float(((out.double().cpu() - ref).abs() / tol).max())
     assert worst <= 1
+
+
+@pytest.mark.parametrize("dtype,x", [(BF16, BF16), (FP16, FP16), (E5M2, BF16), (E5M2, FP16)])
+@pytest.mark.parametrize("lens", [[(3, 300), (2, 2)], [(70, 600), (40, 40)]])
+def test_infinite_scores(dtype, x, lens):
+    """+infinity: the rows that see it are NaN; -infinity: a weight of 0, and a row that sees
+    nothing else sees nothing."""
+    dim, heads, scale = 128, 8, 0.05
+    for value in (math.inf, -math.inf):
+        step = Step(dtype, lens, x=x, spread=0.3)
+        q = torch.randn(step.tokens, heads, dim, generator=step.gen).to(step.x)
+        q[:, :, 7] = q[:, :, 7].abs() + 1
+        at = [n - 2 for _, n in lens]
+        for b, pos in enumerate(at):
+            for h in range(2):
+                step.set_value("k", b, pos, h, 7, value)
+        step.set_value("k", 1, 0, 0, 7, value)
+        out, lse = torch.empty_like(q).cuda(), torch.empty(q.shape[:2], device="cuda")
+        bufs = sz.KVAttentionBuffers(step.cache, step.batch, heads)
+        sz.kv_attention(step.cache, step.batch, q.cuda(), out, bufs, scale, lse=lse)
+        assert int(bufs.status[0]) == sz.OK
+        seen = torch.zeros(step.tokens, heads, dtype=torch.bool)
+        for b, (t, n) in enumerate(lens):
+            for i in range(t):
+                seen[step.cu[b] + i] = n - t + i >= at[b]
+                if b == 1 and n == t:  # from position 0 on, the first kv head
+                    seen[step.cu[b] + i, : heads // 2] = True
+        if value > 0:
+            assert bool(torch.isnan(out.cpu()[seen]).all()) and bool(torch.isnan(lse.cpu()[seen]).all())
+        else:
+            first = step.cu[1]  # sees position 0 alone
+            assert bool((out[first, : heads // 2] == 0).all()) and bool((lse[first, : heads // 2] == -math.inf).all())
+            seen[:] = False
+        ref, ref_lse, mag, _ = attention64(step, q, scale)
+        step.host["k"][~torch.isfinite(step.host["k"])] = 0.0
+        size = attention64(step, q, scale)[3]
+        ref, mag = ref.nan_to_num(0.0), mag.nan_to_num(0.0)
+        keep = ~seen
+        weight = FP16 if x == FP16 or (step.fp8 and step.max_new * heads // 2 <= 32) else BF16
+        check_attention(step, out.cpu()[keep], lse.cpu()[keep], (ref[keep], ref_lse[keep], mag[keep], size[keep]), weight)
