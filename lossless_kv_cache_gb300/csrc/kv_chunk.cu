@@ -15,31 +15,37 @@
 // What bounds it: the tensor core, 4 * head_dim operations for each (row,
 // key), with the exponentials next.  A CTA holds two tiles of 128 rows (new
 // tokens by the query heads that share a kv head) and passes over the keys
-// once for both.  Sixteen warps:
-//   0-3, 4-7   one tile's softmax each: a thread is a row; scores from TMEM,
-//              exponentials back to TMEM as the first operand of the product
-//              with V; rescaling and the final division are theirs too
-//   8-11       loaders: rows of K and V from their pages into swizzled shared
-//              memory (cp.async for a 16-bit cache; FP8 by way of a staging
-//              buffer, converted by the thread that copied it), rows past the
-//              end as zeros
-//   13         one thread walks the CTA's share and describes its pieces
-//   12         issues the products, in the order
+// once for both.  Its warps:
+//   softmax    0-3 and 4-7, one tile's each: a thread is a row; scores from
+//              TMEM, exponentials back to TMEM as the first operand of the
+//              product with V; rescaling and the final division are theirs too
+//   loaders    K and V from their pages into swizzled shared memory.  16-bit
+//              pages of eight tokens and more: warp 8, a box of a tensor map a
+//              lane (twelve warps in all).  Otherwise 8-11, row by row with
+//              cp.async (sixteen in all): smaller 16-bit pages in place, FP8 by
+//              way of a staging buffer, converted by the thread that copied it
+//   products   one warp (9 or 12) issues them, in the order
 //              S0(j+1) | P1(j) V(j) | S1(j+1) | P0(j+1) V(j+1) | ...
 //              so that each tile's softmax runs under the other's products
+//   pieces     one thread of the next warp (10 or 13) walks the CTA's share and
+//              describes its pieces
 // TMEM: S0, S1 (128 columns each, the weights overwrite the scores), O0, O1.
 // The tensor core executes a CTA's products in the order of issue, which is
 // what lets S(j+1) overwrite the weights that P(j) V(j) reads.
 //
-// One GB300, 32 query heads of 128 over 8: 2,048 new tokens over 32,768 of BF16
-// in 835 us (1.28 PFLOP/s, 67 % of the measured library product), a prompt of
-// 8,192 tokens of FP16 in 449 us (1.22 PFLOP/s, 64 %), six chunks of up to 777
-// over up to 5,000 of E4M3 in 138 us (0.5 PFLOP/s).  A unit of 256 rows by 128
+// One GB300, 32 query heads of 128 over 8, in graphs: 2,048 new tokens over
+// 32,768 of BF16 in 853 us (1.25 PFLOP/s, 65 % of the measured library product),
+// a prompt of 8,192 tokens of FP16 in 445 us (1.24 PFLOP/s, 64 %), six chunks of
+// up to 777 over up to 5,000 of E4M3 in 136 us (0.5 PFLOP/s); heads of 64, the
+// first of these, 586 us (0.91 PFLOP/s, 47 %).  A unit of 256 rows by 128
 // keys takes about 3,500 cycles of which the products are 2,048: a tile's next
 // scores wait for its weights (its softmax takes 1,600 and its two hand-overs
 // 650), and what K and V cost of the shared memory's bandwidth slows the
 // products by 600.  FP8 takes about 6,000, bound by the conversion on the way
-// into shared memory (its loaders share the issue slots with the softmax).
+// into shared memory (its loaders share the issue slots with the softmax), and
+// every row tile of a sequence converts all its keys again.  The kernels of
+// sixteen warps have 128 registers a thread at launch and spill 204 bytes (FP16
+// queries over FP8: 286 at 64 dims, 346 at 128); those of twelve spill none.
 // Handing the weights over in halves, two threads a row, spinning waits and
 // pipelined exponentials all measured the same or slower.
 //
@@ -66,7 +72,8 @@ constexpr int kPlanThreads = 1024;
 // What an item costs beside its keys (its rows of Q in and results out, the
 // pipeline's start), in units: the plan counts that many before the item's own.
 // The 8,192-token prompt took 596, 477, 449, 472 and 481 us with 4, 6, 8, 10 and
-// 14; six ragged chunks over E4M3 164, 145, 136, 148 and 142.
+// 14; six ragged chunks over E4M3 164, 145, 136, 148 and 142.  Those two, of 128
+// dims, are what it was chosen by.
 constexpr int kItemCost = 8;
 
 // Tensor maps of K and V (unused by the kernels that copy rows themselves).
@@ -1257,8 +1264,8 @@ int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan_at, uint32_t
     if (a.c.type == SPLITZIP_KV_FP8_E5M2) return launch_type<1>(a, q_half, plan, maps, ctas, s);
     if (a.c.type == SPLITZIP_KV_FP8_E4M3) return launch_type<2>(a, q_half, plan, maps, ctas, s);
     // By tensor maps where the pages allow it: a box's rows have to be whole groups of
-    // eight for the swizzle.  2,048 tokens over 32,768 in pages of 16 take 835 us so, and
-    // 1,104 with every row copied by the loaders' threads.
+    // eight for the swizzle.  2,048 tokens over 32,768 in pages of 16 took 835 us so, and
+    // 1,104 with every row copied by the loaders' threads (in turn on one GPU).
     if (a.c.page_shift >= 3 && make_maps(a, &maps)) return launch_type<3>(a, q_half, plan, maps, ctas, s);
     return launch_type<0>(a, q_half, plan, maps, ctas, s);
 }

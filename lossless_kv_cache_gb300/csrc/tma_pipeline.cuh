@@ -67,7 +67,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     return mbar_wait_limit(bar, parity, kWaitLimitCycles);
 }
 
-// Whether the phase is complete, without suspending the thread as try_wait may.
 // Global -> shared bulk copy; completes `bytes` of the barrier's transaction
 // count.  dst, src and bytes must be multiples of 16.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
