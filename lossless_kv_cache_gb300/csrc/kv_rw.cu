@@ -16,8 +16,8 @@
 // sequence and page is done once for all of them while their loads are in
 // flight; more rows a warp (two passes) measured the same, with more
 // registers.  One GB300: a 32,768-token layer of 8 heads of 128 to E5M2 in
-// 34.9 us (5.8 TB/s, 85 % of the measured copy rate), 65,536 E5M2 tokens read
-// in 62.1 us (6.5 TB/s, 96 %).
+// 34.1 us (5.9 TB/s, 87 % of the measured copy rate), 65,536 E5M2 tokens read
+// in 62.9 us (6.4 TB/s, 95 %).
 #include "kv_common.cuh"
 
 namespace splitzip {

@@ -31,8 +31,8 @@
 //
 // One GB300, 32 query heads of 128 over 8, in a graph: 64 sequences of 8,192 E5M2
 // tokens in 208 us (5.2 TB/s, 77 % of the measured copy rate; 186 to 211 on five of
-// these GPUs), 512 of 1,024 in 218 us, one of 65,536 BF16 tokens in 49 us (5.5 TB/s,
-// 81 %), four of 500 in 8.4 us, most of which is two launches, the scan and the
+// these GPUs), 512 of 1,024 in 218 us, one of 65,536 BF16 tokens in 49 us (5.4 TB/s,
+// 80 %), four of 500 in 8.4 us, most of which is two launches, the scan and the
 // first loads' latency.  Heads of 64, the first of these: 184 us (3.0 TB/s, 44 %).
 #include <algorithm>
 #include <atomic>
