@@ -132,3 +132,15 @@ def test_steps(dtype, x, dim, page, lens):
         if new > 1:
             plant_nan(step, 1 if page == 16 else 7)
             check(step, window=1500)
+
+
+@pytest.mark.parametrize("dtype,x", [(BF16, BF16), (E4M3, FP16)])
+@pytest.mark.parametrize("most", [1, 9, 700])
+def test_batches_of_thousands(dtype, x, most):
+    """More sequences than one round of the chunk kernel's plan (1,024) or of the step kernel's
+    scan (128) takes, with none, one or many tiles of rows in turn."""
+    lens = [(min(most, (0, 1, 3, 1, 9, 1, 0, 40)[b % 8]), 1 + b * 7 % 90) for b in range(2600)]
+    for b in (3, 1023, 1024, 2050, 2599):
+        lens[b] = (most, 1400 + b % 5)
+    step = LongStep(dtype, [(t, max(n, t)) for t, n in lens], kv_heads=2, dim=64, x=x)
+    check(step, group=3)
