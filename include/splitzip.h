@@ -529,6 +529,160 @@ int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_ba
                           uint32_t q_heads, float scale, int causal, uint32_t window, void* d_ws,
                           uint64_t ws_bytes, int* d_status, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A step around the paged cache, speculative ones included: page tables and
+ * lengths kept on the GPU (splitzip_kv_extend), rotary positions with the
+ * write of the new tokens (splitzip_kv_rotary_write), attention of a tree of
+ * drafted tokens (splitzip_kv_tree, splitzip_kv_tree_attention), and the
+ * accepted branch moved to the front of the drafted tokens
+ * (splitzip_kv_keep).  Nothing in them needs the host to know a length, so a
+ * whole step can be captured once.
+ */
+
+/* The pages of one pool and the sequences that hold them: device arrays of
+ * int32, 4-byte aligned.  Sequence b holds held[b] pages, entries 0 ..
+ * held[b] - 1 of its row of the page table; the free pages are entries 0 ..
+ * free_count[0] - 1 of the list d_free, the next one to be taken last. */
+typedef struct {
+    int32_t* d_free;           /* pool_pages entries */
+    const int32_t* d_free_count;
+    const int32_t* d_held;     /* batch: pages of each sequence */
+    const int32_t* d_kv_len;   /* batch: tokens of each sequence */
+    int32_t* d_page_table;     /* batch rows of table_stride entries */
+    uint64_t table_stride;
+    uint32_t table_pages;      /* entries of a row that may be used, <= table_stride */
+    uint32_t pool_pages;
+    uint32_t page_tokens;      /* a power of two, 1 .. 65536 */
+    uint32_t batch;            /* 1 .. 65536 */
+} splitzip_kv_pages_t;
+
+/* What a step makes of them: device arrays; lengths, held pages and the count
+ * may be the arrays that they were read from (the pages are then updated in
+ * place) or others (the next step is prepared while this one's are in use;
+ * list and table are shared).  d_position and d_slot may be null. */
+typedef struct {
+    int32_t* d_free_count;
+    int32_t* d_held;
+    int32_t* d_kv_len;
+    int32_t* d_cu_tokens;      /* batch + 1 */
+    int32_t* d_position;       /* tokens: position of each packed row */
+    int64_t* d_slot;           /* tokens: page * page_tokens + position mod page_tokens; 8-byte aligned */
+    uint32_t tokens;           /* rows that d_position and d_slot have */
+    uint32_t max_tokens;       /* most new tokens of one sequence, <= tokens */
+    uint32_t max_kv_len;       /* most tokens that a sequence may hold, < 2^30 */
+} splitzip_kv_step_t;
+
+int splitzip_kv_extend_workspace_size(uint32_t batch, uint64_t* out_bytes);
+
+/* Gives the sequences the pages of a step: sequence b gives up its last
+ * drop[b] tokens (d_drop null: none), then takes new[b] more, so that
+ *   kv_len'[b] = kv_len[b] - drop[b] + new[b],
+ *   held'[b] = ceil(kv_len'[b] / page_tokens),
+ * cu_tokens' is the exclusive sum of new, and row cu_tokens'[b] + i is position
+ * kv_len'[b] - new[b] + i.  First the pages that sequences no longer need go on
+ * the free list, those of the last sequence first and of each its last first
+ * (which takes an extension back exactly); then the missing ones are taken off
+ * it, for the first sequence first.  drop[b] = kv_len[b] with new[b] = 0 ends a
+ * sequence.  Entries of a table row past a sequence's pages are left as they
+ * were, and so are d_position and d_slot past the last row.
+ *
+ * All or nothing: with fewer free pages than missing ones
+ * (SPLITZIP_ERR_CAPACITY in *d_status), or with any entry out of range (new
+ * outside 0 .. max_tokens, drop outside 0 .. kv_len, lengths past max_kv_len or
+ * the table, more than `tokens` rows, held pages fewer than the tokens need or
+ * more than the table or the pool has, a count outside 0 .. pool_pages;
+ * SPLITZIP_ERR_INVALID_ARG) lengths, held pages and count come out as they
+ * went in, lists, tables, positions and slots are not touched, and cu_tokens'
+ * is all zeros: what follows in the step finds nothing to do.
+ * d_ws: ws_bytes >= splitzip_kv_extend_workspace_size, 16-byte aligned, contents
+ * need not be initialised; calls that share it must not overlap on the GPU.
+ * *d_status is set by the call. */
+int splitzip_kv_extend(const splitzip_kv_pages_t* pages, const int32_t* d_new, const int32_t* d_drop,
+                       const splitzip_kv_step_t* step, void* d_ws, uint64_t ws_bytes, int* d_status,
+                       cudaStream_t stream);
+
+/* Rotary positions.  The first rotary_dim elements of a head are rotary_dim / 2
+ * pairs: elements 2j and 2j + 1 where `interleaved`, else j and j +
+ * rotary_dim / 2.  At position p pair j is turned by the angle 2 pi p f_j and
+ * multiplied by `magnitude`,
+ *   (a, b) -> magnitude (a cos - b sin, a sin + b cos);
+ * the other elements stay as they are.  d_turns[j] is f_j in turns a position as
+ * a fraction of 2^64 (f_j mod 1; the fraction p f_j mod 1 of a turn is then
+ * exact for every p).  Context scaling is a matter of the f_j and of the
+ * magnitude. */
+typedef struct {
+    const uint64_t* d_turns;     /* rotary_dim / 2, 8-byte aligned */
+    const int32_t* d_position;   /* position of each packed row, null: its place in the cache */
+    uint32_t rotary_dim;         /* a multiple of 16, at most head_dim */
+    int32_t interleaved;
+    float magnitude;             /* finite */
+} splitzip_kv_rotary_t;
+
+/* Rotates the queries q (into q_out, which may be q; both null: none) and the
+ * keys k of the new tokens, and writes the rotated keys and the values v into
+ * their pages as splitzip_kv_write does.  Sines, cosines and products are in 32
+ * bits, each result rounded once: of a query to `dtype`, of a key to the
+ * cache's type (FP8: with the scale that the rotated row in 32 bits asks for).
+ * Rows that have no place (splitzip_kv_batch_t) have their queries rotated and
+ * nothing written; rows of no sequence are left alone. */
+int splitzip_kv_rotary_write(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                             const splitzip_kv_rotary_t* rotary, const splitzip_kv_rows_t* q,
+                             const splitzip_kv_rows_t* q_out, uint32_t q_heads, const splitzip_kv_rows_t* k,
+                             const splitzip_kv_rows_t* v, int dtype, int* d_status, cudaStream_t stream);
+
+/* Trees of drafted tokens.  The new tokens of a sequence are a forest over its
+ * older ones: parent[row] is the parent's number among them (0: the
+ * sequence's first new token), smaller than the row's own, or -1 for a
+ * successor of the last older token. */
+#define SPLITZIP_MAX_TREE_TOKENS 1024u /* of one sequence */
+
+typedef struct {
+    uint32_t* d_mask;     /* [tokens][words]: bit j of a row says whether it sees new token j of its sequence */
+    int32_t* d_position;  /* tokens */
+    uint32_t words;       /* >= ceil(max_tokens / 32), <= 32 */
+    uint32_t window;      /* how many positions a row sees up to its own, 0: all */
+} splitzip_kv_tree_t;
+
+/* Fills in masks and positions of a step from d_parent (int32 [tokens]), once
+ * for all layers: a row's mask has its ancestors and itself (the nearest
+ * `window` of them), its position is kv_len - t + depth, depth 0 for parent -1.
+ * A sequence that has a parent out of range gets masks of zeros and the
+ * positions of a chain, one whose entries are out of range nothing, and both are
+ * reported in *d_status (SPLITZIP_ERR_INVALID_ARG).  max_tokens is at most
+ * SPLITZIP_MAX_TREE_TOKENS.  The page table is not looked at. */
+int splitzip_kv_tree(const splitzip_kv_batch_t* batch, const int32_t* d_parent, const splitzip_kv_tree_t* tree,
+                     int* d_status, cudaStream_t stream);
+
+/* Attention as splitzip_kv_attention's, its workspace and roundings included,
+ * of rows that see
+ *   - every position before the sequence's new tokens, with tree->window only
+ *     those after position - window, position being the row's d_position (as the
+ *     nearest that a tree can give it, if it is less than the first new token's
+ *     or past its own place);
+ *   - the new tokens that its mask has a bit for (bits past the last are
+ *     ignored).
+ * Masks and positions are splitzip_kv_tree's, for the same window, or the
+ * caller's own.  A row of no place sees nothing. */
+int splitzip_kv_tree_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                               const splitzip_kv_tree_t* tree, const splitzip_kv_rows_t* q,
+                               const splitzip_kv_rows_t* out, float* d_lse, int dtype, uint32_t q_heads, float scale,
+                               void* d_ws, uint64_t ws_bytes, int* d_status, cudaStream_t stream);
+
+#define SPLITZIP_MAX_LAYERS 256u
+
+/* Moves the accepted new tokens to the front, in `count` caches (layers) of one
+ * geometry at once: new token path[cu_tokens[b] + i] of sequence b, i <
+ * kept[b], to the place of new token i, K, V and scales.  path is strictly
+ * ascending in each sequence.  What the cache holds behind the kept ones is
+ * unspecified; lengths are splitzip_kv_extend's to change (drop = t - kept).
+ * A sequence whose entries, path or count (0 .. t) are out of range, or that has
+ * new tokens without a place, is left as it was and reported, a page out of
+ * range is skipped and reported.  h_caches: host memory, read during the call;
+ * everything but the pointers has to be the same in all
+ * (SPLITZIP_ERR_INVALID_ARG). */
+int splitzip_kv_keep(const splitzip_kv_cache_t* h_caches, uint32_t count, const splitzip_kv_batch_t* batch,
+                     const int32_t* d_path, const int32_t* d_kept, int* d_status, cudaStream_t stream);
+
 /* Self-test of the bounded device wait.  Every wait of the encode and
  * decode kernels on a bulk-copy barrier gives up after a bounded number of SM
  * cycles (about one second), records SPLITZIP_ERR_TIMEOUT in the status word

@@ -7,7 +7,9 @@ status codes.  Every step of the codec runs in the CUDA kernels of
 ``libsplitzip.so``; this module only marshals arguments.  The torch helpers at
 the end (``calibrate``, ``encode``, ``decode``) allocate device memory with
 torch and call the same entry points.  ``kv_write``, ``kv_read`` and
-``kv_attention`` are the operators over the paged cache that the codec moves.
+``kv_attention`` are the operators over the paged cache that the codec moves;
+``kv_extend``, ``kv_rotary_write``, ``kv_tree``, ``kv_tree_attention`` and
+``kv_keep`` are the rest of a (speculative) serving step over it.
 
 Method: "SplitZip: Ultra Fast Lossless KV Compression for Disaggregated LLM
 Serving", section "Method: SplitZip".
@@ -100,8 +102,37 @@ class KVRowsDesc(ctypes.Structure):
     _fields_ = [("d", ctypes.c_void_p), ("token_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64)]
 
 
+class KVPagesDesc(ctypes.Structure):
+    """splitzip_kv_pages_t."""
+    _fields_ = [("d_free", ctypes.c_void_p), ("d_free_count", ctypes.c_void_p), ("d_held", ctypes.c_void_p),
+                ("d_kv_len", ctypes.c_void_p), ("d_page_table", ctypes.c_void_p), ("table_stride", ctypes.c_uint64),
+                ("table_pages", ctypes.c_uint32), ("pool_pages", ctypes.c_uint32), ("page_tokens", ctypes.c_uint32),
+                ("batch", ctypes.c_uint32)]
+
+
+class KVStepDesc(ctypes.Structure):
+    """splitzip_kv_step_t."""
+    _fields_ = [("d_free_count", ctypes.c_void_p), ("d_held", ctypes.c_void_p), ("d_kv_len", ctypes.c_void_p),
+                ("d_cu_tokens", ctypes.c_void_p), ("d_position", ctypes.c_void_p), ("d_slot", ctypes.c_void_p),
+                ("tokens", ctypes.c_uint32), ("max_tokens", ctypes.c_uint32), ("max_kv_len", ctypes.c_uint32)]
+
+
+class KVRotaryDesc(ctypes.Structure):
+    """splitzip_kv_rotary_t."""
+    _fields_ = [("d_turns", ctypes.c_void_p), ("d_position", ctypes.c_void_p), ("rotary_dim", ctypes.c_uint32),
+                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+class KVTreeDesc(ctypes.Structure):
+    """splitzip_kv_tree_t."""
+    _fields_ = [("d_mask", ctypes.c_void_p), ("d_position", ctypes.c_void_p), ("words", ctypes.c_uint32),
+                ("window", ctypes.c_uint32)]
+
+
 MAX_BATCH = 256                 # SPLITZIP_MAX_BATCH
 MAX_BATCH_ITEM_ELEMS = 1 << 26  # SPLITZIP_MAX_BATCH_ITEM_ELEMS
+MAX_TREE_TOKENS = 1024          # SPLITZIP_MAX_TREE_TOKENS
+MAX_LAYERS = 256                # SPLITZIP_MAX_LAYERS
 
 
 class _Address(ctypes.c_void_p):
@@ -129,6 +160,7 @@ class _Address(ctypes.c_void_p):
 _u64, _u32, _int, _vp = ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int, _Address
 _P_u64 = ctypes.POINTER(ctypes.c_uint64)
 _P_cache, _P_batch, _P_rows = (ctypes.POINTER(t) for t in (KVCacheDesc, KVBatchDesc, KVRowsDesc))
+_P_pages, _P_step, _P_rotary, _P_tree = (ctypes.POINTER(t) for t in (KVPagesDesc, KVStepDesc, KVRotaryDesc, KVTreeDesc))
 
 # name -> (restype, argtypes); mirrors include/splitzip.h
 SIGNATURES = {
@@ -168,6 +200,14 @@ SIGNATURES = {
     "splitzip_kv_attention_workspace_size": (_int, [_P_cache, _P_batch, _u32, _P_u64]),
     "splitzip_kv_attention": (_int, [_P_cache, _P_batch, _P_rows, _P_rows, _vp, _int, _u32, ctypes.c_float, _int, _u32,
                                      _vp, _u64, _vp, _vp]),
+    "splitzip_kv_extend_workspace_size": (_int, [_u32, _P_u64]),
+    "splitzip_kv_extend": (_int, [_P_pages, _vp, _vp, _P_step, _vp, _u64, _vp, _vp]),
+    "splitzip_kv_rotary_write": (_int, [_P_cache, _P_batch, _P_rotary, _P_rows, _P_rows, _u32, _P_rows, _P_rows, _int,
+                                        _vp, _vp]),
+    "splitzip_kv_tree": (_int, [_P_batch, _vp, _P_tree, _vp, _vp]),
+    "splitzip_kv_tree_attention": (_int, [_P_cache, _P_batch, _P_tree, _P_rows, _P_rows, _vp, _int, _u32, ctypes.c_float,
+                                          _vp, _u64, _vp, _vp]),
+    "splitzip_kv_keep": (_int, [_P_cache, _u32, _P_batch, _vp, _vp, _vp, _vp]),
 }
 
 _lib = None
@@ -328,6 +368,41 @@ def splitzip_kv_attention(cache, batch, q, out, d_lse, dtype, q_heads, scale, ca
                           stream):
     return lib().splitzip_kv_attention(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(q), ctypes.byref(out),
                                        d_lse, dtype, q_heads, scale, causal, window, d_ws, ws_bytes, d_status, stream)
+
+
+def splitzip_kv_extend_workspace_size(batch, out_bytes):
+    return lib().splitzip_kv_extend_workspace_size(batch, ctypes.byref(out_bytes))
+
+
+def splitzip_kv_extend(pages, d_new, d_drop, step, d_ws, ws_bytes, d_status, stream):
+    """pages, step: KVPagesDesc, KVStepDesc."""
+    return lib().splitzip_kv_extend(ctypes.byref(pages), d_new, d_drop, ctypes.byref(step), d_ws, ws_bytes, d_status,
+                                    stream)
+
+
+def splitzip_kv_rotary_write(cache, batch, rotary, q, q_out, q_heads, k, v, dtype, d_status, stream):
+    """rotary: KVRotaryDesc; q, q_out: KVRowsDesc, or both None."""
+    return lib().splitzip_kv_rotary_write(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(rotary),
+                                          None if q is None else ctypes.byref(q),
+                                          None if q_out is None else ctypes.byref(q_out), q_heads, ctypes.byref(k),
+                                          ctypes.byref(v), dtype, d_status, stream)
+
+
+def splitzip_kv_tree(batch, d_parent, tree, d_status, stream):
+    """tree: KVTreeDesc."""
+    return lib().splitzip_kv_tree(ctypes.byref(batch), d_parent, ctypes.byref(tree), d_status, stream)
+
+
+def splitzip_kv_tree_attention(cache, batch, tree, q, out, d_lse, dtype, q_heads, scale, d_ws, ws_bytes, d_status,
+                               stream):
+    return lib().splitzip_kv_tree_attention(ctypes.byref(cache), ctypes.byref(batch), ctypes.byref(tree), ctypes.byref(q),
+                                            ctypes.byref(out), d_lse, dtype, q_heads, scale, d_ws, ws_bytes, d_status,
+                                            stream)
+
+
+def splitzip_kv_keep(h_caches, count, batch, d_path, d_kept, d_status, stream):
+    """h_caches: ctypes array of KVCacheDesc."""
+    return lib().splitzip_kv_keep(h_caches, count, ctypes.byref(batch), d_path, d_kept, d_status, stream)
 
 
 # ------------------------------------------------------------ size helpers
@@ -824,3 +899,252 @@ def kv_attention(cache, batch, q, out, bufs, scale, causal=True, window=0, lse=N
     _check(splitzip_kv_attention(cache.desc, batch.desc, rq, ro, lse, dtype, bufs.q_heads, scale, int(causal), window,
                                  bufs.ws.data_ptr(), bufs.ws_bytes, bufs.status.data_ptr(), _kv_stream(stream, device)),
            "splitzip_kv_attention")
+
+
+# a step around the paged cache (see splitzip_kv_extend, splitzip_kv_rotary_write, splitzip_kv_tree,
+# splitzip_kv_tree_attention, splitzip_kv_keep)
+
+def _int32(t, shape, what, device):
+    """A contiguous int32 tensor of `shape` on cuda:`device`."""
+    _device_tensor(t, _torch().int32, shape, what, device)
+    if not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous tensor" % what)
+    return t
+
+
+class KVPages:
+    """The pages of one pool, the same for every layer's cache, and the
+    sequences that hold them (splitzip_kv_pages_t): int32 device tensors free
+    (one entry for each page of the pool), count (1), table (batch, pages), held
+    (batch) and kv_len (batch)."""
+
+    def __init__(self, free, count, table, held, kv_len, page_tokens):
+        batch = kv_len.numel()
+        if not free.is_cuda:
+            raise ValueError("free: expected a CUDA tensor, got one on %s" % free.device)
+        self.device = free.get_device()
+        _int32(free, (free.numel(),), "free", self.device)
+        _int32(count, (1,), "count", self.device)
+        if table.dim() != 2 or table.stride(1) != 1:
+            raise ValueError("table: expected (batch, pages) with a contiguous last axis")
+        if batch > 1 and table.stride(0) < table.shape[1]:
+            raise ValueError("table: expected rows that do not overlap")
+        _device_tensor(table, _torch().int32, (batch, table.shape[1]), "table", self.device)
+        _int32(held, (batch,), "held", self.device)
+        _int32(kv_len, (batch,), "kv_len", self.device)
+        self.free, self.count, self.table, self.held, self.kv_len = free, count, table, held, kv_len
+        self.page_tokens = page_tokens
+        self.desc = KVPagesDesc(free.data_ptr(), count.data_ptr(), held.data_ptr(), kv_len.data_ptr(), table.data_ptr(),
+                                max(table.stride(0), table.shape[1]), table.shape[1], free.numel(), page_tokens, batch)
+
+    @classmethod
+    def empty(cls, pool_pages, page_tokens, batch, max_kv_len, device="cuda"):
+        """All pages free, `batch` sequences of no tokens that may grow to max_kv_len."""
+        torch = _torch()
+        zeros = lambda *s: torch.zeros(*s, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(torch.arange(pool_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.full((1,), pool_pages, dtype=torch.int32, device=device),
+                   zeros(batch, -(-max_kv_len // page_tokens)), zeros(batch), zeros(batch), page_tokens)
+
+    def ahead(self):
+        """The same list and tables with a count, held pages and lengths of their
+        own: where kv_extend leaves the next step's while this one's are in use."""
+        return KVPages(self.free, self.count.clone(), self.table, self.held.clone(), self.kv_len.clone(),
+                       self.page_tokens)
+
+
+class KVStep:
+    """What kv_extend makes for a step of at most `tokens` new tokens, max_tokens
+    of one sequence: device tensors cu_tokens (int32, batch + 1), position (int32,
+    tokens) and slot (int64, tokens), the status word and the workspace."""
+
+    def __init__(self, batch, tokens, max_tokens, max_kv_len, device="cuda"):
+        torch = _torch()
+        ints = lambda *s: torch.zeros(*s, dtype=torch.int32, device=device)  # noqa: E731
+        self.batch, self.tokens, self.max_tokens, self.max_kv_len = batch, tokens, max_tokens, max_kv_len
+        self.cu_tokens, self.position, self.status = ints(batch + 1), ints(tokens), ints(4)
+        self.slot = torch.zeros(tokens, dtype=torch.int64, device=device)
+        self.ws_bytes = _size_call(splitzip_kv_extend_workspace_size, batch)
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.device = self.cu_tokens.get_device()
+
+    def batch_of(self, pages):
+        """The KVBatch of this step over `pages`, as kv_extend left them."""
+        return KVBatch(self.cu_tokens, pages.kv_len, pages.table, self.tokens, self.max_tokens, self.max_kv_len)
+
+
+def kv_extend(pages, new, step, drop=None, after=None, stream=None):
+    """Enqueue the page tables and lengths of a step (asynchronous): sequence b
+    gives up drop[b] tokens, then takes new[b] more (int32 device tensors).  after:
+    KVPages of the same list and tables that receive count, held pages and
+    lengths (None: pages itself).  Nothing changes, and cu_tokens is all zeros,
+    where step.status says so."""
+    device, batch = pages.device, pages.kv_len.numel()
+    after = pages if after is None else after
+    if step.device != device or after.device != device:
+        raise ValueError("pages, step and after: expected one device")
+    if step.batch != batch or after.kv_len.numel() != batch or after.free is not pages.free or \
+            after.table is not pages.table:
+        raise ValueError("step and after: expected those of %d sequences and of the same list and tables" % batch)
+    _int32(new, (batch,), "new", device)
+    if drop is not None:
+        _int32(drop, (batch,), "drop", device)
+    to = after.desc
+    _check(splitzip_kv_extend(pages.desc, new.data_ptr(), None if drop is None else drop.data_ptr(),
+                              KVStepDesc(to.d_free_count, to.d_held, to.d_kv_len, step.cu_tokens.data_ptr(),
+                                         step.position.data_ptr(), step.slot.data_ptr(), step.tokens, step.max_tokens,
+                                         step.max_kv_len),
+                              step.ws.data_ptr(), step.ws_bytes, step.status.data_ptr(), _kv_stream(stream, device)),
+           "splitzip_kv_extend")
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, factor=1.0, original_len=0, turns=(1.0, 32.0)):
+    """Radians a position of each pair (float64, rotary_dim / 2): base^(-2j /
+    rotary_dim).  factor: how far the context is stretched.  Without original_len
+    every pair is slowed by it; with it, pairs that make at most turns[0] turns
+    over the original length are, those of turns[1] and more stay as they are, and
+    a part of the way between the two is taken in proportion."""
+    torch = _torch()
+    j = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    f = torch.tensor([float(base) ** (-x / rotary_dim) for x in j.tolist()], dtype=torch.float64)
+    stay = torch.zeros_like(f)
+    if original_len:
+        made = original_len * f / 6.283185307179586
+        stay = ((made - turns[0]) / (turns[1] - turns[0])).clamp(0, 1)
+    return f * (stay + (1 - stay) / factor)
+
+
+class KVRotary:
+    """Rotary positions (splitzip_kv_rotary_t).  frequencies: radians a position of
+    each pair, float64 on the CPU (rotary_frequencies, or any); interleaved: pairs
+    of neighbouring elements, else of the two halves of the first 2 *
+    len(frequencies) elements; magnitude: a factor on what is rotated."""
+
+    def __init__(self, frequencies, interleaved=False, magnitude=1.0, device="cuda"):
+        torch = _torch()
+        f = frequencies.detach().to("cpu", torch.float64)
+        if f.dim() != 1 or f.numel() == 0 or f.numel() % 8 or not bool(torch.isfinite(f).all()):
+            raise ValueError("frequencies: expected finite ones, a multiple of 8 of them")
+        # turns a position as a fraction of 2^64, without its whole turns
+        turns = [(round(x / 6.283185307179586 * 2.0 ** 64) & (1 << 64) - 1) for x in f.tolist()]
+        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.rotary_dim, self.interleaved, self.magnitude = 2 * f.numel(), bool(interleaved), float(magnitude)
+        self.device = self.turns.get_device()
+        self.desc = KVRotaryDesc(self.turns.data_ptr(), None, self.rotary_dim, int(self.interleaved), self.magnitude)
+
+
+def kv_rotary_write(cache, batch, rotary, q, q_out, k, v, status, positions=None, stream=None):
+    """Enqueue the rotation of the new tokens' queries q into q_out (packed (tokens,
+    q_heads, head_dim); q_out may be q, both may be None) and of their keys k, and
+    the write of the rotated keys and of the values v into `cache`'s pages
+    (asynchronous; status: device int32, as for kv_write).  positions: int32
+    (tokens), None: the tokens' places in the cache."""
+    d, heads, dim, device = cache.desc, cache.kv_heads, cache.head_dim, cache.device
+    batch.check(cache)
+    if rotary.device != device:
+        raise ValueError("rotary: expected frequencies on cuda:%d, got cuda:%d" % (device, rotary.device))
+    rk, dtype = _kv_rows(k, batch.tokens, heads, dim, device, "k")
+    rv, dtype_v = _kv_rows(v, batch.tokens, heads, dim, device, "v")
+    rq = ro = None
+    q_heads, types = 0, {dtype, dtype_v}
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: expected both or neither")
+    if q is not None:
+        q_heads = q.shape[1] if q.dim() == 3 else 0
+        rq, dtype_q = _kv_rows(q, batch.tokens, q_heads, dim, device, "q")
+        ro, dtype_o = _kv_rows(q_out, batch.tokens, q_heads, dim, device, "q_out")
+        types |= {dtype_q, dtype_o}
+    if len(types) > 1:
+        raise TypeError("q, q_out, k and v: expected the same type")
+    turn = rotary.desc
+    if positions is not None:
+        _int32(positions, (batch.tokens,), "positions", device)
+        turn = KVRotaryDesc(turn.d_turns, positions.data_ptr(), turn.rotary_dim, turn.interleaved, turn.magnitude)
+    _check(splitzip_kv_rotary_write(d, batch.desc, turn, rq, ro, q_heads, rk, rv, dtype, _kv_status(status, device),
+                                    _kv_stream(stream, device)), "splitzip_kv_rotary_write")
+
+
+class KVTree:
+    """Masks and positions of a step's trees of drafted tokens (splitzip_kv_tree_t),
+    the same for every layer: device tensors mask (int32 (tokens, words), 32 new
+    tokens of the row's sequence a word) and position (int32, tokens), and kv_tree's
+    status word.  window: how many positions a row sees up to its own, 0: all."""
+
+    def __init__(self, batch, window=0):
+        torch = _torch()
+        if not 0 <= window < 1 << 32:
+            raise ValueError("window: expected 0 (none) or a number of positions, got %d" % window)
+        device = batch.kv_len.device
+        self.tokens, self.max_tokens, self.device, self.window = batch.tokens, batch.desc.max_tokens, batch.device, window
+        self.words = max(1, -(-self.max_tokens // 32))
+        if self.max_tokens > MAX_TREE_TOKENS:
+            raise SplitZipError(ERR_UNSUPPORTED, "trees of %d tokens" % self.max_tokens)
+        self.mask = torch.zeros(self.tokens, self.words, dtype=torch.int32, device=device)
+        self.position = torch.zeros(self.tokens, dtype=torch.int32, device=device)
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)  # [0] = status
+        self.desc = KVTreeDesc(self.mask.data_ptr(), self.position.data_ptr(), self.words, window)
+
+    def check(self, batch):
+        """Raises where the tree is of another step."""
+        if self.device != batch.device:
+            raise ValueError("tree on cuda:%d and step on cuda:%d: expected one device" % (self.device, batch.device))
+        if self.tokens != batch.tokens or self.max_tokens < batch.desc.max_tokens:
+            raise ValueError("tree of %d rows, %d of a sequence: expected one of the step's %d and %d"
+                             % (self.tokens, self.max_tokens, batch.tokens, batch.desc.max_tokens))
+
+
+def kv_tree(batch, parents, tree, stream=None):
+    """Enqueue masks and positions of a step's trees into `tree` (asynchronous).
+    parents: int32 (tokens): a new token's parent among its sequence's new tokens,
+    smaller than its own number, -1 for a successor of the last older token."""
+    tree.check(batch)
+    _int32(parents, (batch.tokens,), "parents", batch.device)
+    _check(splitzip_kv_tree(batch.desc, parents.data_ptr(), tree.desc, tree.status.data_ptr(),
+                            _kv_stream(stream, batch.device)), "splitzip_kv_tree")
+
+
+def kv_tree_attention(cache, batch, tree, q, out, bufs, scale, lse=None, stream=None):
+    """Enqueue the attention of trees of drafted tokens over `cache`'s pages: every
+    row sees what was there before its tree, its ancestors and itself
+    (asynchronous; arguments as kv_attention's)."""
+    batch.check(cache)
+    tree.check(batch)
+    device = cache.device
+    if bufs.device != device:
+        raise ValueError("bufs: expected buffers on cuda:%d, got cuda:%d" % (device, bufs.device))
+    rq, dtype = _kv_rows(q, batch.tokens, bufs.q_heads, cache.head_dim, device, "q")
+    ro, dtype_o = _kv_rows(out, batch.tokens, bufs.q_heads, cache.head_dim, device, "out")
+    if dtype != dtype_o:
+        raise TypeError("q and out: expected the same type")
+    if lse is not None:
+        if not lse.is_contiguous():
+            raise ValueError("lse: expected a contiguous tensor")
+        _device_tensor(lse, _torch().float32, (batch.tokens, bufs.q_heads), "lse", device)
+        lse = lse.data_ptr()
+    _check(splitzip_kv_tree_attention(cache.desc, batch.desc, tree.desc, rq, ro, lse, dtype, bufs.q_heads, scale,
+                                      bufs.ws.data_ptr(), bufs.ws_bytes, bufs.status.data_ptr(),
+                                      _kv_stream(stream, device)), "splitzip_kv_tree_attention")
+
+
+class KVLayers:
+    """The caches of a model's layers, of one geometry, for kv_keep."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches or any(c.device != self.caches[0].device for c in self.caches):
+            raise ValueError("caches: expected some, on one device")
+        self.descs = (KVCacheDesc * len(self.caches))(*[c.desc for c in self.caches])
+
+
+def kv_keep(layers, batch, path, kept, status, stream=None):
+    """Enqueue the move of the accepted new tokens to the front of them in every
+    layer's pages (asynchronous): new token path[cu_tokens[b] + i] of sequence b to
+    the place of new token i, for i < kept[b].  path: int32 (tokens), ascending in
+    each sequence; kept: int32 (batch).  kv_extend drops the others."""
+    cache = layers.caches[0]
+    device = cache.device
+    batch.check(cache)
+    _int32(path, (batch.tokens,), "path", device)
+    _int32(kept, (batch.desc.batch,), "kept", device)
+    _check(splitzip_kv_keep(layers.descs, len(layers.caches), batch.desc, path.data_ptr(), kept.data_ptr(),
+                            _kv_status(status, device), _kv_stream(stream, device)), "splitzip_kv_keep")

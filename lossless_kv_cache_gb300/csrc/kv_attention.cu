@@ -1,4 +1,4 @@
-// Host side of splitzip_kv_attention: argument checks, workspace, and which
+// Host side of splitzip_kv_attention and splitzip_kv_tree_attention: argument checks, workspace, and which
 // kernel a step takes.
 #include <algorithm>
 #include <cmath>
@@ -76,14 +76,28 @@ extern "C" int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* c
     return SPLITZIP_OK;
 }
 
-extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
-                                     const splitzip_kv_rows_t* q, const splitzip_kv_rows_t* out, float* d_lse,
-                                     int dtype, uint32_t q_heads, float scale, int causal, uint32_t window,
-                                     void* d_ws, uint64_t ws_bytes, int* d_status, cudaStream_t stream) {
+namespace {
+
+// splitzip_kv_attention, and with a tree splitzip_kv_tree_attention.
+int attend(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch, const splitzip_kv_tree_t* tree,
+           bool is_tree, const splitzip_kv_rows_t* q, const splitzip_kv_rows_t* out, float* d_lse, int dtype,
+           uint32_t q_heads, float scale, int causal, uint32_t window, void* d_ws, uint64_t ws_bytes, int* d_status,
+           cudaStream_t stream) {
     AttentionArgs a;
     Plan p;
     int st = check_kv(cache, batch, &a.c, &a.b, true);
     if (st != SPLITZIP_OK) return st;
+    a.mask = nullptr;
+    a.position = nullptr;
+    a.words = 0;
+    if (is_tree) {
+        if (a.b.max_tokens > SPLITZIP_MAX_TREE_TOKENS) return SPLITZIP_ERR_UNSUPPORTED;
+        if ((st = check_tree(tree, a.b)) != SPLITZIP_OK) return st;
+        a.mask = tree->d_mask;
+        a.position = tree->d_position;
+        a.words = tree->words;
+        window = tree->window;
+    }
     if ((st = plan_for(a.c, a.b, q_heads, &p)) != SPLITZIP_OK) return st;
     if (!kv_dtype_fits(a.c.type, dtype) || !std::isfinite(scale)) return SPLITZIP_ERR_INVALID_ARG;
     if ((st = check_rows(q, a.b, q_heads, a.c.head_dim, &a.q)) != SPLITZIP_OK) return st;
@@ -112,11 +126,32 @@ extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const spl
     int sms;
     if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
     if (p.chunk && a.b.tokens > 0)
-        return launch_kv_chunk(a, a.q_half != 0, static_cast<uint8_t*>(d_ws) + p.plan_off, p.ctas, stream);
+        return (is_tree ? launch_kv_tree_chunk : launch_kv_chunk)(
+            a, a.q_half != 0, static_cast<uint8_t*>(d_ws) + p.plan_off, p.ctas, stream);
     // the step kernel looks at all sequences itself, to share out their units
     if (launch_kv_begin(a.b.tokens > 0 ? KvBatch{} : a.b, d_status, a.counters, p.ctas, stream) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }
-    return a.b.tokens > 0 ? launch_kv_step(a, p.ctas, stream) : int(SPLITZIP_OK);
+    if (a.b.tokens == 0) return SPLITZIP_OK;
+    return (is_tree ? launch_kv_tree_step : launch_kv_step)(a, p.ctas, stream);
+}
+
+}  // namespace
+
+extern "C" int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                                     const splitzip_kv_rows_t* q, const splitzip_kv_rows_t* out, float* d_lse,
+                                     int dtype, uint32_t q_heads, float scale, int causal, uint32_t window,
+                                     void* d_ws, uint64_t ws_bytes, int* d_status, cudaStream_t stream) {
+    return attend(cache, batch, nullptr, false, q, out, d_lse, dtype, q_heads, scale, causal, window, d_ws, ws_bytes,
+                  d_status, stream);
+}
+
+extern "C" int splitzip_kv_tree_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
+                                          const splitzip_kv_tree_t* tree, const splitzip_kv_rows_t* q,
+                                          const splitzip_kv_rows_t* out, float* d_lse, int dtype, uint32_t q_heads,
+                                          float scale, void* d_ws, uint64_t ws_bytes, int* d_status,
+                                          cudaStream_t stream) {
+    return attend(cache, batch, tree, true, q, out, d_lse, dtype, q_heads, scale, 1, 0, d_ws, ws_bytes, d_status,
+                  stream);
 }

@@ -1,5 +1,5 @@
-// Attention over a paged cache: what its two kernels share (kv_step.cu for
-// few rows a sequence, kv_chunk.cu for chunks).
+// Attention over a paged cache: what its two kernels share (kv_step.cuh for
+// few rows a sequence, kv_chunk.cuh for chunks).
 //
 // Work is cut the same way in both.  An item is one (sequence, kv head, tile
 // of rows), rows being (new token, query head of the group) pairs in token
@@ -32,30 +32,66 @@ struct AttentionArgs {
     float lag;  // chunk kernel: how far the reference may lag the maximum, before the scale
     int causal;
     uint32_t window;
+    // a tree's (else null): which new tokens each row sees, `words` words a row, and its position
+    const uint32_t* mask;
+    const int32_t* position;
+    uint32_t words;
     uint32_t* counters;  // workspace, one a CTA (step kernel)
     float* parts;        // workspace, two slots a CTA
     int* status;
 };
 
-// The positions that some row of a sequence's rows first .. last (new tokens
-// i0 .. i1) sees: [lo, hi).
+// Positions [lo, hi).
 struct KeyRange {
     int lo, hi;
 };
 
+// What new token i of a sequence sees.  TREE: a range that holds it.
+template <bool TREE>
 __device__ __forceinline__ KeyRange visible(const AttentionArgs& a, const KvSeq& s, int i) {
-    const int p = s.n - s.t + i;
+    const int p = s.n - s.t + (TREE ? 0 : i);
     KeyRange r;
+    if (TREE) {
+        r.hi = s.n - s.t + i < 0 ? 0 : s.n;
+        r.lo = a.window ? max(0, p + 1 - int(a.window)) : 0;
+        return r;
+    }
     r.hi = p < 0 ? 0 : (a.causal ? p + 1 : s.n);
     r.lo = a.window && p >= 0 ? max(0, p + 1 - int(a.window)) : 0;
     return r;
 }
 
+// What some of new tokens i0 .. i1 sees.
+template <bool TREE>
 __device__ __forceinline__ KeyRange visible(const AttentionArgs& a, const KvSeq& s, int i0, int i1) {
     KeyRange r;
-    r.hi = visible(a, s, i1).hi;
-    r.lo = visible(a, s, max(i0, s.t - s.n)).lo;  // the first row with a place
+    r.hi = visible<TREE>(a, s, i1).hi;
+    r.lo = visible<TREE>(a, s, max(i0, s.t - s.n)).lo;  // the first row with a place
     return r;
+}
+
+// Of a tree, the positions before the sequence's new tokens that new token i
+// sees.
+__device__ __forceinline__ KeyRange visible_before(const AttentionArgs& a, const KvSeq& s, int i) {
+    const int first = s.n - s.t;
+    KeyRange r{0, max(first, 0)};
+    if (first + i < 0) r.hi = 0;
+    // positions are the caller's: they count as ones that a tree can give that token
+    if (a.window) r.lo = max(0, min(max(a.position[s.row0 + i], first), first + i) - int(a.window) + 1);
+    return r;
+}
+
+// Of a tree, positions that every new token up to i1 sees.
+__device__ __forceinline__ KeyRange visible_to_all_before(const AttentionArgs& a, const KvSeq& s, int i1) {
+    const int first = s.n - s.t;
+    return KeyRange{a.window ? max(0, first + i1 - int(a.window) + 1) : 0, max(first, 0)};
+}
+
+// Bits at .. at + 31 of a row of a tree's mask; at may be negative.
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, uint32_t words, int at) {
+    const int w = at >> 5;
+    const uint32_t lo = w >= 0 && w < int(words) ? row[w] : 0u, hi = w + 1 >= 0 && w + 1 < int(words) ? row[w + 1] : 0u;
+    return __funnelshift_r(lo, hi, uint32_t(at) & 31u);
 }
 
 // Units that the range covers; one for a range of none, so that its rows are
@@ -77,16 +113,23 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// kv_step.cu
+// kv_step.cuh, kv_step.cu
 constexpr int kStepRows = 16;  // rows of a tile at most
 uint32_t step_ctas(uint64_t items_max, uint64_t keys_max);
 uint64_t step_part_floats(uint32_t head_dim);
 int launch_kv_step(const AttentionArgs& a, uint32_t ctas, cudaStream_t s);
 
-// kv_chunk.cu
+// kv_chunk.cuh, kv_chunk.cu
 uint32_t chunk_ctas(uint64_t rows, uint64_t batch, uint64_t kv_heads, uint64_t keys_max);
 uint64_t chunk_part_floats(uint32_t head_dim);
 uint64_t chunk_plan_bytes(uint32_t ctas);
 int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s);
+
+// The same with a tree's masks (kv_tree_step.cu, kv_tree_chunk.cu).
+int launch_kv_tree_step(const AttentionArgs& a, uint32_t ctas, cudaStream_t s);
+int launch_kv_tree_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s);
+
+// kv_tree.cu
+int check_tree(const splitzip_kv_tree_t* tree, const KvBatch& b);
 
 }  // namespace splitzip

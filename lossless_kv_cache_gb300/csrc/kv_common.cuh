@@ -1,5 +1,4 @@
-// Shared by the paged-cache operators (kv_rw.cu, kv_attention.cu, kv_step.cu,
-// kv_chunk.cu): their kernel arguments, how a packed row finds its place in
+// Shared by the paged-cache operators (kv_*.cu): their kernel arguments, how a packed row finds its place in
 // the pages, and conversions of the FP8 types.
 #pragma once
 
@@ -109,6 +108,17 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return r;
 }
 
+// Two 16-bit elements (FP16 with H, else BF16) as floats, and back.
+template <bool H>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+    return H ? half2_to_float2(w) : bf16x2_to_float2(w);
+}
+
+template <bool H>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    return H ? pack_half2(a, b) : pack_bf16x2(a, b);
+}
+
 // Two 32-bit operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 r;
@@ -144,8 +154,57 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 __device__ __forceinline__ void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void release_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// The last sequence b with cu[b] <= row, 32 candidates a step; every lane gets
+// the same answer (-1: none).  Where cu descends it may be one that row is not
+// of, on either side.
+__device__ __forceinline__ int find_seq(const KvBatch& B, int row, uint32_t lane) {
+    int lo = 0, n = int(B.batch);
+    while (true) {
+        const int step = (n + 31) / 32;
+        const int i = lo + int(lane) * step;
+        const bool le = i < lo + n && B.cu[i] <= row;
+        const int found = __popc(__ballot_sync(~0u, le));
+        if (found == 0) return -1;
+        n = min(step, n - (found - 1) * step);
+        lo += (found - 1) * step;
+        if (step == 1) return lo;
+    }
+}
+
+// Where a packed row's token lies in the cache; the same in all lanes of a warp.
+struct KvPlace {
+    bool mine;    // the row is of a sequence
+    bool bad;     // whose entries, or the page, are out of range
+    bool placed;  // and has a place
+    int pos;      // negative where it has none
+    uint64_t page;
+    uint32_t slot;
+};
+
+__device__ __forceinline__ KvPlace find_place(const KvCache& C, const KvBatch& B, int row, uint32_t lane) {
+    KvPlace p{false, false, false, 0, 0, 0};
+    const int b = find_seq(B, row, lane);
+    if (b < 0) return p;
+    const int c1 = B.cu[b + 1];
+    p.mine = B.cu[b] <= row && row < c1;
+    if (!p.mine) return p;
+    const KvSeq s = load_seq(B, uint32_t(b));
+    p.bad = !s.ok;
+    p.pos = s.n - (c1 - row);
+    if (s.ok && p.pos >= 0) {
+        const int32_t pg = B.table[uint64_t(b) * B.table_stride + (uint32_t(p.pos) >> C.page_shift)];
+        p.placed = pg >= 0 && uint64_t(pg) < C.pool_pages;
+        p.bad = !p.placed;
+        p.page = uint64_t(uint32_t(pg));
+        p.slot = uint32_t(p.pos) & ((1u << C.page_shift) - 1u);
+    }
+    return p;
+}
+
 // Host side (kv_rw.cu): argument checks shared by the entry points.
 int check_kv(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch, KvCache* c, KvBatch* b, bool need_ptrs);
+// The batch's part of check_kv, without its page table.
+int check_batch(const splitzip_kv_batch_t* batch, KvBatch* b, bool need_ptrs);
 int check_rows(const splitzip_kv_rows_t* r, const KvBatch& b, uint32_t heads, uint32_t head_dim, KvRows* out);
 // Whether rows of `dtype` go with a cache of `type`.
 bool kv_dtype_fits(int type, int dtype);

@@ -40,40 +40,12 @@ __global__ void __launch_bounds__(kBeginThreads)
     if (threadIdx.x == 0) *status = bad ? SPLITZIP_ERR_INVALID_ARG : SPLITZIP_OK;
 }
 
-// The last sequence b with cu[b] <= row, 32 candidates a step; every lane gets
-// the same answer (-1: none).  Where cu descends it may be one that row is not
-// of, on either side.
-__device__ __forceinline__ int find_seq(const KvBatch& B, int row, uint32_t lane) {
-    int lo = 0, n = int(B.batch);
-    while (true) {
-        const int step = (n + 31) / 32;
-        const int i = lo + int(lane) * step;
-        const bool le = i < lo + n && B.cu[i] <= row;
-        const int found = __popc(__ballot_sync(~0u, le));
-        if (found == 0) return -1;
-        n = min(step, n - (found - 1) * step);
-        lo += (found - 1) * step;
-        if (step == 1) return lo;
-    }
-}
-
 struct RwArgs {
     KvCache c;
     KvBatch b;
     KvRows k, v;
     int* status;
 };
-
-// One element's 16 bits as a float, and back.
-template <bool H>
-__device__ __forceinline__ float2 unpack16(uint32_t w) {
-    return H ? half2_to_float2(w) : bf16x2_to_float2(w);
-}
-
-template <bool H>
-__device__ __forceinline__ uint32_t pack16(float a, float b) {
-    return H ? pack_half2(a, b) : pack_bf16x2(a, b);
-}
 
 // Sixteen elements of a row, quantised; LPR lanes hold the row.  Whole warp.
 template <bool E5M2, bool H, int LPR>
@@ -160,26 +132,11 @@ __global__ void __launch_bounds__(kRwWarps * 32) kv_rw_kernel(const __grid_const
                 }
             }
         }
-        const int b = find_seq(a.b, int(token), lane);
-        bool mine = b >= 0, placed = false;
-        uint64_t page = 0;
-        uint32_t slot = 0;
-        if (mine) {
-            const int c1 = a.b.cu[b + 1];
-            mine = a.b.cu[b] <= int(token) && int(token) < c1;
-            if (mine) {
-                const KvSeq s = load_seq(a.b, uint32_t(b));
-                bad = !s.ok;
-                const int pos = s.n - (c1 - int(token));
-                if (s.ok && pos >= 0) {
-                    const int32_t pg = a.b.table[uint64_t(b) * a.b.table_stride + (uint32_t(pos) >> a.c.page_shift)];
-                    placed = pg >= 0 && uint64_t(pg) < a.c.pool_pages;
-                    bad = !placed;
-                    page = uint64_t(uint32_t(pg));
-                    slot = uint32_t(pos) & ((1u << a.c.page_shift) - 1u);
-                }
-            }
-        }
+        const KvPlace at_place = find_place(a.c, a.b, int(token), lane);
+        const bool mine = at_place.mine, placed = at_place.placed;
+        const uint64_t page = at_place.page;
+        const uint32_t slot = at_place.slot;
+        bad = at_place.bad;
         // the same in all lanes
         if (mine && !bad && (placed || !WRITE)) {
             const uint64_t at = page * a.c.page_stride + uint64_t(slot) * a.c.token_stride + head * a.c.head_stride +
@@ -290,6 +247,25 @@ bool kv_dtype_fits(int type, int dtype) {
     return true;
 }
 
+int check_batch(const splitzip_kv_batch_t* batch, KvBatch* b, bool need_ptrs) {
+    if (!batch) return SPLITZIP_ERR_INVALID_ARG;
+    if (need_ptrs && (!batch->d_cu_tokens || !batch->d_kv_len || (reinterpret_cast<uintptr_t>(batch->d_cu_tokens) & 3u) ||
+                      (reinterpret_cast<uintptr_t>(batch->d_kv_len) & 3u)))
+        return SPLITZIP_ERR_INVALID_ARG;
+    if (batch->batch == 0 || batch->max_tokens > batch->tokens) return SPLITZIP_ERR_INVALID_ARG;
+    if (batch->batch > 65536u || batch->tokens >= (1u << 30) || batch->max_kv_len >= (1u << 30))
+        return SPLITZIP_ERR_UNSUPPORTED;
+    b->cu = batch->d_cu_tokens;
+    b->kv_len = batch->d_kv_len;
+    b->table = batch->d_page_table;
+    b->table_stride = batch->table_stride;
+    b->batch = batch->batch;
+    b->tokens = batch->tokens;
+    b->max_tokens = batch->max_tokens;
+    b->max_kv_len = batch->max_kv_len;
+    return SPLITZIP_OK;
+}
+
 int check_kv(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch, KvCache* c, KvBatch* b,
              bool need_ptrs) {
     if (!cache || !batch) return SPLITZIP_ERR_INVALID_ARG;
@@ -315,13 +291,11 @@ int check_kv(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
         if (!cache->d_k || !cache->d_v || (addr(cache->d_k) & 15u) || (addr(cache->d_v) & 15u))
             return SPLITZIP_ERR_INVALID_ARG;
         if (fp8 && (!cache->d_k_scale || !cache->d_v_scale)) return SPLITZIP_ERR_INVALID_ARG;
-        if (!batch->d_cu_tokens || !batch->d_kv_len || (!batch->d_page_table && batch->max_kv_len > 0) ||
-            (addr(batch->d_cu_tokens) & 3u) || (addr(batch->d_kv_len) & 3u) || (addr(batch->d_page_table) & 3u))
+        if ((!batch->d_page_table && batch->max_kv_len > 0) || (addr(batch->d_page_table) & 3u))
             return SPLITZIP_ERR_INVALID_ARG;
     }
-    if (batch->batch == 0 || batch->max_tokens > batch->tokens) return SPLITZIP_ERR_INVALID_ARG;
-    if (batch->batch > 65536u || batch->tokens >= (1u << 30) || batch->max_kv_len >= (1u << 30))
-        return SPLITZIP_ERR_UNSUPPORTED;
+    const int st = check_batch(batch, b, need_ptrs);
+    if (st != SPLITZIP_OK) return st;
     uint32_t shift = 0;
     while ((1u << shift) < pt) ++shift;
     if (batch->table_stride < (uint64_t(batch->max_kv_len) + pt - 1u) >> shift ||
@@ -339,14 +313,6 @@ int check_kv(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
     c->kv_heads = cache->kv_heads;
     c->head_dim = cache->head_dim;
     c->type = cache->type;
-    b->cu = batch->d_cu_tokens;
-    b->kv_len = batch->d_kv_len;
-    b->table = batch->d_page_table;
-    b->table_stride = batch->table_stride;
-    b->batch = batch->batch;
-    b->tokens = batch->tokens;
-    b->max_tokens = batch->max_tokens;
-    b->max_kv_len = batch->max_kv_len;
     return SPLITZIP_OK;
 }
 
