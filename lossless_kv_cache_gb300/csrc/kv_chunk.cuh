@@ -992,6 +992,7 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
                     // is issued after group 0's
                     if (g == 1) mbar_arrive(&sh.noted);
                     if (g == 0 && w.rows > kTileRows && ok) ok = mbar_wait(&sh.noted, noted++ & 1u);
+                    if (g == 0) ok = named_barrier_and(2, 128, ok);  // nor does a warp of group 0 still look for them
                     if (g == 0 && ok) {
                         for (int k = 0; k < C::kTileBytes / 512; ++k) {
                             uint32_t* at = reinterpret_cast<uint32_t*>(v) + uint32_t(k) * 128u + row;
