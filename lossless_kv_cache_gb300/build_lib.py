@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "splitzip")
 LIB = os.path.join(PKG, "libsplitzip.so")
 SOURCES = ["capi.cu", "encode.cu", "decode.cu", "histogram.cu", "encode_noalloc.cu", "transfer.cu", "ablation.cu", "selftest.cu", "merge.cu", "batch.cu", "kv_rw.cu",
-           "kv_attention.cu", "kv_step.cu", "kv_chunk.cu", "kv_tree_step.cu", "kv_tree_chunk.cu", "kv_tree.cu",
+           "kv_attention.cu", "kv_step.cu", "kv_chunk.cu", "kv_tree_step.cu", "kv_tree_chunk.cu", "kv_tree_tile.cu", "kv_tree.cu",
            "kv_extend.cu", "kv_rotary.cu", "kv_keep.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall", "--expt-relaxed-constexpr"]

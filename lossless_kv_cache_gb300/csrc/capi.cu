@@ -196,7 +196,7 @@ int make_input_map(const void* d_in, int dtype, EncodeArgs* a, CUtensorMap* map,
 }  // namespace
 
 bool splitzip::make_rows_map(void* base, uint32_t rank, const uint64_t* dims, const uint64_t* strides,
-                             const uint32_t* box, CUtensorMap* map) {
+                             const uint32_t* box, CUtensorMap* map, bool bytes) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode || rank < 2 || rank > 5) return false;
     cuuint64_t d[5], st[4];
@@ -207,9 +207,9 @@ bool splitzip::make_rows_map(void* base, uint32_t rank, const uint64_t* dims, co
         ones[i] = 1;
         if (i + 1 < rank) st[i] = strides[i];
     }
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, base, d, st, b, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, base, d, st, b,
+                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int splitzip::device_sms(int* sms) {

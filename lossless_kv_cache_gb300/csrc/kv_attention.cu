@@ -125,9 +125,11 @@ int attend(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch, c
     a.status = d_status;
     int sms;
     if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
-    if (p.chunk && a.b.tokens > 0)
-        return (is_tree ? launch_kv_tree_chunk : launch_kv_chunk)(
+    if (p.chunk && a.b.tokens > 0) {
+        const bool tile = uint64_t(a.b.max_tokens) * p.group <= kTreeTileRows;
+        return (!is_tree ? launch_kv_chunk : tile ? launch_kv_tree_tile : launch_kv_tree_chunk)(
             a, a.q_half != 0, static_cast<uint8_t*>(d_ws) + p.plan_off, p.ctas, stream);
+    }
     // the step kernel looks at all sequences itself, to share out their units
     if (launch_kv_begin(a.b.tokens > 0 ? KvBatch{} : a.b, d_status, a.counters, p.ctas, stream) != cudaSuccess) {
         cudaGetLastError();

@@ -128,6 +128,9 @@ int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ct
 // The same with a tree's masks (kv_tree_step.cu, kv_tree_chunk.cu).
 int launch_kv_tree_step(const AttentionArgs& a, uint32_t ctas, cudaStream_t s);
 int launch_kv_tree_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s);
+// Up to kTreeTileRows rows a sequence (kv_tree_tile.cu).
+constexpr uint64_t kTreeTileRows = 128;
+int launch_kv_tree_tile(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s);
 
 // kv_tree.cu
 int check_tree(const splitzip_kv_tree_t* tree, const KvBatch& b);

@@ -78,6 +78,17 @@ constexpr int kPlanThreads = 1024;
 // dims, are what it was chosen by.
 constexpr int kItemCost = 8;
 
+// How work is cut: rows of a tile, what an item costs beside its keys, and
+// whether rows see a tree's masks.
+struct CausalWork {
+    static constexpr bool kTree = false;
+    static constexpr int kTile = kRows, kCost = kItemCost;
+};
+struct TreeWork {
+    static constexpr bool kTree = true;
+    static constexpr int kTile = kRows, kCost = kItemCost;
+};
+
 // Tensor maps of K and V (unused by the kernels that copy rows themselves).
 struct ChunkMaps {
     CUtensorMap k, v;
@@ -101,8 +112,9 @@ struct ChunkPlan {
     ChunkStart start[1];
 };
 
+template <class W>
 __device__ __forceinline__ int tile_count(const AttentionArgs& a, const KvSeq& s) {
-    return (s.t * int(a.group) + kRows - 1) / kRows;
+    return (s.t * int(a.group) + W::kTile - 1) / W::kTile;
 }
 
 struct Tile {
@@ -111,12 +123,12 @@ struct Tile {
     int units;
 };
 
-template <bool TREE>
+template <class W>
 __device__ __forceinline__ Tile tile_of(const AttentionArgs& a, const KvSeq& s, int tile) {
     Tile t;
-    t.row_first = tile * kRows;
-    t.rows = min(kRows, s.t * int(a.group) - t.row_first);
-    t.keys = visible<TREE>(a, s, t.row_first / int(a.group), (t.row_first + t.rows - 1) / int(a.group));
+    t.row_first = tile * W::kTile;
+    t.rows = min(W::kTile, s.t * int(a.group) - t.row_first);
+    t.keys = visible<W::kTree>(a, s, t.row_first / int(a.group), (t.row_first + t.rows - 1) / int(a.group));
     t.units = unit_count(t.keys, kUnit);
     return t;
 }
@@ -127,7 +139,7 @@ __device__ __forceinline__ Tile tile_of(const AttentionArgs& a, const KvSeq& s, 
 // two tiles and the whole warp one of more; then a scan over the sequences, and
 // where each CTA's share starts: by a search for the sequence and, where it has
 // more tiles than two, the same walk again.
-template <bool TREE>
+template <class W>
 __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __grid_constant__ AttentionArgs a,
                                                                      ChunkPlan* plan, uint32_t grid) {
     release_successor();
@@ -139,7 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     if (tid == 0) s_bad = 0;
     __syncthreads();
     const auto weight = [&](const KvSeq& s, int tile) -> uint64_t {
-        return uint64_t(tile_of<TREE>(a, s, tile).units + kItemCost) * a.c.kv_heads;
+        return uint64_t(tile_of<W>(a, s, tile).units + W::kCost) * a.c.kv_heads;
     };
     // the lane's sequence of a round
     const uint32_t nth = lane * kPlanWarps + warp;
@@ -154,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     // Calls each(sequence, index in the round) by the whole warp for every sequence
     // of more than two tiles.
     const auto for_large = [&](const KvSeq& s, const auto& each) {
-        uint32_t many = __ballot_sync(~0u, tile_count(a, s) > 2);
+        uint32_t many = __ballot_sync(~0u, tile_count<W>(a, s) > 2);
         while (many) {
             const int src = __ffs(many) - 1;
             many &= many - 1;
@@ -165,13 +177,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
     // Units through each of the round's sequences into s_upto; returns the round's.
     const auto round_units = [&](const KvSeq& s) -> uint64_t {
         uint64_t w = 0;
-        const int n = tile_count(a, s);
+        const int n = tile_count<W>(a, s);
         for (int i = 0; i < n && n <= 2; ++i) w += weight(s, i);
         __syncthreads();
         if (n <= 2) s_upto[nth] = w;
         for_large(s, [&](const KvSeq& o, uint32_t at) {
             uint64_t part = 0;
-            for (int i = int(lane), tiles = tile_count(a, o); i < tiles; i += 32) part += weight(o, i);
+            for (int i = int(lane), tiles = tile_count<W>(a, o); i < tiles; i += 32) part += weight(o, i);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(~0u, part, d);
             if (lane == 0) s_upto[at] = part;
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
                     at = mid + 1;
             }
             const KvSeq o = load_seq(a.b, b0 + at);
-            const int n = tile_count(a, o);
+            const int n = tile_count<W>(a, o);
             if (n <= 2) {
                 const uint64_t from = from_of(at), x = weight(o, 0);
                 const uint32_t tile = n == 2 && u >= from + x ? 1 : 0;
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_chunk_plan_kernel(const __gri
         }
         for_large(s, [&](const KvSeq& o, uint32_t at) {
             uint64_t from = from_of(at);
-            for (int i0 = 0, tiles = tile_count(a, o); i0 < tiles; i0 += 32) {
+            for (int i0 = 0, tiles = tile_count<W>(a, o); i0 < tiles; i0 += 32) {
                 const int i = i0 + int(lane);
                 const uint64_t x = i < tiles ? weight(o, i) : 0;
                 uint64_t y = x;
@@ -340,7 +352,7 @@ struct Chunk {
 
 // Walks the CTA's share and describes its pieces to the other roles (one
 // thread, ahead of them by up to kSegments).
-template <bool TREE, class Shared>
+template <class W, class Shared>
 __device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh, const ChunkPlan* plan, ChunkSplit* splits,
                                              bool& ok) {
     splits[blockIdx.x] = ChunkSplit{};
@@ -365,19 +377,19 @@ __device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh,
             uint32_t size = 0;
             while (true) {
                 s = load_seq(a.b, b);
-                if (int(tile) >= tile_count(a, s)) {
+                if (int(tile) >= tile_count<W>(a, s)) {
                     ++b;
                     tile = 0;
                     continue;
                 }
-                t = tile_of<TREE>(a, s, int(tile));
-                size = uint32_t(t.units + kItemCost);
+                t = tile_of<W>(a, s, int(tile));
+                size = uint32_t(t.units + W::kCost);
                 if (u < group_start + uint64_t(size) * a.c.kv_heads) break;
                 group_start += uint64_t(size) * a.c.kv_heads;
                 ++tile;
             }
             const uint32_t head = uint32_t((u - group_start) / size);
-            const uint64_t keys_start = group_start + uint64_t(head) * size + kItemCost;
+            const uint64_t keys_start = group_start + uint64_t(head) * size + W::kCost;
             const uint64_t item_end = keys_start + uint32_t(t.units);
             const uint64_t from = max(u, keys_start), stop = min(item_end, end);
             if (from >= stop) {  // the share ends before the item's keys
@@ -784,9 +796,8 @@ __device__ __forceinline__ float* part_at(const AttentionArgs& a, uint32_t cta, 
 }
 
 // The natural logarithm of a row's sum of exponentials l against reference m.
-template <bool H>
-__device__ __forceinline__ float log_sum(float m, float l, float scale) {
-    return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m * scale) - weight_shift<H>() + log2f(l)) * 0.693147180559945309f;
+__device__ __forceinline__ float log_sum(float m, float l, float scale, float shift) {
+    return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m * scale) - shift + log2f(l)) * 0.693147180559945309f;
 }
 
 template <int FMT, bool H, int D, bool TREE>
@@ -1060,7 +1071,7 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             if (a.lse && mine >= 0) {
                 const int r = w.row_first + int(row) + g * kTileRows, i = r / int(a.group);
                 a.lse[uint64_t(w.row0 + i) * a.q_heads + w.head * a.group + uint32_t(r - i * int(a.group))] =
-                    log_sum<H>(m, l, scale);
+                    log_sum(m, l, scale, C::kShift);
             }
         };
         // 32 columns of the row's sums
@@ -1164,7 +1175,7 @@ __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
         if (warp == 8) load_tma_role<C>(a, sh, &maps.k, &maps.v, ok, bad);
     }
     if (warp == C::kProductWarp) product_role<FMT, H, D>(sh, tmem, ok);
-    if (threadIdx.x == C::kSegmentWarp * 32u) segment_role<TREE>(a, sh, plan, splits, ok);
+    if (threadIdx.x == C::kSegmentWarp * 32u) segment_role<std::conditional_t<TREE, TreeWork, CausalWork>>(a, sh, plan, splits, ok);
     if (bad) report(a.status, SPLITZIP_ERR_INVALID_ARG);
     if (!ok) report(a.status, SPLITZIP_ERR_TIMEOUT);
     __syncwarp();
@@ -1186,7 +1197,8 @@ constexpr int kJoinParts = 2, kJoinColumns = 8, kJoinThreads = kJoinParts * kJoi
 
 template <bool H, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-    kv_chunk_join_kernel(const __grid_constant__ AttentionArgs a, const ChunkSplit* splits, float value_scale) {
+    kv_chunk_join_kernel(const __grid_constant__ AttentionArgs a, const ChunkSplit* splits, float value_scale,
+                         float scale, float shift) {
     constexpr int kColumns = D / kJoinColumns;
     __shared__ float s_o[D][32], s_l[kJoinColumns][32];
     wait_predecessor();
@@ -1196,7 +1208,6 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (int(blockIdx.y) * 32 >= w.rows) return;
     const int row = int(blockIdx.y * 32u + lane);  // those past the last read what is there, and write nothing
     const uint32_t g = uint32_t(row) / kTileRows, at = uint32_t(row) % kTileRows;
-    const float scale = a.scale_log2;
     float m = -INFINITY, l = 0.f;
 #pragma unroll 8
     for (uint32_t cta = first; cta <= w.last_cta; ++cta) m = fmaxf(m, part_at<D>(a, cta, first, g)[D * kTileRows + at]);
@@ -1239,7 +1250,7 @@ __global__ void __launch_bounds__(kJoinThreads)
         }
         reinterpret_cast<uint4*>(out)[k] = make_uint4(z[0], z[1], z[2], z[3]);
     }
-    if (a.lse && col0 == 0) a.lse[uint64_t(w.row0 + i) * a.q_heads + head] = log_sum<H>(m, l, scale);
+    if (a.lse && col0 == 0) a.lse[uint64_t(w.row0 + i) * a.q_heads + head] = log_sum(m, l, scale, shift);
 }
 
 uint64_t plan_bytes(uint32_t ctas) { return sizeof(ChunkPlan) + uint64_t(ctas) * sizeof(ChunkStart); }
@@ -1265,7 +1276,7 @@ int launch(const AttentionArgs& a, ChunkPlan* plan, const ChunkMaps& maps, uint3
     if (cudaLaunchKernelEx(&l.cfg, kv_chunk_kernel<FMT, H, D, TREE>, a, static_cast<const ChunkPlan*>(plan), splits, maps) !=
             cudaSuccess ||
         cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<H, D>, a, static_cast<const ChunkSplit*>(splits),
-                           C::kValueScale) != cudaSuccess) {
+                           C::kValueScale, a.scale_log2, C::kShift) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }
@@ -1292,7 +1303,7 @@ bool make_maps(const AttentionArgs& a, ChunkMaps* m) {
 template <bool TREE>
 int launch_chunk(const AttentionArgs& a, bool q_half, void* plan_at, uint32_t ctas, cudaStream_t s) {
     ChunkPlan* plan = static_cast<ChunkPlan*>(plan_at);
-    kv_chunk_plan_kernel<TREE><<<1, kPlanThreads, 0, s>>>(a, plan, ctas);
+    kv_chunk_plan_kernel<std::conditional_t<TREE, TreeWork, CausalWork>><<<1, kPlanThreads, 0, s>>>(a, plan, ctas);
     if (cudaGetLastError() != cudaSuccess) return SPLITZIP_ERR_CUDA;
     ChunkMaps maps;
     std::memset(&maps, 0, sizeof(maps));

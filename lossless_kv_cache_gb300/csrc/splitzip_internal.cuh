@@ -195,10 +195,10 @@ cudaError_t occupancy_decode(int* blocks_per_sm, int dtype);
 cudaError_t occupancy_histogram(int* blocks_per_sm, int dtype);
 
 // Tensor map of 16-bit elements read in boxes of 128-byte rows with the
-// 128-byte swizzle, zeros outside the tensor (strides in bytes, of dimensions
+// 128-byte swizzle (`bytes`: of 8-bit ones in rows as they are), zeros outside the tensor (strides in bytes, of dimensions
 // 1 .. rank - 1); false where the driver takes no such map (capi.cu).
 bool make_rows_map(void* base, uint32_t rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
-                   CUtensorMap* map);
+                   CUtensorMap* map, bool bytes = false);
 
 // SM count of the current device; an error status if it is no sm_103a device
 // (capi.cu).
