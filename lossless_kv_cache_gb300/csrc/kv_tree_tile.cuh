@@ -26,7 +26,7 @@
 //              more): 16-bit K and V to where the products read them, FP8 to
 //              staging buffers
 //   scales     FP8: one warp looks up the keys' scales and makes the factors
-//   converters FP8: four warps, from the staging buffers to FP16 (for E5M2 a
+//   converters FP8: eight warps, from the staging buffers to FP16 (for E5M2 a
 //              permute of bytes and a product)
 //   products   one warp; pieces one thread of another
 // TMEM: S0, S1 (128 columns each, the weights overwrite the scores), O0, O1.
@@ -44,7 +44,7 @@ namespace {
 struct TileWork {
     static constexpr bool kTree = true;
     static constexpr int kTile = kTileRows;
-    static constexpr int kCost = 8;  // what an item costs beside its keys, in units  (COST)
+    static constexpr int kCost = 5;  // what an item costs beside its keys, in units
 };
 
 // What the rows have to know of a unit's scales.
@@ -69,8 +69,8 @@ struct TreeTile {
     // its way from memory, 50 KB and more an SM: 16-bit tiles, or FP8 ones as they come,
     // and then as few converted ones as the products can do with.
     static constexpr int kKeys = kFp8 ? 2 : 98304 / kTileBytes, kValues = kFp8 ? 3 - kHalves : kKeys;
-    static constexpr int kConverters = kFp8 ? 4 : 0;       // warps
-    static constexpr int kThreads = kFp8 ? 512 : 384;
+    static constexpr int kConverters = kFp8 ? 8 : 0;       // warps
+    static constexpr int kThreads = kFp8 ? 640 : 384;
     static constexpr uint32_t kProductWarp = 8 + kConverters, kSegmentWarp = kProductWarp + 1,
                               kCopyWarp = kProductWarp + 2, kScaleWarp = kProductWarp + 3;
     // FP8 tiles as they come: on their way, or being converted
@@ -307,13 +307,13 @@ __device__ __forceinline__ void scale_role(const AttentionArgs& a, typename C::S
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Four warps, a 16-byte piece of every kRowStep-th row of a tile each thread, K a
+// Eight warps, a 16-byte piece of every kRowStep-th row of a tile each thread, K a
 // unit ahead of V.
 template <class C>
 __device__ __forceinline__ void convert_role(typename C::Shared& sh, bool& ok) {
     const uint32_t lt = threadIdx.x - 256u, lane = lt & 31u;
     constexpr uint32_t kRowStep = 32 * C::kConverters / C::kChunks;
-    constexpr int kPieces = 128 / int(kRowStep);
+    constexpr int kPieces = 128 / int(kRowStep), kOnce = 2;  // of a tile, and at a time
     const uint32_t c = lt % C::kChunks, r0 = lt / C::kChunks;
     // a row's lanes of the two column blocks in turns: every bank once
     const bool swap = c & 4u;
@@ -333,18 +333,18 @@ __device__ __forceinline__ void convert_role(typename C::Shared& sh, bool& ok) {
         uint8_t* row = (is_v ? sh.v[u % C::kValues] : sh.k[u % C::kKeys]) + to;
         const bool zeros = is_v && sh.scales[at].own;  // are looked for
 #pragma unroll 1
-        for (int i0 = 0; i0 < kPieces; i0 += 4) {
-            uint4 y[4];
-            uint32_t f[4];
+        for (int i0 = 0; i0 < kPieces; i0 += kOnce) {
+            uint4 y[kOnce];
+            uint32_t f[kOnce];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kOnce; ++i) {
                 y[i] = *reinterpret_cast<const uint4*>(raw + i * int(512 * C::kConverters));
                 f[i] = times[uint32_t(i) * kRowStep];
             }
-            raw += 4 * 512 * C::kConverters;
-            times += 4 * kRowStep;
+            raw += kOnce * 512 * C::kConverters;
+            times += kOnce * kRowStep;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kOnce; ++i) {
                 if (f[i] == 0) y[i] = make_uint4(0, 0, 0, 0);  // whatever is there: 0 times NaN is NaN
                 const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
                 if (zeros) {
@@ -885,19 +885,19 @@ __global__ void __launch_bounds__(TreeTile<FMT, H, D>::kThreads, 1)
     wait_predecessor();  // the plan is written, the status clear
     release_successor();
     bool ok = true, bad = false;
-    // registers of the launch: 384 threads of 168, 2 * 216 + 72 = 3 * 168, or 512 of 128,
-    // 2 * 184 + 96 + 48 = 4 * 128
+    // registers of the launch: 384 threads of 168, 2 * 216 + 72 = 3 * 168, or 640 of 96,
+    // 2 * 136 + 2 * 64 + 56 < 5 * 96
     if (warp < 8) {
         if (C::kFp8)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         tile_softmax_role<FMT, H, D>(a, sh, tmem, ok);
     } else if (warp < C::kProductWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if constexpr (C::kFp8) convert_role<C>(sh, ok);
     } else if (C::kFp8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
