@@ -207,9 +207,15 @@ bool splitzip::make_rows_map(void* base, uint32_t rank, const uint64_t* dims, co
         ones[i] = 1;
         if (i + 1 < rank) st[i] = strides[i];
     }
+    // no more than the rows that are read one after another: 256 bytes of promotion had the
+    // caches of 128-byte rows read half as much again from memory, the next head's
+    const uint64_t row = dims[0] * (bytes ? 1 : 2);
+    const CUtensorMapL2promotion promotion = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                             : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                          : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
     return encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, base, d, st, b,
                   ones, CU_TENSOR_MAP_INTERLEAVE_NONE, bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int splitzip::device_sms(int* sms) {

@@ -350,24 +350,17 @@ struct Chunk {
     static constexpr int kSmem = int(sizeof(Shared));
 };
 
-// Walks the CTA's share and describes its pieces to the other roles (one
-// thread, ahead of them by up to kSegments).
+// Walks the CTA's share, whose first unit is `start`'s, and describes its
+// pieces to the other roles (one thread, ahead of them by up to kSegments).
 template <class W, class Shared>
-__device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh, const ChunkPlan* plan, ChunkSplit* splits,
-                                             bool& ok) {
+__device__ __forceinline__ void walk_share(const AttentionArgs& a, Shared& sh, uint64_t units, uint32_t ctas,
+                                           const ChunkStart& start, ChunkSplit* splits, bool& ok) {
     splits[blockIdx.x] = ChunkSplit{};
-    const uint64_t units = __ldcg(&plan->units);
-    const uint32_t ctas = __ldcg(&plan->ctas);
-    uint64_t u = 0, end = 0, group_start = 0;
-    uint32_t b = 0, tile = 0;
+    uint64_t u = 0, end = 0, group_start = start.group_start;
+    uint32_t b = start.b, tile = start.tile;
     if (blockIdx.x < ctas) {
         u = share_start(units, ctas, blockIdx.x);
         end = share_start(units, ctas, uint64_t(blockIdx.x) + 1);
-        if (u < end) {
-            b = __ldcg(&plan->start[blockIdx.x].b);
-            tile = __ldcg(&plan->start[blockIdx.x].tile);
-            group_start = __ldcg(&plan->start[blockIdx.x].group_start);
-        }
     }
     for (uint32_t i = 0; ok; ++i) {
         Segment g{};
@@ -414,6 +407,19 @@ __device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh,
         mbar_arrive(&sh.seg_full[i % kSegments]);
         if (g.n == 0) break;
     }
+}
+
+// The same with what the plan kernel found.
+template <class W, class Shared>
+__device__ __forceinline__ void segment_role(const AttentionArgs& a, Shared& sh, const ChunkPlan* plan, ChunkSplit* splits,
+                                             bool& ok) {
+    const uint64_t units = __ldcg(&plan->units);
+    const uint32_t ctas = __ldcg(&plan->ctas);
+    ChunkStart start{0, 0, 0};
+    if (blockIdx.x < ctas && share_start(units, ctas, blockIdx.x) < share_start(units, ctas, uint64_t(blockIdx.x) + 1))
+        start = ChunkStart{__ldcg(&plan->start[blockIdx.x].b), __ldcg(&plan->start[blockIdx.x].tile),
+                           __ldcg(&plan->start[blockIdx.x].group_start)};
+    walk_share<W>(a, sh, units, ctas, start, splits, ok);
 }
 
 // Waits until the stage of tile x (K of unit x / 2 where even, else V) can be

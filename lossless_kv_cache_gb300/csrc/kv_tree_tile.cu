@@ -13,8 +13,14 @@ int launch_kv_tree_tile(const AttentionArgs& a, bool q_half, void* plan_at, uint
     if (a.c.page_shift < 3 || !(fp8 ? make_byte_maps(a, &maps) : make_maps(a, &maps)) ||
         (fp8 && ((reinterpret_cast<uintptr_t>(a.c.k_scale) | reinterpret_cast<uintptr_t>(a.c.v_scale)) & 15u)))
         return launch_kv_tree_chunk(a, q_half, plan_at, ctas, s);
-    kv_chunk_plan_kernel<TileWork><<<1, kPlanThreads, 0, s>>>(a, plan, ctas);
-    if (cudaGetLastError() != cudaSuccess) return SPLITZIP_ERR_CUDA;
+    // the status by all sequences' entries, and where there are many, their plan
+    if (a.b.batch > kPlanSequences) {
+        kv_chunk_plan_kernel<TileWork><<<1, kPlanThreads, 0, s>>>(a, plan, ctas);
+        if (cudaGetLastError() != cudaSuccess) return SPLITZIP_ERR_CUDA;
+    } else if (launch_kv_begin(a.b, a.status, nullptr, 0, s) != cudaSuccess) {
+        cudaGetLastError();
+        return SPLITZIP_ERR_CUDA;
+    }
     const bool wide = a.c.head_dim == 128;
     switch (a.c.type) {
         case SPLITZIP_KV_FP8_E5M2:

@@ -47,6 +47,52 @@ struct TileWork {
     static constexpr int kCost = 5;  // what an item costs beside its keys, in units
 };
 
+// Up to so many sequences each CTA deals the units itself, a warp with a few
+// sequences a lane, and no plan kernel runs before.  (PLAN)
+constexpr uint32_t kPlanSequences = 128;
+
+// The units of all items, and where this CTA's share of them starts (whole warp).
+__device__ __forceinline__ uint64_t deal(const AttentionArgs& a, uint32_t* ctas, ChunkStart* start) {
+    constexpr int kRounds = kPlanSequences / 32;
+    const uint32_t lane = threadIdx.x & 31u;
+    uint64_t mine[kRounds], units = 0;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const uint32_t b = uint32_t(i) * 32u + lane;
+        mine[i] = 0;
+        if (b < a.b.batch) {
+            const KvSeq s = load_seq(a.b, b);
+            if (s.t > 0) mine[i] = uint64_t(tile_of<TileWork>(a, s, 0).units + TileWork::kCost) * a.c.kv_heads;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) units += mine[i];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) units += __shfl_xor_sync(~0u, units, d);
+    *ctas = uint32_t(min(uint64_t(gridDim.x), max(units, uint64_t(1))));
+    *start = ChunkStart{0, 0, 0};
+    if (blockIdx.x >= *ctas) return units;
+    const uint64_t u = share_start(units, *ctas, blockIdx.x);
+    uint64_t before = 0;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        uint64_t upto = mine[i];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t y = __shfl_up_sync(~0u, upto, d);
+            if (int(lane) >= d) upto += y;
+        }
+        upto += before;
+        const uint32_t holds = __ballot_sync(~0u, mine[i] > 0 && u >= upto - mine[i] && u < upto);
+        if (holds) {
+            const int src = __ffs(holds) - 1;
+            *start = ChunkStart{uint32_t(i) * 32u + uint32_t(src), 0, __shfl_sync(~0u, upto - mine[i], src)};
+        }
+        before = __shfl_sync(~0u, upto, 31);
+    }
+    return units;
+}
+
 // What the rows have to know of a unit's scales.
 struct UnitScales {
     float k;   // 2^EK
@@ -313,7 +359,7 @@ template <class C>
 __device__ __forceinline__ void convert_role(typename C::Shared& sh, bool& ok) {
     const uint32_t lt = threadIdx.x - 256u, lane = lt & 31u;
     constexpr uint32_t kRowStep = 32 * C::kConverters / C::kChunks;
-    constexpr int kPieces = 128 / int(kRowStep), kOnce = 2;  // of a tile, and at a time
+    constexpr int kPieces = 128 / int(kRowStep), kOnce = kPieces < 4 ? kPieces : 4;  // of a tile, and at a time
     const uint32_t c = lt % C::kChunks, r0 = lt / C::kChunks;
     // a row's lanes of the two column blocks in turns: every bank once
     const bool swap = c & 4u;
@@ -489,9 +535,10 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
         ok = named_barrier_and(4, 256, ok);  // both groups go on or neither
         if (!ok || w.n == 0) break;
         const int n = w.n;
-        const auto place = [&](const KvRows& rows, uint32_t nth) -> int64_t {
-            const int r = w.row_first + int(nth);  // of the sequence
-            if (int(nth) >= w.rows) return -1;
+        // where the row of the warp's sixteen that is the lane's (mod 16) lies, -1 where there is none
+        const auto place = [&](const KvRows& rows) -> int64_t {
+            const int nth = int(row0 + lane % 16u), r = w.row_first + nth;  // of the sequence
+            if (nth >= w.rows) return -1;
             const int i = r / int(a.group);
             return int64_t(uint64_t(w.row0 + i) * rows.token_stride +
                            uint64_t(w.head * a.group + uint32_t(r - i * int(a.group))) * rows.head_stride);
@@ -514,10 +561,11 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
         {
             // the rows of Q, zeros where there is none; a negative scale's sign goes to Q
             const uint32_t flip = a.negate ? 0x80008000u : 0u;
+            const int64_t mine = place(a.q);
             uint4 x[kMoves];
 #pragma unroll
             for (int k = 0; k < kMoves; ++k) {
-                const int64_t at = place(a.q, row0 + uint32_t(k) * kRowsOnce + piece_row);
+                const int64_t at = __shfl_sync(~0u, mine, k * int(kRowsOnce) + int(piece_row));
                 x[k] = at < 0 ? make_uint4(0, 0, 0, 0) : reinterpret_cast<const uint4*>(a.q.d + at)[piece_col];
             }
 #pragma unroll
@@ -783,24 +831,23 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
         float* part = part_at<D>(a, blockIdx.x, first, 0) + row;
         // an infinity or NaN stays one whatever the factor
         const auto times = [](float o, float f) { return fabsf(o) < INFINITY ? o * f : o; };
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-            const int col = g * (D / 2) + 32 * k;
-            uint32_t o0[32], o1[32];
-            tmem_load32(o0, o_at + uint32_t(col));
-            if (n > 1) tmem_load32(o1, o_at + 128u + uint32_t(col));
+#pragma unroll 1
+        for (int col = g * (D / 2); col < (g + 1) * (D / 2); col += 16) {
+            uint32_t o0[16], o1[16];
+            tmem_load16(o0, o_at + uint32_t(col));
+            if (n > 1) tmem_load16(o1, o_at + 128u + uint32_t(col));
             tmem_wait_load();
-            tmem_loaded32(o0);
-            if (n > 1) tmem_loaded32(o1);
-            float o[32];
+            tmem_loaded16(o0);
+            if (n > 1) tmem_loaded16(o1);
+            float o[16];
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
+            for (int y = 0; y < 16; ++y) {
                 o[y] = times(__uint_as_float(o0[y]), f0);
                 if (n > 1) o[y] += times(__uint_as_float(o1[y]), f1);
             }
             if (whole) {
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
+                for (int y = 0; y < 2; ++y) {
                     uint32_t z[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -811,7 +858,7 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
                 }
             } else if (live) {
 #pragma unroll
-                for (int y = 0; y < 32; ++y) part[(col + y) * kTileRows] = o[y];
+                for (int y = 0; y < 16; ++y) part[(col + y) * kTileRows] = o[y];
             }
         }
         if (!whole && live && g == 0) {
@@ -820,10 +867,11 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
         }
         if (whole) {
             ok = named_barrier_and(4, 256, ok);
+            const int64_t mine = place(a.out);
 #pragma unroll
             for (int k = 0; k < kMoves; ++k) {
                 const uint32_t r = row0 + uint32_t(k) * kRowsOnce + piece_row;
-                const int64_t at = place(a.out, r);
+                const int64_t at = __shfl_sync(~0u, mine, k * int(kRowsOnce) + int(piece_row));
                 if (at >= 0) reinterpret_cast<uint4*>(a.out.d + at)[piece_col] = *staged(r, piece_col);
             }
             if (a.lse && g == 0 && live) {
@@ -882,7 +930,7 @@ __global__ void __launch_bounds__(TreeTile<FMT, H, D>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    wait_predecessor();  // the plan is written, the status clear
+    if (plan) wait_predecessor();  // the plan is written
     release_successor();
     bool ok = true, bad = false;
     // registers of the launch: 384 threads of 168, 2 * 216 + 72 = 3 * 168, or 640 of 96,
@@ -906,7 +954,17 @@ __global__ void __launch_bounds__(TreeTile<FMT, H, D>::kThreads, 1)
         if (warp == C::kScaleWarp) scale_role<C>(a, sh, ok);
     }
     if (warp == C::kProductWarp) tile_product_role<C, D>(sh, tmem, ok);
-    if (threadIdx.x == C::kSegmentWarp * 32u) segment_role<TileWork>(a, sh, plan, splits, ok);
+    if (warp == C::kSegmentWarp) {
+        if (plan) {
+            if ((threadIdx.x & 31u) == 0) segment_role<TileWork>(a, sh, plan, splits, ok);
+        } else {
+            uint32_t ctas;
+            ChunkStart start;
+            const uint64_t units = deal(a, &ctas, &start);
+            if ((threadIdx.x & 31u) == 0) walk_share<TileWork>(a, sh, units, ctas, start, splits, ok);
+        }
+    }
+    wait_predecessor();  // the status is clear
     if (bad) report(a.status, SPLITZIP_ERR_INVALID_ARG);
     if (!ok) report(a.status, SPLITZIP_ERR_TIMEOUT);
     __syncwarp();
@@ -929,7 +987,7 @@ bool make_byte_maps(const AttentionArgs& a, ChunkMaps* m) {
 }
 
 template <int FMT, bool H, int D>
-int launch_tile(const AttentionArgs& a, ChunkPlan* plan, const ChunkMaps& maps, uint32_t ctas, cudaStream_t s) {
+int launch_tile(const AttentionArgs& a, ChunkPlan* plan_at, const ChunkMaps& maps, uint32_t ctas, cudaStream_t s) {
     using C = TreeTile<FMT, H, D>;
     static_assert(C::kSmem <= 232448, "shared memory of a CTA");
     static std::atomic<uint64_t> ready{0};
@@ -944,12 +1002,12 @@ int launch_tile(const AttentionArgs& a, ChunkPlan* plan, const ChunkMaps& maps, 
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_release);
     }
     ChainedLaunch l(dim3(ctas), dim3(C::kThreads), C::kSmem, s);
-    ChunkSplit* splits = reinterpret_cast<ChunkSplit*>(reinterpret_cast<uint8_t*>(plan) + plan_bytes(ctas));
+    ChunkSplit* splits = reinterpret_cast<ChunkSplit*>(reinterpret_cast<uint8_t*>(plan_at) + plan_bytes(ctas));
+    const ChunkPlan* plan = a.b.batch <= kPlanSequences ? nullptr : plan_at;
     ChainedLaunch join(dim3(ctas, kTileRows / 32), dim3(kJoinThreads), 0, s);
     const bool out_half = C::kFp8 ? a.q_half != 0 : H;
     const float scale = C::kFp8 ? 1.f : a.scale_log2, value_scale = float(1 << C::kRoom), shift = C::kShift;
-    cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv_tree_tile_kernel<FMT, H, D>, a, static_cast<const ChunkPlan*>(plan),
-                                       splits, maps);
+    cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv_tree_tile_kernel<FMT, H, D>, a, plan, splits, maps);
     if (e == cudaSuccess)
         e = out_half ? cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<true, D>, a,
                                           static_cast<const ChunkSplit*>(splits), value_scale, scale, shift)
