@@ -23,6 +23,8 @@ namespace splitzip {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr uint32_t kAhead = 2;
+constexpr int kMinCtas = 6;
 
 struct RotaryArgs {
     KvCache c;
@@ -87,7 +89,7 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], uint2 (&out)[2]
 // FMT 0: 16-bit cache, 1: E5M2, 2: E4M3.  H: rows in FP16, else BF16.  LPR lanes
 // hold a row.  INTER: pairs of neighbours, else of the two halves.
 template <int FMT, bool H, int LPR, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32) kv_rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kMinCtas) kv_rotary_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr uint32_t kHeads = 32 / LPR;
     const uint32_t lane = threadIdx.x & 31u, col = lane % LPR, nth = lane / LPR;
     const uint64_t warp = uint64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -117,32 +119,51 @@ __global__ void __launch_bounds__(kWarps * 32) kv_rotary_kernel(const __grid_con
                 x[1] = __ldcs(from + piece1);
             }
         };
-        uint4 x[2];
-        load(unit0, x);
+        // kAhead units on their way
+        uint4 x[kAhead][2];
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; ++i) load(unit0 + i, x[i]);
         const KvPlace p = find_place(a.c, a.b, int(token), lane);
         bad = p.bad;
         if (p.mine && !(p.bad && unit1 <= 2 * a.row_units)) {
-            float cs[8], sn[8];
+            // cosines and sines of the lane's eight pairs, two to a register pair
+            float2 cs[4], sn[4];
             if (unit1 > a.row_units) {
+                // a lane makes those of kMade pairs of the token's, for the rows of the warp
+                // turn by the same angles
+                constexpr uint32_t kMade = LPR * 8 / 32;
                 const int64_t pos = a.position ? a.position[token] : p.pos;
+                float c[kMade], s[kMade];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    cs[i] = 1.f, sn[i] = 0.f;
-                    if (rotates) {
-                        const uint64_t turn = __ldg(a.turns + col * 8u + uint32_t(i)) * uint64_t(pos);
-                        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &sn[i], &cs[i]);
-                        cs[i] *= a.magnitude;
-                        sn[i] *= a.magnitude;
+                for (uint32_t i = 0; i < kMade; ++i) {
+                    c[i] = 1.f, s[i] = 0.f;
+                    const uint32_t pair = lane * kMade + i;
+                    if (2 * pair < a.rot) {
+                        const uint64_t turn = __ldg(a.turns + pair) * uint64_t(pos);
+                        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &s[i], &c[i]);
+                        c[i] *= a.magnitude;
+                        s[i] *= a.magnitude;
                     }
                 }
+#pragma unroll
+                for (uint32_t i = 0; i < 8; ++i) {
+                    const int from = int(col * (8 / kMade) + i / kMade);
+                    (i & 1 ? cs[i / 2].y : cs[i / 2].x) = __shfl_sync(~0u, c[i % kMade], from);
+                    (i & 1 ? sn[i / 2].y : sn[i / 2].x) = __shfl_sync(~0u, s[i % kMade], from);
+                }
             }
-            for (uint32_t unit = unit0; unit < unit1; ++unit) {
-                uint4 ahead[2];
-                load(unit + 1, ahead);
+#pragma unroll 1
+            for (uint32_t base = unit0; base < unit1; base += kAhead)
+#pragma unroll
+            for (uint32_t slot = 0; slot < kAhead; ++slot) {
+                const uint32_t unit = base + slot;
+                if (unit >= unit1) break;
+                const uint4 now[2] = {x[slot][0], x[slot][1]};
+                load(unit + kAhead, x[slot]);
                 int side;
                 uint32_t head;
                 const bool there = row_of(unit, &side, &head);
-                const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+                const uint32_t w[8] = {now[0].x, now[0].y, now[0].z, now[0].w, now[1].x, now[1].y, now[1].z, now[1].w};
                 float f[16];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -151,18 +172,30 @@ __global__ void __launch_bounds__(kWarps * 32) kv_rotary_kernel(const __grid_con
                 }
                 if (side != 0 && rotates) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float& e = f[INTER ? 2 * i : i];
-                        float& o = f[INTER ? 2 * i + 1 : i + 8];
-                        const float t = e * cs[i] - o * sn[i];
-                        o = e * sn[i] + o * cs[i];
-                        e = t;
+                    for (int i = 0; i < 4; ++i) {
+                        if (INTER) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float &e = f[4 * i + 2 * h], &o = f[4 * i + 2 * h + 1];
+                                const float ch = h ? cs[i].y : cs[i].x, sh = h ? sn[i].y : sn[i].x;
+                                const float t = e * ch - o * sh;
+                                o = e * sh + o * ch;
+                                e = t;
+                            }
+                        } else {
+                            const float2 e = make_float2(f[2 * i], f[2 * i + 1]);
+                            const float2 o = make_float2(f[2 * i + 8], f[2 * i + 9]);
+                            const float2 t = fma2(e, cs[i], mul2(o, make_float2(-sn[i].x, -sn[i].y)));
+                            const float2 z = fma2(e, sn[i], mul2(o, cs[i]));
+                            f[2 * i] = t.x, f[2 * i + 1] = t.y;
+                            f[2 * i + 8] = z.x, f[2 * i + 9] = z.y;
+                        }
                     }
                 }
                 if (side == 2 || FMT == 0) {
                     uint4 y[2];
                     if (side == 0 || !rotates) {
-                        y[0] = x[0], y[1] = x[1];  // as they are, NaN included
+                        y[0] = now[0], y[1] = now[1];  // as they are, NaN included
                     } else {
                         uint32_t z[8];
 #pragma unroll
@@ -197,7 +230,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv_rotary_kernel(const __grid_con
                                                                p.slot] = uint8_t(scale);
                     }
                 }
-                x[0] = ahead[0], x[1] = ahead[1];
             }
         }
     }
