@@ -27,6 +27,17 @@ uint64_t align256(uint64_t x) { return (x + 255u) & ~uint64_t(255); }
 // other numbers of heads follow this table without one of their own.
 constexpr uint64_t kStepRowsMax = 32;
 
+// The same of trees, whose second kernel (kv_tree_tile.cuh) has one tile of rows
+// and is bound by the bytes too: 17 to 32 rows, of which the first reads the keys
+// twice, take the second, but for short contexts, where its start counts.  In us
+// for 8 kv heads of 128 in pages of 16, the first by 16 / 32 rows, then the second:
+//   BF16, 1 sequence of 2,000     17 / 17     21       E5M2    19 / 21     24
+//   BF16, 1 of 16,000             30 / 32     30       E5M2    35 / 38     33
+//   BF16, 8 of 4,000              39 / 49     39       E5M2    38 / 53     44
+//   BF16, 64 of 2,000            101 / 178   111       E5M2    95 / 164   140
+//   BF16, 200 of 1,000           149 / 276   184       E5M2   151 / 265   288
+constexpr uint64_t kTreeStepRowsMax = 16, kTreeStepKeysMax = 8192;
+
 struct Plan {
     uint32_t group, ctas;
     bool chunk;
@@ -40,22 +51,31 @@ uint64_t lay_out(Plan* p, uint64_t plan_bytes, uint64_t counters, uint64_t part_
     return align256(p->parts_off + 4ull * 2 * p->ctas * part_floats);
 }
 
-int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, Plan* p) {
+int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, bool tree, Plan* p) {
     if (q_heads == 0 || q_heads % c.kv_heads != 0) return SPLITZIP_ERR_INVALID_ARG;
     p->group = q_heads / c.kv_heads;
     // the kernels count a sequence's rows, and up to a tile past them, in an int
     if (p->group > 64 || uint64_t(b.max_tokens) * p->group > 0x7FFFFF00u) return SPLITZIP_ERR_UNSUPPORTED;
     const uint64_t rows = uint64_t(b.tokens) * p->group;
-    p->chunk = uint64_t(b.max_tokens) * p->group > kStepRowsMax;
+    const uint64_t most = uint64_t(b.max_tokens) * p->group;
+    const bool long_tree = tree && uint64_t(b.batch) * b.max_kv_len > kTreeStepKeysMax;
+    p->chunk = most > (long_tree ? kTreeStepRowsMax : kStepRowsMax);
     // tiles of rows over all sequences: each has a partial one at most
     const uint64_t tiles = std::min<uint64_t>((rows + 7) / 8 + b.batch, rows);
     p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);
     p->ws_bytes = lay_out(p, 0, p->ctas, step_part_floats(c.head_dim));
-    if (p->chunk) {
-        // a step of the same rows, but fewer of a sequence, takes the other kernel:
-        // the size is enough for both
+    if (p->chunk || most > kTreeStepRowsMax) {
+        // a step of the same rows, but fewer of a sequence, takes the other kernel, and so
+        // may a tree: the size is enough for both
+        const uint32_t step = p->ctas;
         p->ctas = chunk_ctas(rows, b.batch, c.kv_heads, b.max_kv_len);
-        p->ws_bytes = std::max(p->ws_bytes, lay_out(p, chunk_plan_bytes(p->ctas), 0, chunk_part_floats(c.head_dim)));
+        const uint64_t bytes = lay_out(p, chunk_plan_bytes(p->ctas), 0, chunk_part_floats(c.head_dim));
+        const uint64_t both = std::max(p->ws_bytes, bytes);
+        if (!p->chunk) {
+            p->ctas = step;
+            lay_out(p, 0, p->ctas, step_part_floats(c.head_dim));
+        }
+        p->ws_bytes = both;
     }
     return SPLITZIP_OK;
 }
@@ -71,7 +91,7 @@ extern "C" int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* c
     int st = check_kv(cache, batch, &c, &b, false);
     if (st != SPLITZIP_OK) return st;
     if (!out_bytes) return SPLITZIP_ERR_INVALID_ARG;
-    if ((st = plan_for(c, b, q_heads, &p)) != SPLITZIP_OK) return st;
+    if ((st = plan_for(c, b, q_heads, false, &p)) != SPLITZIP_OK) return st;
     *out_bytes = p.ws_bytes;
     return SPLITZIP_OK;
 }
@@ -98,7 +118,7 @@ int attend(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch, c
         a.words = tree->words;
         window = tree->window;
     }
-    if ((st = plan_for(a.c, a.b, q_heads, &p)) != SPLITZIP_OK) return st;
+    if ((st = plan_for(a.c, a.b, q_heads, is_tree, &p)) != SPLITZIP_OK) return st;
     if (!kv_dtype_fits(a.c.type, dtype) || !std::isfinite(scale)) return SPLITZIP_ERR_INVALID_ARG;
     if ((st = check_rows(q, a.b, q_heads, a.c.head_dim, &a.q)) != SPLITZIP_OK) return st;
     if ((st = check_rows(out, a.b, q_heads, a.c.head_dim, &a.out)) != SPLITZIP_OK) return st;

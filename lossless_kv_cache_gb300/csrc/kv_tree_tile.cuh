@@ -7,7 +7,7 @@
 // so the loaders bring K and V to the largest scale of the unit, 2^EK and 2^EV,
 // which a row takes into the one factor of its scores and into its reference,
 // the maximum of s + EV; its sums l are of 2^(s-ref).  FP16 holds that exactly
-// but for elements 2^-27 of their row's largest.  Where scales differ by more
+// but for elements under 2^-22 of their row's largest.  Where scales differ by more
 // than 2^kSpread, or EV from the piece's first by more than 2^30, the keys keep
 // scales of their own, as in kv_step.cuh: K's go to the scores, V's to the
 // weights, and rows of zeros, whose scale says nothing of their size, count as
@@ -124,7 +124,7 @@ struct TreeTile {
     static constexpr int kChunks = D / 16;                 // their 16-byte pieces of a row
     static constexpr uint32_t kFactors = 4;                // slots of the keys' factors, a unit each
     static constexpr int kScaleUnits = 6;                  // units whose scales are on their way
-    static constexpr int kSpread = 10;            // scales of a unit that are brought to the largest
+    static constexpr int kSpread = 6;             // scales of a unit that are brought to the largest
     static constexpr int kRoom = kFp8 && !kE5M2 ? 7 : 0;  // E4M3's largest times 2^7 is in FP16's range
 
     struct Shared {
