@@ -31,12 +31,12 @@ constexpr uint64_t kStepRowsMax = 32;
 // and is bound by the bytes too: 17 to 32 rows, of which the first reads the keys
 // twice, take the second, but for short contexts, where its start counts.  In us
 // for 8 kv heads of 128 in pages of 16, the first by 16 / 32 rows, then the second:
-//   BF16, 1 sequence of 2,000     17 / 17     21       E5M2    19 / 21     24
+//   BF16, 1 sequence of 2,000     13 / 18     21       E5M2    14 / 17     24
 //   BF16, 1 of 16,000             30 / 32     30       E5M2    35 / 38     33
 //   BF16, 8 of 4,000              39 / 49     39       E5M2    38 / 53     44
 //   BF16, 64 of 2,000            101 / 178   111       E5M2    95 / 164   140
 //   BF16, 200 of 1,000           149 / 276   184       E5M2   151 / 265   288
-constexpr uint64_t kTreeStepRowsMax = 16, kTreeStepKeysMax = 8192;
+constexpr uint64_t kTreeStepRowsMax = 16;
 
 struct Plan {
     uint32_t group, ctas;
@@ -58,8 +58,7 @@ int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, bool tree, Pl
     if (p->group > 64 || uint64_t(b.max_tokens) * p->group > 0x7FFFFF00u) return SPLITZIP_ERR_UNSUPPORTED;
     const uint64_t rows = uint64_t(b.tokens) * p->group;
     const uint64_t most = uint64_t(b.max_tokens) * p->group;
-    const bool long_tree = tree && uint64_t(b.batch) * b.max_kv_len > kTreeStepKeysMax;
-    p->chunk = most > (long_tree ? kTreeStepRowsMax : kStepRowsMax);
+    p->chunk = most > (tree && !short_tree(b) ? kTreeStepRowsMax : kStepRowsMax);
     // tiles of rows over all sequences: each has a partial one at most
     const uint64_t tiles = std::min<uint64_t>((rows + 7) / 8 + b.batch, rows);
     p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);

@@ -128,6 +128,9 @@ int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ct
 // The same with a tree's masks (kv_tree_step.cu, kv_tree_chunk.cu).
 int launch_kv_tree_step(const AttentionArgs& a, uint32_t ctas, cudaStream_t s);
 int launch_kv_tree_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s);
+// Trees over so few keys that their kernels' start counts more than their bytes.
+inline bool short_tree(const KvBatch& b) { return uint64_t(b.batch) * b.max_kv_len <= 8192; }
+
 // Up to kTreeTileRows rows a sequence (kv_tree_tile.cu).
 constexpr uint64_t kTreeTileRows = 128;
 int launch_kv_tree_tile(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s);

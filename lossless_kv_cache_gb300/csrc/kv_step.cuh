@@ -232,7 +232,10 @@ __global__ void __launch_bounds__(kWarps * 32, Step<FMT, H, D, ROWS>::kCtasPerSm
     const uint64_t items = units >> kItemsAt;
     units &= kUnitsMask;
     const uint64_t most = max(items, (units + kMinUnits - 1) / kMinUnits);
-    const uint32_t ctas = most < gridDim.x ? uint32_t(most) : gridDim.x;
+    uint32_t ctas = most < gridDim.x ? uint32_t(most) : gridDim.x;
+    // Short shares that go past an item's end start, drain and join twice: as many for each
+    // item then (2 trees of 8 tokens over 600: 64 items, 21 us with 304 CTAs, 14 with 256).
+    if (TREE && most > ctas && items <= ctas && units <= uint64_t(ctas) * 8) ctas = ctas / uint32_t(items) * uint32_t(items);
     uint64_t u = 0, end = 0;
     if (blockIdx.x < ctas) {
         u = share_start(units, ctas, blockIdx.x);
@@ -875,7 +878,10 @@ template <int FMT, bool H, bool TREE>
 int launch_shape(const AttentionArgs& a, uint32_t ctas, cudaStream_t s) {
     // Tiles of 8 rows where no sequence has more: half the products and registers.  64 sequences
     // of 8,192 E5M2 tokens and 4 rows take 204 us so and 253 with tiles of 16, four of 500 8.4 and 9.3.
-    const bool few = uint64_t(a.b.max_tokens) * a.group <= 8;
+    // So do trees over short contexts, whose parts' latency counts and whose keys the L2
+    // holds for the next tile: 4 sequences of 500 with 16 rows 13 us so and 16 with tiles
+    // of 16 rows, with 28 rows 15 and 17; 3 of 900 14 and 25, 15 and 18.
+    const bool few = uint64_t(a.b.max_tokens) * a.group <= 8 || (TREE && short_tree(a.b));
     if (a.c.head_dim == 128) return few ? launch<FMT, H, 128, 8, TREE>(a, ctas, s) : launch<FMT, H, 128, 16, TREE>(a, ctas, s);
     return few ? launch<FMT, H, 64, 8, TREE>(a, ctas, s) : launch<FMT, H, 64, 16, TREE>(a, ctas, s);
 }
