@@ -115,6 +115,10 @@ struct TreeTile {
     // its way from memory, 50 KB and more an SM: 16-bit tiles, or FP8 ones as they come,
     // and then as few converted ones as the products can do with.
     static constexpr int kKeys = kFp8 ? 2 : 98304 / kTileBytes, kValues = kFp8 ? 3 - kHalves : kKeys;
+    // Barriers of V's tiles, two and more even for one tile: a group that looks at V before its
+    // product is asked for knows that the tile two units before was there, and with one barrier
+    // would take that tile's phase for its own.
+    static constexpr int kValueBars = kValues > 1 ? kValues : 2;
     static constexpr int kConverters = kFp8 ? 8 : 0;       // warps
     static constexpr int kThreads = kFp8 ? 640 : 384;
     static constexpr uint32_t kProductWarp = 8 + kConverters, kSegmentWarp = kProductWarp + 1,
@@ -142,7 +146,7 @@ struct TreeTile {
         UnitScales scales[kFp8 ? kFactors : 1];
         float2 group_ml[2][kTileRows];              // the groups' references and sums
         float row_scale[kFp8 ? kTileRows : 1];
-        uint64_t k_full[kKeys], k_freed[kKeys], v_full[kValues], v_freed[kValues];
+        uint64_t k_full[kKeys], k_freed[kKeys], v_full[kValueBars], v_freed[kValues];
         uint64_t raw_full[kFp8 ? kRaw : 1], raw_freed[kFp8 ? kRaw : 1];
         uint64_t scale_full[kFp8 ? kFactors : 1], scale_freed[kFp8 ? kFactors : 1];
         uint64_t q_full, s_full[2], p_full[2], o_full[2], drained;
@@ -418,7 +422,7 @@ __device__ __forceinline__ void convert_role(typename C::Shared& sh, bool& ok) {
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&sh.raw_freed[slot]);
-            mbar_arrive(is_v ? &sh.v_full[u % C::kValues] : &sh.k_full[u % C::kKeys]);
+            mbar_arrive(is_v ? &sh.v_full[u % C::kValueBars] : &sh.k_full[u % C::kKeys]);
             if (is_v) mbar_arrive(&sh.scale_freed[at]);  // which the softmax may be done with before
         }
     };
@@ -467,7 +471,7 @@ __device__ __forceinline__ void tile_product_role(typename C::Shared& sh, uint32
             if (j >= 2) {
                 const uint32_t u = unit + uint32_t(j - 2), stage = u % C::kValues;
                 if (ok) ok = mbar_wait(&sh.p_full[g], weights[g]++ & 1u);
-                if (ok) ok = mbar_wait(&sh.v_full[stage], (u / C::kValues) & 1u);
+                if (ok) ok = mbar_wait(&sh.v_full[u % C::kValueBars], (u / C::kValueBars) & 1u);
                 tc_fence_after();
                 const uint64_t v = v_operand + stage * kTileStep;
 #pragma unroll
@@ -665,7 +669,7 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
                 tmem_store16(s_at + uint32_t(c + 16), x + 16);
                 tmem_wait_store();
             };
-            if (C::kFp8 && own) await(&sh.v_full[stage], u / C::kValues);  // which rows of V are zeros is known
+            if (C::kFp8 && own) await(&sh.v_full[u % C::kValueBars], u / C::kValueBars);  // which rows of V are zeros is known
             if (warp_live) {
                 float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll 1
@@ -706,7 +710,7 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
             if (k0 < k1) {
                 const bool outside = !C::kFp8 && (k0 > pos0 || k1 < pos0 + kUnit);
                 // the same in all of the group's threads
-                if (ok) ok = mbar_wait(&sh.v_full[stage], (u / C::kValues) & 1u);
+                if (ok) ok = mbar_wait(&sh.v_full[u % C::kValueBars], (u / C::kValueBars) & 1u);
                 uint8_t* v = sh.v[stage];
                 constexpr uint32_t kInf = C::kHalf ? 0x7C00u : 0x7F80u;
                 if (outside) {
@@ -900,10 +904,8 @@ __global__ void __launch_bounds__(TreeTile<FMT, H, D>::kThreads, 1)
             mbar_init(&sh.k_full[i], C::kFp8 ? C::kConverters : 1);
             mbar_init(&sh.k_freed[i], 1);
         }
-        for (int i = 0; i < C::kValues; ++i) {
-            mbar_init(&sh.v_full[i], C::kFp8 ? C::kConverters : 1);
-            mbar_init(&sh.v_freed[i], 1);
-        }
+        for (int i = 0; i < C::kValueBars; ++i) mbar_init(&sh.v_full[i], C::kFp8 ? C::kConverters : 1);
+        for (int i = 0; i < C::kValues; ++i) mbar_init(&sh.v_freed[i], 1);
         for (int i = 0; i < C::kRaw; ++i) {
             mbar_init(&sh.raw_full[i], 1);
             mbar_init(&sh.raw_freed[i], C::kConverters);

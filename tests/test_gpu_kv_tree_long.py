@@ -194,3 +194,23 @@ def test_infinite_scores(dtype, x):
         check_attention(step, out.cpu()[keep], lse.cpu()[keep],
                         (ref.nan_to_num(0.0)[keep], ref_lse[keep], mag.nan_to_num(0.0)[keep], size[keep]),
                         FP16 if x == FP16 and dtype == FP16 else BF16)
+
+
+@pytest.mark.parametrize("dtype", [E5M2, E4M3, BF16])
+def test_looks_at_its_own_values(dtype):
+    """Units that look at V before their product, for NaN or for rows of zeros, the one tile of it in
+    turns: the same bits however the groups' steps fall."""
+    for seed in range(3):
+        step = LongStep(dtype, [(8 + b % 4, 100 + 3 * b) for b in range(150)], seed=seed)
+        plant_nan(step)
+        q = torch.randn(step.tokens, 32, 128, generator=step.gen).to(step.x).cuda()
+        first = run(step, q, 0.03)
+        for _ in range(25):
+            out, lse = run(step, q, 0.03)
+            assert torch.equal(out.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
+        if dtype != BF16:
+            vary_scales(step, "v", -12, 0)
+            first = run(step, q, 0.03)
+            for _ in range(25):
+                out, lse = run(step, q, 0.03)
+                assert torch.equal(out.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
