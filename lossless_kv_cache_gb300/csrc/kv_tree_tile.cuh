@@ -538,7 +538,7 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
         if (ok) ok = mbar_wait(&sh.seg_full[piece % kSegments], (piece / kSegments) & 1u);
         ok = named_barrier_and(4, 256, ok);  // both groups go on or neither
         if (!ok || w.n == 0) break;
-        const int n = w.n;
+        const int n = w.n, piece_lo = w.lo, piece_hi = w.hi;
         // where the row of the warp's sixteen that is the lane's (mod 16) lies, -1 where there is none
         const auto place = [&](const KvRows& rows) -> int64_t {
             const int nth = int(row0 + lane % 16u), r = w.row_first + nth;  // of the sequence
@@ -618,18 +618,19 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
         for (int j = g; j < n; j += 2, begun = true) {
             const uint32_t u = base + uint32_t(j), stage = u % C::kValues, factors = u % C::kFactors;
             const int pos0 = (w.first_unit + j) * kUnit;
-            await(&sh.s_full[g], scored++);
             const bool all_seen = j >= plain_from && j < plain_to;  // by every row
-            float f = 1.f;                  // what the sums so far are multiplied by
             float unit_scale = scale, unit_e = 0.f;
             bool own = false;
             if (C::kFp8) {
+                // made before the scores, so the wait for those covers the reading
                 await(&sh.scale_full[factors], u / C::kFactors);
                 const UnitScales us = sh.scales[factors];
                 own = us.own;
                 unit_scale = fmaxf(row_scale * us.k, 1.17549435e-38f);
                 unit_e = us.e;
             }
+            await(&sh.s_full[g], scored++);
+            float f = 1.f;  // what the sums so far are multiplied by
             // a bit for each of 32 keys from column c on that the row sees
             const auto sees = [&](int c) -> uint32_t {
                 const int at = pos0 + c;
@@ -706,8 +707,8 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
             // A weight of 0 hides a finite value of V, not an infinity or a NaN: where
             // some row does not see all of this unit's keys, such values are noted for
             // the rows that see them and taken out of V.
-            const int k0 = all_seen ? 0 : max(pos0, w.lo), k1 = all_seen ? 0 : min(pos0 + kUnit, w.hi);
-            if (k0 < k1) {
+            const int k0 = max(pos0, piece_lo), k1 = min(pos0 + kUnit, piece_hi);
+            if (!all_seen && k0 < k1) {
                 const bool outside = !C::kFp8 && (k0 > pos0 || k1 < pos0 + kUnit);
                 // the same in all of the group's threads
                 if (ok) ok = mbar_wait(&sh.v_full[u % C::kValueBars], (u / C::kValueBars) & 1u);
