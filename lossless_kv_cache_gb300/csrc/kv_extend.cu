@@ -14,7 +14,8 @@
 // checks and sums everything before anything is written, since the arrays may
 // be updated in place and a step that does not fit changes nothing.  A page
 // that is taken begins with a new token, so the rows' threads enter the pages
-// into the tables.
+// into the tables.  64 sequences of a token take 4.3 us in a graph, 256 with 85,000
+// tokens 9.6, of which launches and the plan's chain of loads are 7.
 #include "kv_common.cuh"
 
 namespace splitzip {
@@ -23,8 +24,10 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kRowThreads = 128;
 constexpr int kWarpRows = 128;  // rows of a warp of the second kernel
-// Up to so many rows the planning CTA does them itself.  (EXT)
-constexpr uint32_t kRowsInPlan = 2048;
+// Up to so many rows the planning CTA does them itself: 1,792 rows of 256 sequences
+// take 5.3 us so and 7.2 with a second kernel, 4,000 of 8 6.2 and 6.8, 4,096 of 256
+// 7.0 and 7.6, 7,936 of them 9.5 and 7.7.
+constexpr uint32_t kRowsInPlan = 4096;
 
 struct ExtendArgs {
     int32_t* free;
@@ -127,6 +130,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     release_successor();
     constexpr uint32_t kWarps = kPlanThreads / 32;
     __shared__ Sums s_warp[kWarps];
+    __shared__ uint32_t s_upto[kPlanThreads];
+    __shared__ int s_held[kPlanThreads];
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
     // inclusive sums over the CTA's threads; total: over all of them
     const auto scan = [&](const Sums& mine, Sums* total) -> Sums {
@@ -176,10 +181,11 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (uint32_t b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
         const uint32_t b = b0 + tid;
         const bool there = b < a.batch;
+        Sums round = all;  // the only one of up to kPlanThreads sequences
+        const uint64_t before_round = before.less;
         if (a.batch > kPlanThreads) {
             e = Extent{0, 0, 0, 0, true};
             if (there) e = extent_of(a, b);
-            Sums round;
             upto = scan(e.sums(), &round);
             upto += before;
             before += round;
@@ -196,16 +202,27 @@ __global__ void __launch_bounds__(kPlanThreads)
             a.len[b] = n;
             a.held[b] = h;
         }
-        // pages given up, by the whole warp for each sequence that has some
-        uint32_t giving = __ballot_sync(~0u, go && own.less > 0);
-        while (giving) {
-            const int src = __ffs(giving) - 1;
-            giving &= giving - 1;
-            const int need = __shfl_sync(~0u, e.need, src), held = __shfl_sync(~0u, e.held, src);
-            const int64_t at = top - int64_t(__shfl_sync(~0u, upto.less, src)) + held - 1;
-            const int32_t* row = a.table + uint64_t(b0 + warp * 32u + uint32_t(src)) * a.table_stride;
-#pragma unroll 4
-            for (int j = need + int(lane); j < held; j += 32) a.free[at - j] = row[j];
+        // Pages given up, a thread each whosever they are: some sequences give many, most none
+        // (with a warp a sequence 64 of them, half of which gave up some, took 9.1 us, so 5.0).
+        const uint32_t given = go ? uint32_t(round.less) : 0u;
+        if (given > 0) {
+            __syncthreads();
+            s_upto[tid] = uint32_t(upto.less - before_round);
+            s_held[tid] = e.held;
+            __syncthreads();
+            for (uint32_t k = tid; k < given; k += kPlanThreads) {
+                uint32_t at = 0, last = kPlanThreads - 1;  // the first sequence that s_upto > k
+                while (at < last) {
+                    const uint32_t mid = (at + last) / 2;
+                    if (s_upto[mid] > k)
+                        last = mid;
+                    else
+                        at = mid + 1;
+                }
+                const int held = s_held[at], j = held - int(s_upto[at] - k);
+                a.free[top - int64_t(before_round) - int64_t(s_upto[at]) + held - 1 - j] =
+                    a.table[uint64_t(b0 + at) * a.table_stride + uint32_t(j)];
+            }
         }
     }
     if (tid == 0) {
