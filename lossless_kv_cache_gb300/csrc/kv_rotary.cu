@@ -13,7 +13,9 @@
 // elements a lane, dealt so that a lane has both elements of its eight pairs
 // whatever the layout and however much of the head is rotated.  The sines and
 // cosines of those pairs are made once and serve all the warp's heads, of
-// queries and keys.  (ROT)
+// queries and keys.  32,768 tokens (32 query heads of 128 over 8) into BF16 pages
+// with neighbours turned take 128 us, 94 % of a copy's rate; into E5M2 134 us, 82 %,
+// where the arithmetic of the rounding counts too.
 #include <algorithm>
 #include <cmath>
 
@@ -23,7 +25,7 @@ namespace splitzip {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr uint32_t kAhead = 2;
+constexpr uint32_t kAhead = 2;  // units of rows on their way (32,768 tokens into E5M2: 149 us with one, 134)
 constexpr int kMinCtas = 6;
 
 struct RotaryArgs {
@@ -239,7 +241,9 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) kv_rotary_kernel(const 
 
 // Heads that a warp takes for one set of sines and cosines, in units of 32 / LPR:
 // all of them where tokens alone fill the GPU, fewer where the step is small and
-// its latency counts.  (PERWARP)
+// its latency counts.  64 tokens into E5M2 take 4.4 us with a unit a warp and 8.7
+// with all; 4,096 tokens 34.8 and 23.6.  At this many warps the middle is as near:
+// 512 tokens 6.0 (7.4 and 10.8), 2,048 14.7 (18.5 and 14.2).
 constexpr uint64_t kWarpsWanted = 152 * 32;
 
 template <int FMT, bool H>

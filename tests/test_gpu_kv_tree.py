@@ -395,3 +395,41 @@ def test_helpers_refuse_what_does_not_go_together():
         sz.kv_tree_attention(step.cache, step.batch, tree, q, q.half(), bufs, 0.1)
     with pytest.raises(sz.SplitZipError):
         sz.KVTree(Step(BF16, [(1025, 1025)]).batch)
+
+
+@pytest.mark.parametrize("batch,most", [(1, 1), (32, 33), (32, 64), (33, 64), (5, 65), (300, 20), (3, 1024), (40, 200)])
+@pytest.mark.parametrize("window", [0, 1, 40, 700])
+def test_masks_and_positions(batch, most, window):
+    """Of steps that one block takes and of others, ancestors any number of words back, whatever the mask held."""
+    r = random.Random(batch * most + window)
+    sizes = [r.randrange(most + 1) for _ in range(batch - 1)] + [most]
+    lens = [r.randrange(3 * t + 5) for t in sizes]  # some of fewer tokens than the tree
+    parents, bits, positions = [], [], []
+    words = min(32, -(-most // 32) + 1)
+    for b, (t, n) in enumerate(zip(sizes, lens)):
+        up = [[lambda i: i - 1, lambda i: r.randrange(-1, i), lambda i: -1 if i % 3 else r.randrange(-1, i),
+               lambda i: max(-1, i - 1 - r.randrange(40))][b % 4](i) for i in range(t)]
+        lines = []
+        for i, p in enumerate(up):
+            lines.append((lines[p] if p >= 0 else []) + [i])
+            bits.append([sum(1 << (j % 32) for j in (lines[i][-window:] if window else lines[i]) if j // 32 == w)
+                         for w in range(words)])
+            positions.append(n - t + len(lines[i]) - 1)
+        parents += up
+    cu = [sum(sizes[:b]) for b in range(batch + 1)]
+    step = sz.KVBatch(ints(cu), ints(lens), torch.zeros(batch, max(lens) + 1, dtype=torch.int32, device="cuda"),
+                      cu[-1], most, max(max(lens), 1))
+    tree = sz.KVTree(step, window)
+    tree.mask = torch.full((cu[-1], words), -1, dtype=torch.int32, device="cuda")  # wider than it has to be
+    tree.desc.d_mask, tree.desc.words = tree.mask.data_ptr(), words
+    tree.status.fill_(-1)
+    sz.kv_tree(step, ints(parents), tree)
+    assert int(tree.status[0]) == sz.OK
+    assert (tree.mask.long() & 0xFFFFFFFF).tolist() == bits
+    assert tree.position.tolist() == positions
+    if most > 1:
+        parents[cu[-1] - 1] = most - 1  # a parent of its own
+        sz.kv_tree(step, ints(parents), tree)
+        assert int(tree.status[0]) == sz.ERR_INVALID_ARG
+        last = cu[-1] - most
+        assert (tree.mask.long() & 0xFFFFFFFF).tolist() == bits[:last] + [[0] * words] * most
