@@ -662,7 +662,10 @@ int splitzip_kv_tree(const splitzip_kv_batch_t* batch, const int32_t* d_parent, 
  *   - the new tokens that its mask has a bit for (bits past the last are
  *     ignored).
  * Masks and positions are splitzip_kv_tree's, for the same window, or the
- * caller's own.  A row of no place sees nothing. */
+ * caller's own.  A row of no place sees nothing.  Roundings are
+ * splitzip_kv_attention's too, but that over an FP8 cache exp() may be rounded to
+ * FP16 up to 128 rows of a sequence: beside that rounding each product of a
+ * weight and a value may then be off by 2^-24 of the row's largest. */
 int splitzip_kv_tree_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch,
                                const splitzip_kv_tree_t* tree, const splitzip_kv_rows_t* q,
                                const splitzip_kv_rows_t* out, float* d_lse, int dtype, uint32_t q_heads, float scale,

@@ -137,6 +137,7 @@ extern "C" int splitzip_kv_keep(const splitzip_kv_cache_t* h_caches, uint32_t co
     KeepArgs a;
     std::memset(&a, 0, sizeof(a));
     Pools pools[SPLITZIP_MAX_LAYERS];
+    const uint8_t* bases[2 * SPLITZIP_MAX_LAYERS];
     for (uint32_t i = 0; i < count; ++i) {
         const splitzip_kv_cache_t &c = h_caches[i], &o = h_caches[0];
         const int st = check_kv(&c, batch, &a.c, &a.b, true);
@@ -146,7 +147,11 @@ extern "C" int splitzip_kv_keep(const splitzip_kv_cache_t* h_caches, uint32_t co
             c.head_dim != o.head_dim || c.type != o.type)
             return SPLITZIP_ERR_INVALID_ARG;
         pools[i] = Pools{a.c.k, a.c.v, a.c.k_scale, a.c.v_scale};
+        bases[2 * i] = a.c.k, bases[2 * i + 1] = a.c.v;
     }
+    // a pool that is given twice would be moved twice, at once
+    std::sort(bases, bases + 2 * count);
+    if (std::adjacent_find(bases, bases + 2 * count) != bases + 2 * count) return SPLITZIP_ERR_INVALID_ARG;
     if (!d_kept || (reinterpret_cast<uintptr_t>(d_kept) & 3u) || (reinterpret_cast<uintptr_t>(d_path) & 3u) ||
         (!d_path && a.b.tokens > 0))
         return SPLITZIP_ERR_INVALID_ARG;

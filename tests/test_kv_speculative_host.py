@@ -48,8 +48,9 @@ def attend(cache=None, batch=None, tree=None, q=None, out=None, lse=A, dtype=sz.
 
 
 def keep(cache=None, batch=None, count=2, other=None, path=A, kept=A, status=A):
-    array = (sz.KVCacheDesc * max(count, 1))(*[desc(sz.KVCacheDesc, CACHE, dict(cache or {}, **(other or {}) if i else {}))
-                                               for i in range(max(count, 1))])
+    array = (sz.KVCacheDesc * max(count, 1))(*[
+        desc(sz.KVCacheDesc, CACHE, {"d_k": A + 8192 * i, "d_v": A + 8192 * i + 4096, **(cache or {}),
+                                     **(other or {} if i else {})}) for i in range(max(count, 1))])
     return sz.splitzip_kv_keep(array, count, desc(sz.KVBatchDesc, BATCH, batch or {}), path, kept, status, 0)
 
 
@@ -149,6 +150,10 @@ def test_keep_arguments_are_checked(splitzip_lib):
     for kw in (dict(pool_pages=8), dict(page_tokens=8), dict(kv_heads=1), dict(head_dim=64), dict(type=sz.KV_FP8_E4M3),
                dict(page_stride=16 * 3 * 128), dict(token_stride=3 * 128), dict(head_stride=256)):
         assert keep(other=kw) == sz.ERR_INVALID_ARG, kw
+    # a pool given twice would be moved twice
+    for kw in (dict(d_k=A), dict(d_v=A + 4096), dict(d_k=A + 4096), dict(d_v=A)):
+        assert keep(other=kw) == sz.ERR_INVALID_ARG, kw
+    assert keep(count=1, cache=dict(d_v=A)) == sz.ERR_INVALID_ARG
 
 
 def test_frequencies():
