@@ -653,8 +653,7 @@ typedef struct {
 int splitzip_kv_tree(const splitzip_kv_batch_t* batch, const int32_t* d_parent, const splitzip_kv_tree_t* tree,
                      int* d_status, cudaStream_t stream);
 
-/* Attention as splitzip_kv_attention's, its workspace and roundings included,
- * of rows that see
+/* Attention as splitzip_kv_attention's, its workspace included, of rows that see
  *   - every position before the sequence's new tokens, with tree->window only
  *     those after position - window, position being the row's d_position (as the
  *     nearest that a tree can give it, if it is less than the first new token's
@@ -681,8 +680,8 @@ int splitzip_kv_tree_attention(const splitzip_kv_cache_t* cache, const splitzip_
  * A sequence whose entries, path or count (0 .. t) are out of range, or that has
  * new tokens without a place, is left as it was and reported, a page out of
  * range is skipped and reported.  h_caches: host memory, read during the call;
- * everything but the pointers has to be the same in all
- * (SPLITZIP_ERR_INVALID_ARG). */
+ * everything but the pointers has to be the same in all, and no pool is given
+ * twice (SPLITZIP_ERR_INVALID_ARG). */
 int splitzip_kv_keep(const splitzip_kv_cache_t* h_caches, uint32_t count, const splitzip_kv_batch_t* batch,
                      const int32_t* d_path, const int32_t* d_kept, int* d_status, cudaStream_t stream);
 

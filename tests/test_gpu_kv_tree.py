@@ -433,3 +433,48 @@ def test_masks_and_positions(batch, most, window):
         assert int(tree.status[0]) == sz.ERR_INVALID_ARG
         last = cu[-1] - most
         assert (tree.mask.long() & 0xFFFFFFFF).tolist() == bits[:last] + [[0] * words] * most
+
+
+# up to 128 rows of a sequence: trees longer than their sequence, none, of no place, beside keys' units
+TILE = [(12, 12), (10, 3), (0, 9), (16, 1), (9, 0), (32, 300), (11, 140), (1, 128), (20, 129), (17, 256)]
+
+
+@pytest.mark.parametrize("dtype,x", TYPES)
+@pytest.mark.parametrize("dim,page,layout", [(128, 16, "hnd"), (64, 8, "nhd"), (128, 128, "kv"), (64, 1024, "hnd")])
+def test_one_tile_of_rows(dtype, x, dim, page, layout):
+    for window in (0, 1, 9, 130, (1 << 32) - 1):
+        check(Step(dtype, TILE, dim=dim, x=x, page=page, layout=layout, spare_rows=5), window=window, spare=5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("lens", [FEW, TILE, MANY], ids=["few", "tile", "many"])
+def test_two_streams_at_once(dtype, lens):
+    """Two layers' calls with buffers of their own, one tree for both."""
+    steps = [Step(dtype, lens, seed=seed) for seed in (1, 2)]
+    parents = parents_of(steps[0], "random")
+    qs = [torch.randn(s.tokens, 8, s.dim, generator=s.gen).to(s.x).cuda() for s in steps]
+    bufs = [sz.KVAttentionBuffers(s.cache, s.batch, 8) for s in steps]
+    want = [run(s, parents, q, 0.1, bufs=b) for s, q, b in zip(steps, qs, bufs)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    outs = [torch.zeros_like(q) for q in qs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, q, out, b, w, stream in zip(steps, qs, outs, bufs, want, streams):
+            with torch.cuda.stream(stream):
+                out.zero_()
+                sz.kv_tree_attention(s.cache, s.batch, want[0][3], q, out, b, 0.1)
+        torch.cuda.synchronize()
+        for out, b, w in zip(outs, bufs, want):
+            assert int(b.status[0]) == sz.OK and torch.equal(out.view(torch.int16), w[0].view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", [FP16, E4M3])
+@pytest.mark.parametrize("lens", [FEW, TILE, MANY, [(9, 3000), (30, 2000)]], ids=["few", "tile", "many", "shares"])
+def test_results_in_the_queries_place(dtype, lens):
+    step = Step(dtype, lens)
+    parents = parents_of(step, "random")
+    q = torch.randn(step.tokens, 8, step.dim, generator=step.gen).to(step.x).cuda()
+    want, want_lse, _, tree = run(step, parents, q, 0.1)
+    out, lse, status, _ = run(step, parents, q, 0.1, tree=tree, out=q)
+    assert status == sz.OK and out is q and torch.equal(lse, want_lse)
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
