@@ -4,9 +4,12 @@
 // Mathematics: pair j of a row at position p is turned by p f_j turns.  f_j is a
 // fraction of 2^64, so that the low 64 bits of the integer product p f_j are the
 // fraction of a turn, exactly, at any position (in 32-bit floats position
-// 1,000,000 would be off by 0.03 rad and more); its upper 32 bits, signed, make
-// the angle in [-1/2, 1/2) turns, off by 2^-32 of a turn.  The quantised write is
-// kv_rw.cu's, of the 32-bit rotated row: one rounding, of what the cache keeps.
+// 1,000,000 would be off by 0.03 rad and more).  The upper 24 bits, signed, go to
+// sincospi, the next 24 are a small turn after it, to first order.  The quantised
+// write is kv_rw.cu's, of the 32-bit rotated row: one rounding, of what the cache
+// keeps.  (One key element in two million comes out on the other side of a tie, as
+// with sines, cosines and products rounded to 32 bits one after another.  Elements
+// near a tie made again in 64 bits cost 9 to 16 % of the time.)
 //
 // What bounds it: HBM, mostly the queries (in and out).  A warp takes a token and
 // some of its heads, 32 / LPR at a time: head_dim / 16 lanes a row, sixteen
@@ -88,6 +91,15 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], uint2 (&out)[2]
     out[1] = make_uint2(__byte_perm(q[4], q[5], 0x5410), __byte_perm(q[6], q[7], 0x5410));
 }
 
+// Of an angle of `turn` / 2^64 turns, times the magnitude.
+__device__ __forceinline__ void sine_cosine(uint64_t turn, float magnitude, float* s, float* c) {
+    float s0, c0;
+    sincospif(float(int32_t(turn >> 32) & ~0xFF) * 0x1p-31f, &s0, &c0);
+    const float rest = float(uint32_t(turn >> 16) & 0xFFFFFFu) * (3.14159265358979f * 0x1p-47f);
+    *c = fmaf(-s0, rest, c0) * magnitude;
+    *s = fmaf(c0, rest, s0) * magnitude;
+}
+
 // FMT 0: 16-bit cache, 1: E5M2, 2: E4M3.  H: rows in FP16, else BF16.  LPR lanes
 // hold a row.  INTER: pairs of neighbours, else of the two halves.
 template <int FMT, bool H, int LPR, bool INTER>
@@ -142,9 +154,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) kv_rotary_kernel(const 
                     const uint32_t pair = lane * kMade + i;
                     if (2 * pair < a.rot) {
                         const uint64_t turn = __ldg(a.turns + pair) * uint64_t(pos);
-                        sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &s[i], &c[i]);
-                        c[i] *= a.magnitude;
-                        s[i] *= a.magnitude;
+                        sine_cosine(turn, a.magnitude, &s[i], &c[i]);
                     }
                 }
 #pragma unroll

@@ -1,10 +1,10 @@
 """GPU: rotary positions with the write into the cache, against the formula in
 64 bits, element by element.
 
-Errors counted.  The angle: the fraction of a turn is cut to 32 bits and
-rounded to 24 bits of at most half a turn (2^-25 turns, 2^-22.3 rad), the sine
-and cosine are off by two units of their last place at most (2^-22): together
-2^-21.  Their product with the magnitude, two products and a sum add four
+Errors counted.  The angle: 24 bits of the fraction of a turn exactly and 24
+more to first order (under 2^-40 rad off), a rounding of 2^-25 with them; the
+sine and cosine are off by two units of their last place at most (2^-22): at
+most 2^-21 together.  Their product with the magnitude, two products and a sum add four
 roundings of 2^-24.  So an element of a pair (a, b) is off by at most
 2^-20 * magnitude * (|a| + |b|) before it is rounded to its type."""
 import math
