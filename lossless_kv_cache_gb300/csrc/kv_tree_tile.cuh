@@ -32,12 +32,12 @@
 // TMEM: S0, S1 (128 columns each, the weights overwrite the scores), O0, O1.
 //
 // Measured in a graph (32 query heads of 128 over 8, pages of 16): 32 trees of 16
-// over 4,096 take 113 us over BF16 (4.9 TB/s, 73 % of a copy's rate; the chunk
-// kernel 157 for as many rows) and 127 over E5M2 (the chunk kernel 210).  With 16
-// bits a piece's start and end cost most of what is missing: about 10 us, once or
-// twice a CTA.  With FP8 a unit costs some 3,100 cycles: converters, softmax and
-// products take the shared memory's and the issue slots' time from one another
-// (the 16-bit unit 2,000), so half the bytes are no faster.
+// over 4,096 take 113 us over BF16 (4.9 TB/s, 73 % of a copy's rate) and 127 over
+// E5M2 (kv_chunk.cuh's kernel with masks 210).  With 16 bits a unit takes about
+// 1.3 us, which is HBM's; a CTA's first piece starts after 5 to 6 us, a piece's end
+// costs 3 to 6.  With FP8 a unit takes 1.5 us, 2,900 cycles, half the bytes for
+// nothing: a chain of conversion, scores, softmax and product in which neither the
+// tensor pipe (24 %) nor the issue slots (40 %) nor shared memory is full.
 // Roles stay small, with rolled loops and one place for each step: when their
 // unrolled code did not fit the instruction caches together, every role was slow
 // (262 us over E5M2).
