@@ -34,8 +34,8 @@ constexpr uint64_t kStepRowsMax = 32;
 //   BF16, 1 sequence of 2,000     13 / 18     21       E5M2    14 / 17     24
 //   BF16, 1 of 16,000             30 / 32     30       E5M2    35 / 38     33
 //   BF16, 8 of 4,000              39 / 49     39       E5M2    38 / 53     44
-//   BF16, 64 of 2,000            101 / 178   111       E5M2    95 / 164   140
-//   BF16, 200 of 1,000           149 / 276   184       E5M2   151 / 265   288
+//   BF16, 64 of 2,000            101 / 178   111       E5M2    95 / 164   137
+//   BF16, 200 of 1,000           149 / 276   183       E5M2   151 / 265   282
 constexpr uint64_t kTreeStepRowsMax = 16;
 
 struct Plan {
