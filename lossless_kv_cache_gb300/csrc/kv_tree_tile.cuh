@@ -8,10 +8,11 @@
 // which a row takes into the one factor of its scores and into its reference,
 // the maximum of s + EV; its sums l are of 2^(s-ref).  FP16 holds what they make
 // exactly (E5M2's elements are 2^-16 and more, 2^-22 with scales 2^kSpread apart).
-// Where scales differ by more than 2^kSpread, or EV from the piece's first by
-// more than 2^30, the keys keep scales of their own, as in kv_step.cuh: K's go to the scores, V's to the
-// weights, and rows of zeros, whose scale says nothing of their size, count as
-// e = -80 with the weight 0.  So no key takes precision from another.
+// Where scales differ by more than 2^kSpread, EV from the piece's first by more
+// than 2^30, or V has a row of scale 2^0, which may be zeros, the keys keep scales of their own, as in
+// kv_step.cuh: K's go to the scores, V's to the weights, and rows of zeros, whose
+// scale says nothing of their size, count as e = -80 with the weight 0.  So no
+// key takes precision from another.
 //
 // What bounds it: up to some 290 rows the bytes of the cache, so it is built to
 // keep them coming.  A CTA's two softmax groups take every other unit of 128
@@ -299,7 +300,7 @@ __device__ __forceinline__ void scale_role(const AttentionArgs& a, typename C::S
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        int v_first = 127;
+        int v_first = 0;  // EV's byte of the first unit that has one
 #pragma unroll 1
         for (int j = 0; j < C::kScaleUnits; ++j) ask(j, look_up(j));
         int32_t found = look_up(C::kScaleUnits);
@@ -318,24 +319,35 @@ __device__ __forceinline__ void scale_role(const AttentionArgs& a, typename C::S
                 k_now[i] = in ? sh.raw_scale[u % 8u][0][32 * i + int(lane)] : 0u;
                 v_now[i] = in ? sh.raw_scale[u % 8u][1][32 * i + int(lane)] : 0u;
             }
+            // Rows of V with the scale 2^0, kv_write's for rows of zeros, say nothing of V's size until
+            // they have been looked at: they have no part in EV, and their unit's keys keep scales
+            // of their own.
             uint32_t most[2] = {0, 0}, least[2] = {255, 255};
+            bool zeros = false;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 most[0] = max(most[0], k_now[i]);
-                most[1] = max(most[1], v_now[i]);
                 if (k_now[i]) least[0] = min(least[0], k_now[i]);
-                if (v_now[i]) least[1] = min(least[1], v_now[i]);
+                if (v_now[i] == 127u) {
+                    zeros = true;
+                } else if (v_now[i]) {
+                    most[1] = max(most[1], v_now[i]);
+                    least[1] = min(least[1], v_now[i]);
+                }
             }
+            zeros = __any_sync(~0u, zeros);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 most[i] = __reduce_max_sync(~0u, most[i]);
                 least[i] = __reduce_min_sync(~0u, least[i]);
-                if (most[i] == 0) most[i] = least[i] = 127;
             }
+            if (v_first == 0) v_first = int(most[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (most[i] == 0) most[i] = least[i] = 127;
             const int v_most = int(most[1]);
-            if (j == 0) v_first = v_most;
-            const bool own = int(most[0] - least[0]) > C::kSpread || int(most[1] - least[1]) > C::kSpread ||
-                             least[1] < 47u || most[1] > 237u || abs(v_most - v_first) > 30;
+            const bool own = zeros || int(most[0] - least[0]) > C::kSpread || int(most[1] - least[1]) > C::kSpread ||
+                             least[1] < 47u || most[1] > 237u || (v_first > 0 && abs(v_most - v_first) > 30);
             if (ok) ok = C::template await<C::kFactors>(sh.scale_freed, u);
             ok = __all_sync(~0u, ok);
             if (ok) {
