@@ -519,8 +519,10 @@ int splitzip_kv_attention_workspace_size(const splitzip_kv_cache_t* cache, const
  * V's scales, and keep all bits down to 2^-28 of a row's largest such product
  * (rows of zeros aside), with scales under 2^-80 counted as 2^-80: V rows
  * smaller than that (elements below 1e-20) lose bits, and vanish from 2^-119
- * on.  With more rows, FP16 queries over an FP8 cache take values of V beyond
- * 131,008 as infinite.
+ * on.  The scales of V that a row sees, so counted, are to be within 2^100 of
+ * one another: weights of keys with smaller values yet may be missing from lse
+ * and from what the sums are divided by.  With more rows, FP16 queries over an
+ * FP8 cache take values of V beyond 131,008 as infinite.
  * d_ws: ws_bytes >= splitzip_kv_attention_workspace_size, 16-byte aligned,
  * contents need not be initialised; calls that share it must not overlap on
  * the GPU.  Results do not depend on the order in which blocks run. */

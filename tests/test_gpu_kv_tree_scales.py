@@ -1,5 +1,5 @@
 """GPU: tree attention over FP8 pages whose scales say little of the values'
-size: whole units of rows of zeros."""
+size, whole units of rows of zeros, or differ far from unit to unit."""
 import math
 
 import pytest
@@ -64,5 +64,36 @@ def test_units_of_nothing_but_zeros(dtype, dim, small, where):
     for b in range(20):
         set_rows(step, "k", b, positions, row)
         set_rows(step, "v", b, positions, torch.zeros(dim, dtype=torch.float64))
+    out, _ = run(step, q.cuda(), scale)
+    own_size(step, q, out, attention64(step, q, scale), scale)
+
+
+@pytest.mark.parametrize("dtype", [E5M2, E4M3])
+@pytest.mark.parametrize("at", [5, 300, 500])
+def test_a_value_that_dwarfs_the_ones_after_it(dtype, at):
+    """The sum of weights is of every key, down to values 2^100 smaller than another's."""
+    step, q, scale, row = aligned_step(dtype, 128, [(5, 897)] * 20)
+    shift_scales(step, "v", -30)
+    large = torch.ldexp(torch.sign(torch.randn(128, generator=step.gen, dtype=torch.float64)), torch.tensor(70))
+    for b in range(20):
+        set_rows(step, "k", b, [at], row)
+        set_rows(step, "v", b, [at], large)
+    out, _ = run(step, q.cuda(), scale)
+    own_size(step, q, out, attention64(step, q, scale), scale)
+
+
+@pytest.mark.parametrize("dtype,dim", [(E5M2, 128), (E4M3, 64)])
+@pytest.mark.parametrize("seed", range(3))
+def test_units_of_any_scale(dtype, dim, seed):
+    step, q, scale, _ = aligned_step(dtype, dim, [(5, 897)] * 20)
+    jumps = torch.tensor([-55, -31, 0, 31, 40])
+    for b in range(20):
+        e = jumps[torch.randint(len(jumps), (8,), generator=torch.Generator().manual_seed(31 * seed + b))]
+        at = torch.tensor([step.place(b, pos) for pos in range(897)])
+        by = e[torch.arange(897) // 128]
+        step.host["v"][at[:, 0], at[:, 1]] = torch.ldexp(step.host["v"][at[:, 0], at[:, 1]], by[:, None, None])
+        scales = step.cache.v_scale.transpose(1, 2)
+        at = at.cuda()
+        scales[at[:, 0], at[:, 1]] = (scales[at[:, 0], at[:, 1]].int() + by.cuda()[:, None].int()).to(torch.uint8)
     out, _ = run(step, q.cuda(), scale)
     own_size(step, q, out, attention64(step, q, scale), scale)
