@@ -316,8 +316,9 @@ __device__ __forceinline__ void scale_role(const AttentionArgs& a, typename C::S
             for (int i = 0; i < 4; ++i) {
                 const int pos = (first_unit + j) * kUnit + 32 * i + int(lane);
                 const bool in = pos >= lo && pos < hi;
-                k_now[i] = in ? sh.raw_scale[u % 8u][0][32 * i + int(lane)] : 0u;
-                v_now[i] = in ? sh.raw_scale[u % 8u][1][32 * i + int(lane)] : 0u;
+                // a slot that nothing was written to may hold 255, and 0 times infinity is NaN
+                k_now[i] = in ? min(uint32_t(sh.raw_scale[u % 8u][0][32 * i + int(lane)]), 254u) : 0u;
+                v_now[i] = in ? min(uint32_t(sh.raw_scale[u % 8u][1][32 * i + int(lane)]), 254u) : 0u;
             }
             // Rows of V with the scale 2^0, kv_write's for rows of zeros, say nothing of V's size until
             // they have been looked at: they have no part in EV, and their unit's keys keep scales

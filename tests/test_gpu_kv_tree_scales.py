@@ -5,8 +5,11 @@ import math
 import pytest
 import torch
 
+import lossless_kv_cache_gb300 as sz
 from tests.kv_long_reference import LongStep, attention64
-from tests.kv_reference import RAW, quantise
+from tests.kv_reference import RAW, Step, check_attention, quantise
+from tests.test_gpu_kv_tree import attention, parents_of, seen_by_tree
+from tests.test_gpu_kv_tree import run as run_tree
 from tests.test_gpu_kv_tree_long import own_size, run
 from tests.test_gpu_kv_weights import shift_scales
 
@@ -97,3 +100,24 @@ def test_units_of_any_scale(dtype, dim, seed):
         scales[at[:, 0], at[:, 1]] = (scales[at[:, 0], at[:, 1]].int() + by.cuda()[:, None].int()).to(torch.uint8)
     out, _ = run(step, q.cuda(), scale)
     own_size(step, q, out, attention64(step, q, scale), scale)
+
+
+@pytest.mark.parametrize("dtype", [E5M2, E4M3])
+@pytest.mark.parametrize("t,before", [(2, 70), (7, 200), (30, 70), (70, 60)], ids=["8", "28", "120", "280"])
+def test_scales_of_slots_that_a_row_does_not_see(dtype, t, before):
+    """Whatever was left in them, 0 and 255 too, with the number of rows that each kernel takes."""
+    for k_scale, v_scale in ((255, 255), (127, 255), (255, 127), (0, 0), (255, 0), (254, 254)):
+        step = Step(dtype, [(t, t + before), (1, 5)])
+        parents = parents_of(step, "roots")  # of t tokens, each sees itself alone
+        hidden = [0, t - 1]
+        for i in hidden:
+            pg, off = step.place(0, before + i)
+            step.cache.k_scale[pg, :, off] = k_scale
+            step.cache.v_scale[pg, :, off] = v_scale
+        q = torch.randn(step.tokens, 8, step.dim, generator=step.gen).to(step.x)
+        out, lse, status, _ = run_tree(step, parents, q, 0.1)
+        assert status == sz.OK
+        ref = attention(step, q, 0.1, seen_by_tree(step, parents, 0))
+        keep = torch.tensor([r for r in range(step.tokens) if r not in hidden], dtype=torch.long)
+        if len(keep) > 0:
+            check_attention(step, out.cpu()[keep], lse.cpu()[keep], [x[keep] for x in ref], BF16)
