@@ -682,8 +682,9 @@ int splitzip_kv_tree_attention(const splitzip_kv_cache_t* cache, const splitzip_
  * A sequence whose entries, path or count (0 .. t) are out of range, or that has
  * new tokens without a place, is left as it was and reported, a page out of
  * range is skipped and reported.  h_caches: host memory, read during the call;
- * everything but the pointers has to be the same in all, and no pool is given
- * twice (SPLITZIP_ERR_INVALID_ARG). */
+ * everything but the pointers has to be the same in all, and no pool and, of an
+ * FP8 type, no array of scales is given twice (SPLITZIP_ERR_INVALID_ARG), nor
+ * may they share elements otherwise. */
 int splitzip_kv_keep(const splitzip_kv_cache_t* h_caches, uint32_t count, const splitzip_kv_batch_t* batch,
                      const int32_t* d_path, const int32_t* d_kept, int* d_status, cudaStream_t stream);
 

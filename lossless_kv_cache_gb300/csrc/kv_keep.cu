@@ -137,7 +137,6 @@ extern "C" int splitzip_kv_keep(const splitzip_kv_cache_t* h_caches, uint32_t co
     KeepArgs a;
     std::memset(&a, 0, sizeof(a));
     Pools pools[SPLITZIP_MAX_LAYERS];
-    const uint8_t* bases[2 * SPLITZIP_MAX_LAYERS];
     for (uint32_t i = 0; i < count; ++i) {
         const splitzip_kv_cache_t &c = h_caches[i], &o = h_caches[0];
         const int st = check_kv(&c, batch, &a.c, &a.b, true);
@@ -147,11 +146,15 @@ extern "C" int splitzip_kv_keep(const splitzip_kv_cache_t* h_caches, uint32_t co
             c.head_dim != o.head_dim || c.type != o.type)
             return SPLITZIP_ERR_INVALID_ARG;
         pools[i] = Pools{a.c.k, a.c.v, a.c.k_scale, a.c.v_scale};
-        bases[2 * i] = a.c.k, bases[2 * i + 1] = a.c.v;
     }
-    // a pool that is given twice would be moved twice, at once
-    std::sort(bases, bases + 2 * count);
-    if (std::adjacent_find(bases, bases + 2 * count) != bases + 2 * count) return SPLITZIP_ERR_INVALID_ARG;
+    // what is given twice would be moved twice, at once
+    const uint8_t* bases[2 * SPLITZIP_MAX_LAYERS];
+    const auto twice = [&](uint8_t* Pools::*k, uint8_t* Pools::*v) {
+        for (uint32_t i = 0; i < count; ++i) bases[2 * i] = pools[i].*k, bases[2 * i + 1] = pools[i].*v;
+        std::sort(bases, bases + 2 * count);
+        return std::adjacent_find(bases, bases + 2 * count) != bases + 2 * count;
+    };
+    if (twice(&Pools::k, &Pools::v)) return SPLITZIP_ERR_INVALID_ARG;
     if (!d_kept || (reinterpret_cast<uintptr_t>(d_kept) & 3u) || (reinterpret_cast<uintptr_t>(d_path) & 3u) ||
         (!d_path && a.b.tokens > 0))
         return SPLITZIP_ERR_INVALID_ARG;
@@ -160,9 +163,10 @@ extern "C" int splitzip_kv_keep(const splitzip_kv_cache_t* h_caches, uint32_t co
     a.status = d_status;
     int sms, st;
     if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;
+    const bool fp8 = a.c.type == SPLITZIP_KV_FP8_E5M2 || a.c.type == SPLITZIP_KV_FP8_E4M3;
+    if (fp8 && twice(&Pools::k_scale, &Pools::v_scale)) return SPLITZIP_ERR_INVALID_ARG;
     // the sequences' entries are looked at by the kernels themselves
     cudaError_t e = launch_kv_begin(KvBatch{}, d_status, nullptr, 0, stream);
-    const bool fp8 = a.c.type == SPLITZIP_KV_FP8_E5M2 || a.c.type == SPLITZIP_KV_FP8_E4M3;
     for (uint32_t i = 0; i < count && e == cudaSuccess; i += kLayers) {
         const uint32_t n = std::min(kLayers, count - i);
         std::memcpy(a.layer, pools + i, n * sizeof(Pools));

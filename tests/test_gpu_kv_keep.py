@@ -173,3 +173,24 @@ def test_helpers_refuse_what_does_not_go_together():
     other = Step(BF16, [(3, 9), (2, 8)], page=4)
     with pytest.raises(sz.SplitZipError):
         sz.kv_keep(sz.KVLayers([step.cache, other.cache]), step.batch, path, kept, step.status)
+
+
+@pytest.mark.parametrize("dtype", [E5M2, E4M3])
+def test_scales_given_twice_are_refused(dtype):
+    """They would be moved twice, at once; nothing is launched."""
+    step = Step(dtype, [(5, 30), (2, 8)])
+    other = layers_of(step, 2)[1]
+    a = step.cache
+    path, kept = ints([1, 3, 4, 0, 0, 1, 0]), ints([3, 1])
+    for caches in ([sz.KVCache(a.k, a.v, a.k_scale, a.k_scale)],
+                   [a, sz.KVCache(other.k, other.v, a.k_scale, other.v_scale)],
+                   [a, sz.KVCache(other.k, other.v, other.k_scale, a.v_scale)],
+                   [a, sz.KVCache(other.k, other.v, a.v_scale, other.v_scale)]):
+        before = [bits(c) for c in caches]
+        step.status.fill_(-1)
+        with pytest.raises(sz.SplitZipError):
+            sz.kv_keep(sz.KVLayers(caches), step.batch, path, kept, step.status)
+        torch.cuda.synchronize()
+        assert int(step.status[0]) == -1
+        assert all(torch.equal(x, y) for c, old in zip(caches, before) for x, y in zip(bits(c), old))
+    check(Step(dtype, LENS), 2)
