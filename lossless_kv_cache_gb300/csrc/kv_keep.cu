@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_keep_kernel(const __grid_const
         const KvSeq s = load_seq(a.b, uint32_t(seq));
         const int kept = a.kept[seq], first = s.n - s.t;
         const int32_t* path = a.path + s.row0;
-        bad = !s.ok || kept < 0 || kept > s.t || (kept > 0 && first < 0);
+        bad = !s.ok || kept < 0 || kept > s.t || (s.t > 0 && first < 0);
         if (!bad) {
             for (int i0 = 0; i0 < kept; i0 += 32) {
                 const int i = i0 + int(lane);

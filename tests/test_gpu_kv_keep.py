@@ -194,3 +194,13 @@ def test_scales_given_twice_are_refused(dtype):
         assert int(step.status[0]) == -1
         assert all(torch.equal(x, y) for c, old in zip(caches, before) for x, y in zip(bits(c), old))
     check(Step(dtype, LENS), 2)
+
+
+@pytest.mark.parametrize("kept", [0, 1, 4])
+def test_tokens_without_a_place_are_reported_whatever_is_kept(kept):
+    step = Step(E5M2, [(4, 3), (3, 20), (0, 0)])
+    before = bits(step.cache)
+    path = [0, 1, 2, 3, 1, 2, 0]
+    sz.kv_keep(sz.KVLayers([step.cache]), step.batch, ints(path), ints([kept, 2, 0]), step.status)
+    assert int(step.status[0]) == sz.ERR_INVALID_ARG
+    assert all(torch.equal(a, b) for a, b in zip(bits(step.cache), moved(step, before, path, [0, 2, 0])))
