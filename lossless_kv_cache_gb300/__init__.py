@@ -784,17 +784,22 @@ class KVBatch:
         self.table_pages = page_table.shape[1]
         self.cu_tokens, self.kv_len, self.page_table = cu_tokens, kv_len, page_table
         self.tokens, self.max_kv_len = tokens, max_kv_len
+        self.pages = None  # the KVPages that the table is of, where known
         self.desc = KVBatchDesc(cu_tokens.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.stride(0),
                                 batch, tokens, max_tokens, max_kv_len)
 
     def check(self, cache):
-        """Raises where the step is on another device than the cache, and where the page
-        table is narrower than max_kv_len tokens need."""
+        """Raises where the step is on another device than the cache, where the page table is
+        narrower than max_kv_len tokens need, and where it is of pages unlike the cache's."""
         if self.device != cache.device:
             raise ValueError("cache on cuda:%d and step on cuda:%d: expected one device" % (cache.device, self.device))
         if self.table_pages * cache.page_tokens < self.max_kv_len:
             raise SplitZipError(ERR_INVALID_ARG, "page_table of %d pages for %d tokens"
                                 % (self.table_pages, self.max_kv_len))
+        pages = self.pages
+        if pages is not None and (pages.page_tokens != cache.page_tokens or pages.desc.pool_pages > cache.desc.pool_pages):
+            raise ValueError("step over a pool of %d pages of %d tokens: expected a cache of as many and such, got %d of %d"
+                             % (pages.desc.pool_pages, pages.page_tokens, cache.desc.pool_pages, cache.page_tokens))
 
 
 _ROW_TYPES = {}
@@ -969,8 +974,11 @@ class KVStep:
         self.device = self.cu_tokens.get_device()
 
     def batch_of(self, pages):
-        """The KVBatch of this step over `pages`, as kv_extend left them."""
-        return KVBatch(self.cu_tokens, pages.kv_len, pages.table, self.tokens, self.max_tokens, self.max_kv_len)
+        """The KVBatch of this step over `pages`, as kv_extend left them: for caches of pages
+        of the same size, and of as many at least."""
+        batch = KVBatch(self.cu_tokens, pages.kv_len, pages.table, self.tokens, self.max_tokens, self.max_kv_len)
+        batch.pages = pages
+        return batch
 
 
 def kv_extend(pages, new, step, drop=None, after=None, stream=None):

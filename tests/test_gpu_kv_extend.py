@@ -296,3 +296,28 @@ def test_helpers_refuse_what_does_not_go_together():
         sz.KVPages(pages.free, pages.count, pages.table[:1].expand(3, -1), pages.held, pages.kv_len, 16)
     sz.kv_extend(pages, good, step)
     assert int(step.status[0]) == sz.OK and pages.kv_len.tolist() == [1, 0, 0]
+
+
+def test_a_step_is_of_its_pages():
+    """With pages of another size the table's entries past a sequence's pages would be taken for its own."""
+    pages = sz.KVPages.empty(8, 32, 2, 120)
+    pages.table = torch.zeros(2, 8, dtype=torch.int32, device="cuda")
+    pages = sz.KVPages(pages.free, pages.count, pages.table, pages.held, pages.kv_len, 32)
+    step = sz.KVStep(2, 4, 2, 120)
+    batch = step.batch_of(pages)
+    sz.kv_extend(pages, ints([2, 1]), step)
+    rows = torch.zeros(4, 2, 128, dtype=torch.bfloat16, device="cuda")
+    status = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    for many, size in ((8, 16), (16, 16), (8, 64), (7, 32)):
+        cache = sz.KVCache.empty(many, size, 2, 128, torch.bfloat16)
+        rotary = sz.KVRotary(sz.rotary_frequencies(128))
+        for call in (lambda: sz.kv_write(cache, batch, rows, rows, status),
+                     lambda: sz.kv_rotary_write(cache, batch, rotary, None, None, rows, rows, status),
+                     lambda: sz.kv_tree_attention(cache, batch, sz.KVTree(batch), rows, rows.clone(), None, 0.1),
+                     lambda: sz.kv_keep(sz.KVLayers([cache]), batch, ints([0] * 4), ints([0, 0]), status)):
+            with pytest.raises(ValueError):
+                call()
+    assert int(status[0]) == -1
+    for many in (8, 9):
+        sz.kv_write(sz.KVCache.empty(many, 32, 2, 128, torch.bfloat16), batch, rows, rows, status)
+        assert int(status[0]) == sz.OK
