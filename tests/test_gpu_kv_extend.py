@@ -321,3 +321,19 @@ def test_a_step_is_of_its_pages():
     for many in (8, 9):
         sz.kv_write(sz.KVCache.empty(many, 32, 2, 128, torch.bfloat16), batch, rows, rows, status)
         assert int(status[0]) == sz.OK
+
+
+@pytest.mark.parametrize("room", [4095, 4096, 4097, 4100])
+@pytest.mark.parametrize("short", [0, 1, 3000])
+@pytest.mark.parametrize("batch", [5, 300])
+def test_either_side_of_the_room_that_the_planning_block_maps(room, short, batch):
+    """Up to 4,096 rows that there is room for are mapped by the block that plans, however many there are."""
+    lists = Lists(5000, 16, batch, 700, 3)
+    lists.fill([100, 0, 33, 16, 7] * (batch // 5))
+    pages = lists.on_gpu()
+    before = pages.table.tolist()
+    new = [room - short - batch + 2] + [0] + [1] * (batch - 2)
+    step = step_for(batch, room, max(new), 12000)
+    expected = lists.extend(new, [0] * batch)
+    sz.kv_extend(pages, ints(new), step)
+    check(lists, pages, step, expected, before)
