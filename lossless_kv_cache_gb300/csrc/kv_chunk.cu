@@ -9,8 +9,6 @@ uint32_t chunk_ctas(uint64_t rows, uint64_t batch, uint64_t kv_heads, uint64_t k
     return uint32_t(std::min<uint64_t>(kChunkCtas, std::max<uint64_t>(1, units)));
 }
 
-uint64_t chunk_part_floats(uint32_t head_dim) { return uint64_t(kRows) * (head_dim + 2); }
-
 uint64_t chunk_plan_bytes(uint32_t ctas) { return plan_bytes(ctas) + uint64_t(ctas) * sizeof(ChunkSplit); }
 
 int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s) {

@@ -69,6 +69,7 @@ namespace {
 constexpr int kUnit = 128;       // keys
 constexpr int kTileRows = 128;   // rows of a softmax group
 constexpr int kRows = 2 * kTileRows;
+static_assert(kRows == kChunkRows, "rows of a part");
 constexpr uint32_t kChunkCtas = 152;  // one on each SM
 constexpr int kPlanThreads = 1024;
 // What an item costs beside its keys (its rows of Q in and results out, the
@@ -795,10 +796,17 @@ __device__ __noinline__ void note_special(const uint8_t* v, Seen seen, Reached<D
 }
 
 // Where a CTA's part of an item that CTA `first` begins is, of tile g: columns
-// o[0] .. o[D - 1], reference, sum of kTileRows floats each.
-template <int D>
+// o[0] .. o[D - 1], reference, sum of kTileRows floats each (or of as many as a slot of fewer rows has).
+template <int D, bool TREE>
 __device__ __forceinline__ float* part_at(const AttentionArgs& a, uint32_t cta, uint32_t first, uint32_t g) {
-    return a.parts + ((uint64_t(cta) * 2 + (cta == first ? 1 : 0)) * 2 + g) * (kTileRows * (D + 2));
+    return a.parts + (uint64_t(cta) * 2 + (cta == first ? 1 : 0)) * ((TREE ? a.part_rows : kRows) * (D + 2)) +
+           g * (kTileRows * (D + 2));
+}
+
+// From a column of a part to the next.
+template <bool TREE>
+__device__ __forceinline__ int part_stride(const AttentionArgs& a) {
+    return TREE ? int(min(a.part_rows, uint32_t(kTileRows))) : kTileRows;
 }
 
 // The natural logarithm of a row's sum of exponentials l against reference m.
@@ -1107,19 +1115,20 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             put(low, sum);
         } else {
             const bool live = int(row) + g * kTileRows < w.rows;
-            float* mine = part_at<D>(a, blockIdx.x, first, uint32_t(g)) + row;
+            float* mine = part_at<D, TREE>(a, blockIdx.x, first, uint32_t(g)) + row;
+            const int stride = part_stride<TREE>(a);
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
                 float o[32];
                 sums32(k, o);
                 if (live) {
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) mine[(32 * k + y) * kTileRows] = o[y];
+                    for (int y = 0; y < 32; ++y) mine[(32 * k + y) * stride] = o[y];
                 }
             }
             if (live) {
-                mine[D * kTileRows] = low;
-                mine[(D + 1) * kTileRows] = sum;
+                mine[D * stride] = low;
+                mine[(D + 1) * stride] = sum;
             }
         }
         // the loads of O are done before the next piece's product overwrites it
@@ -1201,7 +1210,7 @@ __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
 // the one that wrote the last of them.
 constexpr int kJoinParts = 2, kJoinColumns = 8, kJoinThreads = kJoinParts * kJoinColumns * 32;
 
-template <bool H, int D>
+template <bool H, int D, bool TREE>
 __global__ void __launch_bounds__(kJoinThreads)
     kv_chunk_join_kernel(const __grid_constant__ AttentionArgs a, const ChunkSplit* splits, float value_scale,
                          float scale, float shift) {
@@ -1214,21 +1223,22 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (int(blockIdx.y) * 32 >= w.rows) return;
     const int row = int(blockIdx.y * 32u + lane);  // those past the last read what is there, and write nothing
     const uint32_t g = uint32_t(row) / kTileRows, at = uint32_t(row) % kTileRows;
+    const int stride = part_stride<TREE>(a);
     float m = -INFINITY, l = 0.f;
 #pragma unroll 8
-    for (uint32_t cta = first; cta <= w.last_cta; ++cta) m = fmaxf(m, part_at<D>(a, cta, first, g)[D * kTileRows + at]);
+    for (uint32_t cta = first; cta <= w.last_cta; ++cta) m = fmaxf(m, part_at<D, TREE>(a, cta, first, g)[D * stride + int(at)]);
     float o[kColumns];
 #pragma unroll
     for (int y = 0; y < kColumns; ++y) o[y] = 0.f;
 #pragma unroll 2
     for (uint32_t cta = first + uint32_t(part0); cta <= w.last_cta; cta += kJoinParts) {
-        const float* part = part_at<D>(a, cta, first, g) + at;
+        const float* part = part_at<D, TREE>(a, cta, first, g) + at;
         float x[kColumns];
 #pragma unroll
-        for (int y = 0; y < kColumns; ++y) x[y] = part[(col0 + y) * kTileRows];
+        for (int y = 0; y < kColumns; ++y) x[y] = part[(col0 + y) * stride];
         // parts of no reference (a scale of about zero leaves it there) count as they are
-        const float mc = part[D * kTileRows], e = exp2_fast((mc - m) * scale), f = mc == m ? 1.f : e;
-        l += f * part[(D + 1) * kTileRows];
+        const float mc = part[D * stride], e = exp2_fast((mc - m) * scale), f = mc == m ? 1.f : e;
+        l += f * part[(D + 1) * stride];
 #pragma unroll
         for (int y = 0; y < kColumns; ++y) o[y] += f * x[y];
     }
@@ -1281,7 +1291,7 @@ int launch(const AttentionArgs& a, ChunkPlan* plan, const ChunkMaps& maps, uint3
     ChainedLaunch join(dim3(ctas, kRows / 32), dim3(kJoinThreads), 0, s);
     if (cudaLaunchKernelEx(&l.cfg, kv_chunk_kernel<FMT, H, D, TREE>, a, static_cast<const ChunkPlan*>(plan), splits, maps) !=
             cudaSuccess ||
-        cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<H, D>, a, static_cast<const ChunkSplit*>(splits),
+        cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<H, D, TREE>, a, static_cast<const ChunkSplit*>(splits),
                            C::kValueScale, a.scale_log2, C::kShift) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;

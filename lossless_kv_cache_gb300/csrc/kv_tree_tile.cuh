@@ -858,7 +858,8 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
         const uint32_t first = w.first_cta, last = w.last_cta;
         const bool whole = first == last, live = int(row) < w.rows;
         const float inv = l == 0.f ? 0.f : 1.f / (l * (1 << C::kRoom));
-        float* part = part_at<D>(a, blockIdx.x, first, 0) + row;
+        float* part = part_at<D, true>(a, blockIdx.x, first, 0) + row;
+        const int stride = part_stride<true>(a);
         // an infinity or NaN stays one whatever the factor
         const auto times = [](float o, float f) { return fabsf(o) < INFINITY ? o * f : o; };
 #pragma unroll 1
@@ -888,12 +889,12 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
                 }
             } else if (live) {
 #pragma unroll
-                for (int y = 0; y < 16; ++y) part[(col + y) * kTileRows] = o[y];
+                for (int y = 0; y < 16; ++y) part[(col + y) * stride] = o[y];
             }
         }
         if (!whole && live && g == 0) {
-            part[D * kTileRows] = m;
-            part[(D + 1) * kTileRows] = l;
+            part[D * stride] = m;
+            part[(D + 1) * stride] = l;
         }
         if (whole) {
             ok = named_barrier_and(4, 256, ok);
@@ -1037,9 +1038,9 @@ int launch_tile(const AttentionArgs& a, ChunkPlan* plan_at, const ChunkMaps& map
     const float scale = C::kFp8 ? 1.f : a.scale_log2, value_scale = float(1 << C::kRoom), shift = C::kShift;
     cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv_tree_tile_kernel<FMT, H, D>, a, plan, splits, maps);
     if (e == cudaSuccess)
-        e = out_half ? cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<true, D>, a,
+        e = out_half ? cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<true, D, true>, a,
                                           static_cast<const ChunkSplit*>(splits), value_scale, scale, shift)
-                     : cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<false, D>, a,
+                     : cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<false, D, true>, a,
                                           static_cast<const ChunkSplit*>(splits), value_scale, scale, shift);
     if (e != cudaSuccess) cudaGetLastError();
     return e == cudaSuccess ? int(SPLITZIP_OK) : int(SPLITZIP_ERR_CUDA);

@@ -214,3 +214,26 @@ def test_looks_at_its_own_values(dtype):
             for _ in range(25):
                 out, lse = run(step, q, 0.03)
                 assert torch.equal(out.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("page", [4, 16])
+@pytest.mark.parametrize("lens,kv_heads,group", [([(5, 9000)], 1, 4), ([(8, 3000)] * 12, 2, 4), ([(32, 2500), (3, 7000)], 3, 1),
+                                                 ([(2, 600), (1, 300)] * 16, 1, 16)])
+def test_few_rows_do_with_the_workspace_that_they_ask_for(dtype, dim, page, lens, kv_heads, group):
+    """17 to 32 rows of a sequence; nothing behind it is touched."""
+    step = LongStep(dtype, lens, page=page, kv_heads=kv_heads, dim=dim)
+    q = torch.randn(step.tokens, kv_heads * group, dim, generator=step.gen).to(step.x)
+    parents = torch.cat([torch.arange(-1, t - 1) for t, _ in lens]).int().cuda()
+    tree = sz.KVTree(step.batch)
+    sz.kv_tree(step.batch, parents, tree)
+    bufs = sz.KVAttentionBuffers(step.cache, step.batch, kv_heads * group)
+    bufs.ws = torch.full((bufs.ws_bytes + (1 << 22),), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q).cuda(), torch.empty(q.shape[:2], device="cuda")
+    scale = 0.3 / math.sqrt(dim)
+    for _ in range(2):
+        sz.kv_tree_attention(step.cache, step.batch, tree, q.cuda(), out, bufs, scale, lse=lse)
+        assert int(bufs.status[0]) == sz.OK
+        assert bool((bufs.ws[bufs.ws_bytes:] == 0xA5).all())
+        check_attention(step, out, lse, attention64(step, q, scale), BF16)

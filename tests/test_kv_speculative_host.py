@@ -201,3 +201,39 @@ def test_helpers_refuse_tensors_off_the_device(splitzip_lib):
         sz.KVTree(None, window=-1)
     with pytest.raises(ValueError):
         sz.KVTree(None, window=1 << 32)
+
+
+def size_of(heads=32, **kw):
+    need = ctypes.c_uint64(0)
+    cache = desc(sz.KVCacheDesc, CACHE, dict(kv_heads=kw.pop("kv_heads", 8), token_stride=8 * 128,
+                                             page_stride=16 * 8 * 128))
+    batch = desc(sz.KVBatchDesc, BATCH, dict(table_stride=1 << 20, **kw))
+    assert sz.splitzip_kv_attention_workspace_size(cache, batch, heads, need) == sz.OK
+    return need.value
+
+
+def test_workspace_of_steps_of_few_rows_is_the_step_kernels(splitzip_lib):
+    """Two parts of 16 rows for each of 608 blocks and their counters, up to 32 rows of a sequence."""
+    step = 2560 + 608 * 2 * 16 * (128 + 2) * 4
+    for t in (1, 4, 5, 8):
+        assert size_of(batch=64, tokens=64 * t, max_tokens=t, max_kv_len=2000) == step, t
+    assert size_of(batch=64, tokens=64 * 9, max_tokens=9, max_kv_len=2000) > step
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU error path")
+def test_trees_do_with_that_workspace(splitzip_lib):
+    """Whatever the sizes: the call is not refused for want of it, and is with a byte less."""
+    for kv_heads, group in ((1, 1), (1, 17), (2, 4), (8, 4), (3, 16)):
+        for t in (1, 3, 5, 8, 17, 32, 33, 100):
+            for n in (1, 2, 7, 64, 400):
+                for kv in (1, 65, 500, 1171, 8193, 100000):
+                    step = dict(batch=n, max_tokens=t, max_kv_len=kv)
+                    for tokens in {t, t * n}:
+                        heads = kv_heads * group
+                        need = size_of(heads, kv_heads=kv_heads, tokens=tokens, **step)
+                        rows = dict(token_stride=heads * 128)
+                        kw = dict(batch=dict(table_stride=1 << 20, tokens=tokens, **step), q_heads=heads, q=rows, out=rows,
+                                  tree=dict(words=-(-t // 32)),
+                                  cache=dict(kv_heads=kv_heads, token_stride=8 * 128, page_stride=16 * 8 * 128))
+                        assert attend(ws_bytes=need, **kw) in (sz.ERR_CUDA, sz.ERR_UNSUPPORTED)
+                        assert attend(ws_bytes=need - 1, **kw) == sz.ERR_CAPACITY
