@@ -39,7 +39,8 @@ constexpr uint64_t kStepRowsMax = 32;
 constexpr uint64_t kTreeStepRowsMax = 16;
 
 struct Plan {
-    uint32_t group, ctas, part_rows;
+    uint32_t group, ctas;
+    bool few;
     bool chunk;
     uint64_t plan_off, parts_off, ws_bytes;
 };
@@ -63,11 +64,11 @@ int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, bool tree, Pl
     const uint64_t tiles = std::min<uint64_t>((rows + 7) / 8 + b.batch, rows);
     p->ctas = step_ctas(tiles * c.kv_heads, b.max_kv_len);
     p->ws_bytes = lay_out(p, 0, p->ctas, step_part_floats(c.head_dim));
-    p->part_rows = kChunkRows;
+    p->few = false;
     if (!p->chunk) return SPLITZIP_OK;
     p->ctas = chunk_ctas(rows, b.batch, c.kv_heads, b.max_kv_len);
     const auto chunk_bytes = [&] {
-        return lay_out(p, chunk_plan_bytes(p->ctas), 0, uint64_t(p->part_rows) * (c.head_dim + 2));
+        return lay_out(p, chunk_plan_bytes(p->ctas), 0, uint64_t(p->few ? kFewRows : kChunkRows) * (c.head_dim + 2));
     };
     if (most > kStepRowsMax) {
         // a step of the same rows, but fewer of a sequence, takes the other kernel: the size
@@ -78,7 +79,8 @@ int plan_for(const KvCache& c, const KvBatch& b, uint32_t q_heads, bool tree, Pl
     // A tree of rows with which kv_attention takes the step kernel does with that one's size:
     // its parts have few rows, and their number follows what there is room for (all 152 CTAs
     // where the step kernel would have 306, which is so but for short contexts of few heads).
-    p->part_rows = uint32_t(kStepRowsMax);
+    static_assert(kFewRows == kStepRowsMax, "rows of a part");
+    p->few = true;
     while (p->ctas > 1 && chunk_bytes() > p->ws_bytes) --p->ctas;
     return chunk_bytes() <= p->ws_bytes ? SPLITZIP_OK : SPLITZIP_ERR_UNSUPPORTED;
 }
@@ -145,7 +147,7 @@ int attend(const splitzip_kv_cache_t* cache, const splitzip_kv_batch_t* batch, c
     a.window = std::min(window, 1u << 30);  // past every position
     a.counters = static_cast<uint32_t*>(d_ws);
     a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + p.parts_off);
-    a.part_rows = p.part_rows;
+    a.part_blocks = (p.few ? kFewRows : kChunkRows) / kFewRows;
     a.status = d_status;
     int sms;
     if ((st = device_sms(&sms)) != SPLITZIP_OK) return st;

@@ -38,7 +38,7 @@ struct AttentionArgs {
     uint32_t words;
     uint32_t* counters;  // workspace, one a CTA (step kernel)
     float* parts;        // workspace, two slots a CTA
-    uint32_t part_rows;  // rows that a slot has (chunk kernels of trees; kChunkRows for others)
+    uint32_t part_blocks;  // chunk kernels of trees: blocks of kFewRows rows of a part
     int* status;
 };
 
@@ -121,7 +121,7 @@ uint64_t step_part_floats(uint32_t head_dim);
 int launch_kv_step(const AttentionArgs& a, uint32_t ctas, cudaStream_t s);
 
 // kv_chunk.cuh, kv_chunk.cu
-constexpr uint32_t kChunkRows = 256;  // rows of a tile, and of a part
+constexpr uint32_t kChunkRows = 256, kFewRows = 32;  // rows that a part has room for
 uint32_t chunk_ctas(uint64_t rows, uint64_t batch, uint64_t kv_heads, uint64_t keys_max);
 uint64_t chunk_plan_bytes(uint32_t ctas);
 int launch_kv_chunk(const AttentionArgs& a, bool q_half, void* plan, uint32_t ctas, cudaStream_t s);

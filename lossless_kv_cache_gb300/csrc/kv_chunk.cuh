@@ -795,18 +795,21 @@ __device__ __noinline__ void note_special(const uint8_t* v, Seen seen, Reached<D
     }
 }
 
-// Where a CTA's part of an item that CTA `first` begins is, of tile g: columns
-// o[0] .. o[D - 1], reference, sum of kTileRows floats each (or of as many as a slot of fewer rows has).
-template <int D, bool TREE>
-__device__ __forceinline__ float* part_at(const AttentionArgs& a, uint32_t cta, uint32_t first, uint32_t g) {
-    return a.parts + (uint64_t(cta) * 2 + (cta == first ? 1 : 0)) * ((TREE ? a.part_rows : kRows) * (D + 2)) +
-           g * (kTileRows * (D + 2));
+// Where row `row` of a CTA's part of an item that CTA `first` begins is: columns
+// o[0] .. o[D - 1], reference, sum, part_stride() floats apart.  A part lies in
+// tiles of kTileRows rows, a tree's in a.part_blocks blocks of kFewRows, so that
+// trees of few rows do with one.
+template <bool TREE>
+__device__ __forceinline__ constexpr int part_stride() {
+    return TREE ? int(kFewRows) : kTileRows;
 }
 
-// From a column of a part to the next.
-template <bool TREE>
-__device__ __forceinline__ int part_stride(const AttentionArgs& a) {
-    return TREE ? int(min(a.part_rows, uint32_t(kTileRows))) : kTileRows;
+template <int D, bool TREE>
+__device__ __forceinline__ float* part_at(const AttentionArgs& a, uint32_t cta, uint32_t first, uint32_t row,
+                                          uint32_t blocks) {
+    constexpr uint32_t kStride = part_stride<TREE>();
+    const uint64_t slot = uint64_t(cta) * 2 + (cta == first ? 1 : 0);
+    return a.parts + (slot * blocks + row / kStride) * (kStride * (D + 2)) + row % kStride;
 }
 
 // The natural logarithm of a row's sum of exponentials l against reference m.
@@ -1115,20 +1118,20 @@ __device__ __forceinline__ void softmax_role(const AttentionArgs& a, typename Ch
             put(low, sum);
         } else {
             const bool live = int(row) + g * kTileRows < w.rows;
-            float* mine = part_at<D, TREE>(a, blockIdx.x, first, uint32_t(g)) + row;
-            const int stride = part_stride<TREE>(a);
+            constexpr int kStride = part_stride<TREE>();
+            float* mine = part_at<D, TREE>(a, blockIdx.x, first, row + uint32_t(g) * kTileRows, TREE ? a.part_blocks : 2);
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
                 float o[32];
                 sums32(k, o);
                 if (live) {
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) mine[(32 * k + y) * stride] = o[y];
+                    for (int y = 0; y < 32; ++y) mine[(32 * k + y) * kStride] = o[y];
                 }
             }
             if (live) {
-                mine[D * stride] = low;
-                mine[(D + 1) * stride] = sum;
+                mine[D * kStride] = low;
+                mine[(D + 1) * kStride] = sum;
             }
         }
         // the loads of O are done before the next piece's product overwrites it
@@ -1210,11 +1213,11 @@ __global__ void __launch_bounds__(Chunk<FMT, H, D>::kThreads, 1)
 // the one that wrote the last of them.
 constexpr int kJoinParts = 2, kJoinColumns = 8, kJoinThreads = kJoinParts * kJoinColumns * 32;
 
-template <bool H, int D, bool TREE>
+template <bool H, int D, bool TREE, int BLOCKS>
 __global__ void __launch_bounds__(kJoinThreads)
     kv_chunk_join_kernel(const __grid_constant__ AttentionArgs a, const ChunkSplit* splits, float value_scale,
                          float scale, float shift) {
-    constexpr int kColumns = D / kJoinColumns;
+    constexpr int kColumns = D / kJoinColumns, kStride = part_stride<TREE>();
     __shared__ float s_o[D][32], s_l[kJoinColumns][32];
     wait_predecessor();
     const uint32_t first = blockIdx.x, lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -1222,23 +1225,21 @@ __global__ void __launch_bounds__(kJoinThreads)
     const ChunkSplit w = splits[first];
     if (int(blockIdx.y) * 32 >= w.rows) return;
     const int row = int(blockIdx.y * 32u + lane);  // those past the last read what is there, and write nothing
-    const uint32_t g = uint32_t(row) / kTileRows, at = uint32_t(row) % kTileRows;
-    const int stride = part_stride<TREE>(a);
     float m = -INFINITY, l = 0.f;
 #pragma unroll 8
-    for (uint32_t cta = first; cta <= w.last_cta; ++cta) m = fmaxf(m, part_at<D, TREE>(a, cta, first, g)[D * stride + int(at)]);
+    for (uint32_t cta = first; cta <= w.last_cta; ++cta) m = fmaxf(m, part_at<D, TREE>(a, cta, first, uint32_t(row), BLOCKS)[D * kStride]);
     float o[kColumns];
 #pragma unroll
     for (int y = 0; y < kColumns; ++y) o[y] = 0.f;
 #pragma unroll 2
     for (uint32_t cta = first + uint32_t(part0); cta <= w.last_cta; cta += kJoinParts) {
-        const float* part = part_at<D, TREE>(a, cta, first, g) + at;
+        const float* part = part_at<D, TREE>(a, cta, first, uint32_t(row), BLOCKS);
         float x[kColumns];
 #pragma unroll
-        for (int y = 0; y < kColumns; ++y) x[y] = part[(col0 + y) * stride];
+        for (int y = 0; y < kColumns; ++y) x[y] = part[(col0 + y) * kStride];
         // parts of no reference (a scale of about zero leaves it there) count as they are
-        const float mc = part[D * stride], e = exp2_fast((mc - m) * scale), f = mc == m ? 1.f : e;
-        l += f * part[(D + 1) * stride];
+        const float mc = part[D * kStride], e = exp2_fast((mc - m) * scale), f = mc == m ? 1.f : e;
+        l += f * part[(D + 1) * kStride];
 #pragma unroll
         for (int y = 0; y < kColumns; ++y) o[y] += f * x[y];
     }
@@ -1269,6 +1270,21 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (a.lse && col0 == 0) a.lse[uint64_t(w.row0 + i) * a.q_heads + head] = log_sum(m, l, scale, shift);
 }
 
+// Of the kernel above on `ctas` CTAs, whose items have up to `rows` rows.
+template <bool H, int D, bool TREE>
+cudaError_t launch_join(const AttentionArgs& a, uint32_t ctas, int rows, const ChunkSplit* splits, float value_scale,
+                        float scale, float shift, cudaStream_t s) {
+    ChainedLaunch l(dim3(ctas, uint32_t(rows) / 32), dim3(kJoinThreads), 0, s);
+    if constexpr (TREE) {
+        if (a.part_blocks == 1) {
+            l.cfg.gridDim.y = 1;
+            return cudaLaunchKernelEx(&l.cfg, kv_chunk_join_kernel<H, D, true, 1>, a, splits, value_scale, scale, shift);
+        }
+    }
+    return cudaLaunchKernelEx(&l.cfg, kv_chunk_join_kernel<H, D, TREE, kRows / part_stride<TREE>()>, a, splits, value_scale,
+                              scale, shift);
+}
+
 uint64_t plan_bytes(uint32_t ctas) { return sizeof(ChunkPlan) + uint64_t(ctas) * sizeof(ChunkStart); }
 
 template <int FMT, bool H, int D, bool TREE>
@@ -1288,11 +1304,9 @@ int launch(const AttentionArgs& a, ChunkPlan* plan, const ChunkMaps& maps, uint3
     }
     ChainedLaunch l(dim3(ctas), dim3(C::kThreads), C::kSmem, s);
     ChunkSplit* splits = reinterpret_cast<ChunkSplit*>(reinterpret_cast<uint8_t*>(plan) + plan_bytes(ctas));
-    ChainedLaunch join(dim3(ctas, kRows / 32), dim3(kJoinThreads), 0, s);
     if (cudaLaunchKernelEx(&l.cfg, kv_chunk_kernel<FMT, H, D, TREE>, a, static_cast<const ChunkPlan*>(plan), splits, maps) !=
             cudaSuccess ||
-        cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<H, D, TREE>, a, static_cast<const ChunkSplit*>(splits),
-                           C::kValueScale, a.scale_log2, C::kShift) != cudaSuccess) {
+        launch_join<H, D, TREE>(a, ctas, kRows, splits, C::kValueScale, a.scale_log2, C::kShift, s) != cudaSuccess) {
         cudaGetLastError();
         return SPLITZIP_ERR_CUDA;
     }

@@ -858,8 +858,8 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
         const uint32_t first = w.first_cta, last = w.last_cta;
         const bool whole = first == last, live = int(row) < w.rows;
         const float inv = l == 0.f ? 0.f : 1.f / (l * (1 << C::kRoom));
-        float* part = part_at<D, true>(a, blockIdx.x, first, 0) + row;
-        const int stride = part_stride<true>(a);
+        constexpr int kStride = part_stride<true>();
+        float* part = part_at<D, true>(a, blockIdx.x, first, row, a.part_blocks);
         // an infinity or NaN stays one whatever the factor
         const auto times = [](float o, float f) { return fabsf(o) < INFINITY ? o * f : o; };
 #pragma unroll 1
@@ -889,12 +889,12 @@ __device__ __forceinline__ void tile_softmax_role(const AttentionArgs& a, typena
                 }
             } else if (live) {
 #pragma unroll
-                for (int y = 0; y < 16; ++y) part[(col + y) * stride] = o[y];
+                for (int y = 0; y < 16; ++y) part[(col + y) * kStride] = o[y];
             }
         }
         if (!whole && live && g == 0) {
-            part[D * stride] = m;
-            part[(D + 1) * stride] = l;
+            part[D * kStride] = m;
+            part[(D + 1) * kStride] = l;
         }
         if (whole) {
             ok = named_barrier_and(4, 256, ok);
@@ -1033,15 +1033,12 @@ int launch_tile(const AttentionArgs& a, ChunkPlan* plan_at, const ChunkMaps& map
     ChainedLaunch l(dim3(ctas), dim3(C::kThreads), C::kSmem, s);
     ChunkSplit* splits = reinterpret_cast<ChunkSplit*>(reinterpret_cast<uint8_t*>(plan_at) + plan_bytes(ctas));
     const ChunkPlan* plan = a.b.batch <= kPlanSequences ? nullptr : plan_at;
-    ChainedLaunch join(dim3(ctas, kTileRows / 32), dim3(kJoinThreads), 0, s);
     const bool out_half = C::kFp8 ? a.q_half != 0 : H;
     const float scale = C::kFp8 ? 1.f : a.scale_log2, value_scale = float(1 << C::kRoom), shift = C::kShift;
     cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv_tree_tile_kernel<FMT, H, D>, a, plan, splits, maps);
     if (e == cudaSuccess)
-        e = out_half ? cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<true, D, true>, a,
-                                          static_cast<const ChunkSplit*>(splits), value_scale, scale, shift)
-                     : cudaLaunchKernelEx(&join.cfg, kv_chunk_join_kernel<false, D, true>, a,
-                                          static_cast<const ChunkSplit*>(splits), value_scale, scale, shift);
+        e = out_half ? launch_join<true, D, true>(a, ctas, kTileRows, splits, value_scale, scale, shift, s)
+                     : launch_join<false, D, true>(a, ctas, kTileRows, splits, value_scale, scale, shift, s);
     if (e != cudaSuccess) cudaGetLastError();
     return e == cudaSuccess ? int(SPLITZIP_OK) : int(SPLITZIP_ERR_CUDA);
 }
