@@ -9,6 +9,7 @@ import torch
 
 import lossless_kv_cache_gb300 as sz
 from tests.kv_reference import Step, check_attention
+from tests.kv_reference import attention as causal_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -478,3 +479,21 @@ def test_results_in_the_queries_place(dtype, lens):
     out, lse, status, _ = run(step, parents, q, 0.1, tree=tree, out=q)
     assert status == sz.OK and out is q and torch.equal(lse, want_lse)
     assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("lens", [[(2, 200), (1, 9), (2, 65)], [(6, 500), (7, 300)], [(40, 300), (17, 17), (9, 128)],
+                                  [(80, 300), (3, 129)]], ids=["8", "28", "160", "320"])
+@pytest.mark.parametrize("dtype,x", TYPES)
+@pytest.mark.parametrize("window", [0, 50])
+def test_a_chain_sees_what_causal_attention_shows(dtype, x, lens, window):
+    """Both within their roundings of the causal formula, whichever kernels take them."""
+    step = Step(dtype, lens, x=x)
+    q = torch.randn(step.tokens, 8, step.dim, generator=step.gen).to(step.x)
+    ref = causal_attention(step, q, 0.09, True, window)
+    out, lse, status, _ = run(step, parents_of(step, "chain"), q, 0.09, window)
+    assert status == sz.OK
+    check_attention(step, out, lse, ref, weight_type(step))
+    bufs = sz.KVAttentionBuffers(step.cache, step.batch, 8)
+    sz.kv_attention(step.cache, step.batch, q.cuda(), out, bufs, 0.09, window=window, lse=lse)
+    assert int(bufs.status[0]) == sz.OK
+    check_attention(step, out, lse, ref, weight_type(step))
