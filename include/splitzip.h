@@ -462,6 +462,12 @@ typedef struct {
     uint32_t max_kv_len;          /* most tokens that a sequence holds, < 2^30 */
 } splitzip_kv_batch_t;
 
+/* The device arrays' entries may change within these maxima.  Kernels, launches
+ * and workspaces are chosen by the maxima alone, so a step of short sequences
+ * under a large max_kv_len may be slower than under its own (8 trees of 5
+ * tokens over 500: 13 us with max_kv_len 500, 21 with 32,768; splitzip_kv_attention
+ * of so few rows takes the same time). */
+
 /* Packed rows [row][head][head_dim]: element (row, head, i) is at
  * row * token_stride + head * head_stride + i (elements; multiples of 8, so a
  * slice of a fused projection's output needs no copy).  Base 16-byte aligned. */
@@ -544,7 +550,8 @@ int splitzip_kv_attention(const splitzip_kv_cache_t* cache, const splitzip_kv_ba
 /* The pages of one pool and the sequences that hold them: device arrays of
  * int32, 4-byte aligned.  Sequence b holds held[b] pages, entries 0 ..
  * held[b] - 1 of its row of the page table; the free pages are entries 0 ..
- * free_count[0] - 1 of the list d_free, the next one to be taken last. */
+ * free_count[0] - 1 of the list d_free, the next one to be taken last.  A page
+ * is free or one sequence's: one that two rows held would go on the list twice. */
 typedef struct {
     int32_t* d_free;           /* pool_pages entries */
     const int32_t* d_free_count;

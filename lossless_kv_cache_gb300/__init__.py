@@ -767,7 +767,8 @@ class KVBatch:
     int32 device tensors cu_tokens (batch + 1), kv_len (batch) and page_table
     (batch, at least the pages of max_kv_len tokens); the packed tensors' row
     count; the most new tokens and the most tokens of a sequence.  The device
-    tensors may be updated in place between steps within those maxima."""
+    tensors may be updated in place between steps within those maxima, by which
+    alone kernels and workspaces are chosen."""
 
     def __init__(self, cu_tokens, kv_len, page_table, tokens, max_tokens, max_kv_len):
         torch = _torch()
@@ -1011,7 +1012,11 @@ def rotary_frequencies(rotary_dim, base=10000.0, factor=1.0, original_len=0, tur
     rotary_dim).  factor: how far the context is stretched.  Without original_len
     every pair is slowed by it; with it, pairs that make at most turns[0] turns
     over the original length are, those of turns[1] and more stay as they are, and
-    a part of the way between the two is taken in proportion."""
+    those between are in proportion to their turns: the published interpolation
+    "by parts" with (1, 32), and the one of models that state a low and a high
+    factor of (1, 4).  Implementations that ramp over the number of the pair,
+    between limits rounded to whole pairs, have other frequencies between the two:
+    give those to KVRotary as they are."""
     torch = _torch()
     j = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
     f = torch.tensor([float(base) ** (-x / rotary_dim) for x in j.tolist()], dtype=torch.float64)

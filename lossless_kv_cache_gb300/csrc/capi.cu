@@ -207,8 +207,11 @@ bool splitzip::make_rows_map(void* base, uint32_t rank, const uint64_t* dims, co
         ones[i] = 1;
         if (i + 1 < rank) st[i] = strides[i];
     }
-    // no more than the rows that are read one after another: 256 bytes of promotion had the
-    // caches of 128-byte rows read half as much again from memory, the next head's
+    // No more than the rows that are read one after another: 256 bytes of promotion had the
+    // caches of 128-byte rows read half as much again from memory, the next head's (trees over
+    // E5M2).  kv_attention's chunks over BF16 heads of 64 take the same time with 128 and 256
+    // bytes, in either order of heads and tokens (8 x 64 tokens over 8,192 62.2 and 62.4 us for
+    // [token][head], 62.6 and 62.5 for [head][token]; 2,048 over 32,768 590 and 586, 590 and 585).
     const uint64_t row = dims[0] * (bytes ? 1 : 2);
     const CUtensorMapL2promotion promotion = row >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                              : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B

@@ -7,10 +7,15 @@
 // overwritten before it is read.  One warp does all tokens of a sequence for
 // its heads, so the order is its own and nobody else's.
 //
-// What bounds it: the latency of path, table and rows, and then HBM, for a step
-// keeps a few tokens a sequence and the layers are moved together: 64 sequences
-// of 16 drafted tokens, 32 layers, 8 heads of 128, take 8.1 us over E5M2 (5.6 TB/s),
-// 12.9 over BF16; 2 sequences of 7, one layer, 3.8, which is two launches.
+// What bounds it: latency.  A warp's tokens come eight at a time, a group is a
+// chain of path, table, row and store, and a step keeps a few tokens a sequence.
+// In a graph, 64 sequences of 16 drafted tokens, 32 layers, 8 heads of 128, bytes
+// of the tokens that move (those in their place already are skipped) read and
+// written once:
+//   125 of 342 kept tokens move    E5M2  8.2 us (2.0 TB/s)    BF16 15.4 (2.1)
+//   194 of 258                          10.5 (2.4)                16.2 (3.1)
+//   all of 512, every other one         15.8 (4.3)                26.7 (5.0)
+// 2 sequences of 7, one layer, take 3.8, which is two launches.
 #include <algorithm>
 #include <cstring>
 
