@@ -497,3 +497,17 @@ def test_a_chain_sees_what_causal_attention_shows(dtype, x, lens, window):
     sz.kv_attention(step.cache, step.batch, q.cuda(), out, bufs, 0.09, window=window, lse=lse)
     assert int(bufs.status[0]) == sz.OK
     check_attention(step, out, lse, ref, weight_type(step))
+
+
+@pytest.mark.parametrize("lens", [FEW, [(7, 300), (1, 40), (5, 130)], TILE], ids=["few", "28", "tile"])
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+@pytest.mark.parametrize("max_tokens", [0, 7, 30, 100])
+def test_maxima_far_above_the_steps_own(dtype, lens, max_tokens):
+    """What a captured step has: kernels are chosen by maxima that its sequences do not come near."""
+    step = Step(dtype, lens)
+    table = torch.full((len(lens), 2048), -7, dtype=torch.int32, device="cuda")
+    table[:, : step.table.shape[1]] = step.batch.page_table
+    most = max(step.max_new, min(max_tokens, step.tokens))
+    step.batch = sz.KVBatch(step.batch.cu_tokens, step.batch.kv_len, table, step.tokens, most, 32768)
+    for window in (0, 60):
+        check(step, window=window)
